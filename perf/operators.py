@@ -133,8 +133,8 @@ def _quantise(x):
     """Blocks of 32 along the last dimension: (codes uint8, scales fp16).  d is minus an eighth of
     the value of largest magnitude (the lowest dimension on ties), rounded to eight significant
     bits; c = x / d + 8 rounded half up, in 0..15.  What is not a number counts as 0, and
-    magnitudes end at 65504."""
-    b = torch.nan_to_num(x, nan=0.0, posinf=65504.0, neginf=-65504.0).clamp(-65504.0, 65504.0)
+    magnitudes end at 65280 (where -8 d still fits fp16)."""
+    b = torch.nan_to_num(x, nan=0.0, posinf=65280.0, neginf=-65280.0).clamp(-65280.0, 65280.0)
     b = b.reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
     mag = b.abs()
     at = torch.arange(32, device=x.device)
