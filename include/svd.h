@@ -62,6 +62,16 @@ enum {
     SVD_ST_EMPTY = 16         /* the distribution drawn from had zero mass: no token  */
 };
 
+/* Status bits of the paged cache's calls, per request (svd_paged_tables) or token
+ * (svd_paged_append); 0 = clean. */
+enum {
+    SVD_ST_BAD_REQUEST = 32, /* lengths that contradict each other, or more pages than a row has */
+    SVD_ST_NO_PAGES = 64,    /* the free pages do not suffice: nothing granted                  */
+    SVD_ST_NO_TOKENS = 128,  /* the call's token slots do not suffice: nothing granted          */
+    SVD_ST_NONFINITE = 256,  /* a key or value was NaN or infinite; stored as 0 or the largest  */
+    SVD_ST_BAD_SLOT = 512    /* a slot beyond the pool: the token was not stored                */
+};
+
 /* Weight layouts. */
 enum {
     SVD_LAYOUT_CANONICAL = 0, /* codes[out][in/2] bytes, input 2t in the low nibble,
@@ -407,6 +417,96 @@ int svd_kv_attention_append(const uint16_t *q, const float *k, const float *v, i
 int svd_kv_attention(const uint16_t *q, const void *cache, int capacity, int n_q_heads,
                      int n_kv_heads, int n_past, int C, float scale, float *out, void *workspace,
                      size_t workspace_bytes, svd_stream_t stream);
+
+/* ---- paged cache held in 4 bits -------------------------------------------------------------- */
+/* Several requests' windows in one pass ("100 tokens per second ...", "Why a hiring company is
+ * writing this"), each with its own cache length, over a cache of 4.5 bits per value ("Decode is
+ * memory-bound ...", "The ceiling": 4.4 GB at 262K against 17 GB in fp16).
+ *
+ * The pool of one layer is n_pages pages of page_size positions (a multiple of 16 up to
+ * SVD_PAGED_PAGE_MAX) of every kv head, [page][kv head][page_size / 16] units of 16 positions and
+ * SVD_PAGED_UNIT_BYTES: K codes [4 blocks of 32 dimensions][16 positions][16 bytes] (dimensions 2b
+ * and 2b + 1 of the block in the low and high nibble of byte b); V codes [64][16 bytes] (row d:
+ * dimension d in the low, d + 64 in the high nibbles; position 4k + j at byte 4k + (0, 2, 1, 3)[j]);
+ * K scales fp16 [16 positions][4 blocks]; V scales fp16 [4 blocks][16 positions].  Code c stands
+ * for d (c - 8).  Scales have eight significant bits, so that every value is exact in fp16.
+ * Position p of request r lies at slot table[r][p / page_size] * page_size + p % page_size.
+ *
+ * svd_paged_tables: block tables and slot maps from request lengths, on the GPU, in one launch.
+ *   held [R]: positions in the cache; window, emitted [R] (both NULL: zeros): the last window's
+ *   tokens and how many of them stay (svd_accept's n_emitted), so keep = held - window + emitted;
+ *   n_new [R]: tokens to add.  Row r of table [R][max_pages] holds ceil(held / page_size) page ids.
+ *   Pages no longer needed for keep + n_new positions go onto the stack of free pages (free_ids
+ *   [n_pages], its first *n_free entries, the last one on top); then missing pages are taken from
+ *   the top; both in request order, then page order.  Outputs: the new table (-1 past a row's
+ *   pages), stack (-1 past its end) and count; kv_len [R] = keep + n_new; q_start [R + 1], the first
+ *   of each request's tokens and their total; slots and positions [max_tokens] of the new tokens
+ *   (-1 past the total); status [R].  A request that cannot be served is given nothing and keeps
+ *   its pages: SVD_ST_BAD_REQUEST for window or emitted out of order (0 <= emitted <= window <= held),
+ *   n_new < 0 or a row too short (kv_len 0, row copied); SVD_ST_NO_TOKENS when the tokens asked for up to
+ *   and including it exceed max_tokens; SVD_ST_NO_PAGES when the pages asked for do (kv_len = keep,
+ *   the row as held).  After a request with status, pass its old held again.
+ *   Outputs must not be the inputs.  R <= SVD_PAGED_MAX_REQUESTS; max_pages * page_size and
+ *   R * max_pages < 2^31; n_pages, max_tokens <= 2^30.
+ * svd_paged_append: for every token t the row qkv[t * ld ..] holds Hq query, Hkv key and Hkv value
+ *   heads of 128 (fp32 or bf16; 16-byte aligned, ld a multiple of 4).  Queries and keys are rotated:
+ *   pair i of dimensions, (i, i + n_pairs) or, interleaved, (2i, 2i + 1), turns by
+ *   positions[axis[i] * positions_ld + t] * inv_freq[i] radians (axes: time, height and width of
+ *   an image token, or one); dimensions past 2 n_pairs stay; rope NULL rotates nothing.  Queries go
+ *   to q, bf16 [T][Hq][128]; keys and values are stored at slots[t] (negative: not stored).  Per
+ *   block of 32: m = the value of largest magnitude (the lowest dimension on ties), d = m / -8
+ *   rounded to eight significant bits, then to fp16, c = floor(x / d + 8.5) limited to 0..15 (8 when
+ *   d = 0); decided as in exact arithmetic, also next to a border.  NaN counts as 0 and magnitudes
+ *   end at 65280; status (NULL, or int32 [T] that the call ORs into) has SVD_ST_NONFINITE and
+ *   SVD_ST_BAD_SLOT.  Slots of one call must differ.
+ * svd_paged_read: the values that the pool holds at slots[t], fp32 [T][Hkv][128] each (0 for a slot
+ *   outside the pool).
+ * svd_paged_attention: request r has the tokens q_start[r] .. q_start[r + 1] - 1 of q, bf16
+ *   [T][Hq][128], the last of them at position kv_len[r] - 1.  A token at position p, query head h
+ *   (kv head h / (Hq / Hkv)): out[t][h] = sum_{j <= p} softmax_j(scale <q, k_j>) v_j, as bf16 or
+ *   fp32 (out_dtype); a token that sees no position gets zeros.  Tokens from q_start[R] on are not
+ *   written.  max_new bounds the tokens of a request (later ones are not written).  Positions whose
+ *   page id lies outside the pool take no part; bytes of positions from kv_len on are never read
+ *   into the result.  Queries are used as fp16: exact for bf16 of magnitude in [2^-14, 65504] and 0,
+ *   rounded outside.  The scales of positions before kv_len must be finite (svd_paged_append
+ *   writes no others).
+ * Errors: SVD_ERR_INVALID_ARG for null or misaligned (16 bytes) pointers, sizes out of range, Hq %
+ * Hkv != 0; SVD_ERR_WORKSPACE for a short workspace.  The workspace is zero-filled before its first
+ * use and serves any number of calls in stream order; its first word gets bit 0 set if a bounded wait
+ * of the kernel gave up (the output is then undefined). */
+#define SVD_PAGED_UNIT_BYTES 2304
+#define SVD_PAGED_PAGE_MAX 256
+#define SVD_PAGED_MAX_REQUESTS 4096
+#define SVD_ROPE_MAX_PAIRS 64
+#define SVD_ROPE_MAX_AXES 4
+enum { SVD_F32 = 0, SVD_BF16 = 1 };
+typedef struct svd_rope { /* host memory, copied by the call */
+    double inv_freq[SVD_ROPE_MAX_PAIRS]; /* radians per position, |inv_freq| < 2^32 */
+    uint8_t axis[SVD_ROPE_MAX_PAIRS];    /* < n_axes */
+    int32_t n_pairs;                     /* a multiple of 4, 4..64 */
+    int32_t n_axes;                      /* 1..SVD_ROPE_MAX_AXES */
+    int32_t interleaved;
+} svd_rope;
+size_t svd_paged_cache_bytes(int n_kv_heads, int page_size, int64_t n_pages);
+int svd_paged_tables(const int32_t *held, const int32_t *window, const int32_t *emitted,
+                     const int32_t *n_new, int n_requests, int page_size, const int32_t *table,
+                     int max_pages, const int32_t *free_ids, const int32_t *n_free, int64_t n_pages,
+                     int32_t *table_out, int32_t *free_out, int32_t *n_free_out, int32_t *kv_len,
+                     int32_t *q_start, int64_t *slots, int32_t *positions, int64_t max_tokens,
+                     int32_t *status, svd_stream_t stream);
+int svd_paged_append(const void *qkv, int dtype, int64_t ld, int n_tokens, int n_q_heads,
+                     int n_kv_heads, const svd_rope *rope, const int32_t *positions,
+                     int64_t positions_ld, const int64_t *slots, void *pages, int page_size,
+                     int64_t n_pages, uint16_t *q, int32_t *status, svd_stream_t stream);
+int svd_paged_read(const int64_t *slots, int n_tokens, int n_kv_heads, const void *pages,
+                   int page_size, int64_t n_pages, float *k, float *v, svd_stream_t stream);
+size_t svd_paged_attention_workspace_bytes(int n_q_heads, int n_kv_heads, int n_requests,
+                                           int max_new);
+int svd_paged_attention(const uint16_t *q, int n_tokens, const int32_t *kv_len,
+                        const int32_t *q_start, int n_requests, int max_new, const int32_t *table,
+                        int max_pages, const void *pages, int page_size, int64_t n_pages,
+                        int n_q_heads, int n_kv_heads, float scale, void *out, int out_dtype,
+                        void *workspace, size_t workspace_bytes, svd_stream_t stream);
 
 /* ---- host-side companions: depth policy and n-gram drafter ----------------------------- */
 /* No GPU work; safe to call from any host thread (a handle is not shared between threads

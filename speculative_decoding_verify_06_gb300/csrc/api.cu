@@ -32,6 +32,22 @@ int accept(const float *p, const int64_t *p_rows, const float *q, const int64_t 
            uint64_t seed, uint64_t woff, const float *uniforms, int32_t *out_tokens,
            int32_t *n_emitted, int32_t *status, cudaStream_t stream);
 
+int paged_tables(const int32_t *held, const int32_t *window, const int32_t *emitted, const int32_t *n_new,
+                 int R, int page, const int32_t *table, int width, const int32_t *free_ids,
+                 const int32_t *n_free, int64_t n_pages, int32_t *table_out, int32_t *free_out,
+                 int32_t *n_free_out, int32_t *kv_len, int32_t *q_start, int64_t *slots,
+                 int32_t *positions, int64_t tokens, int32_t *status, cudaStream_t stream);
+int paged_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv, const svd_rope *rope,
+                 const int32_t *positions, int64_t positions_ld, const int64_t *slots, void *pages,
+                 int page, int64_t n_pages, void *q, int32_t *status, cudaStream_t stream);
+int paged_read(const int64_t *slots, int T, int Hkv, const void *pages, int page, int64_t n_pages, float *k,
+               float *v, cudaStream_t stream);
+size_t paged_attention_ws_bytes(int Hq, int Hkv, int R, int max_new);
+int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,
+                    int max_new, const int32_t *table, int width, const void *pages, int page,
+                    int64_t n_pages, int Hq, int Hkv, float scale, void *out, int out_dtype, void *ws,
+                    size_t ws_bytes, cudaStream_t stream);
+
 static thread_local int g_last_cuda_error = 0;
 void set_cuda_error(cudaError_t e) { g_last_cuda_error = (int)e; }
 
@@ -171,6 +187,48 @@ int svd_accept(const float *p, const int64_t *p_rows, const float *q, const int6
                int32_t *n_emitted, int32_t *status, svd_stream_t stream) {
     return svd::accept(p, p_rows, q, q_rows, target_argmax, draft, n, k, V, seed, woff, uniforms,
                        out_tokens, n_emitted, status, (cudaStream_t)stream);
+}
+
+size_t svd_paged_cache_bytes(int n_kv_heads, int page_size, int64_t n_pages) {
+    if (n_kv_heads < 1 || n_kv_heads > 1024 || page_size < 16 || page_size > SVD_PAGED_PAGE_MAX ||
+        page_size % 16 || n_pages < 1 || n_pages > (int64_t)1 << 30)
+        return 0;
+    return (size_t)n_pages * n_kv_heads * (page_size / 16) * SVD_PAGED_UNIT_BYTES;
+}
+
+int svd_paged_tables(const int32_t *held, const int32_t *window, const int32_t *emitted,
+                     const int32_t *n_new, int R, int page, const int32_t *table, int width,
+                     const int32_t *free_ids, const int32_t *n_free, int64_t n_pages, int32_t *table_out,
+                     int32_t *free_out, int32_t *n_free_out, int32_t *kv_len, int32_t *q_start,
+                     int64_t *slots, int32_t *positions, int64_t tokens, int32_t *status,
+                     svd_stream_t stream) {
+    return svd::paged_tables(held, window, emitted, n_new, R, page, table, width, free_ids, n_free, n_pages,
+                             table_out, free_out, n_free_out, kv_len, q_start, slots, positions, tokens,
+                             status, (cudaStream_t)stream);
+}
+
+int svd_paged_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv, const svd_rope *rope,
+                     const int32_t *positions, int64_t positions_ld, const int64_t *slots, void *pages,
+                     int page, int64_t n_pages, uint16_t *q, int32_t *status, svd_stream_t stream) {
+    return svd::paged_append(qkv, dtype, ld, T, Hq, Hkv, rope, positions, positions_ld, slots, pages, page,
+                             n_pages, q, status, (cudaStream_t)stream);
+}
+
+int svd_paged_read(const int64_t *slots, int T, int Hkv, const void *pages, int page, int64_t n_pages,
+                   float *k, float *v, svd_stream_t stream) {
+    return svd::paged_read(slots, T, Hkv, pages, page, n_pages, k, v, (cudaStream_t)stream);
+}
+
+size_t svd_paged_attention_workspace_bytes(int Hq, int Hkv, int R, int max_new) {
+    return svd::paged_attention_ws_bytes(Hq, Hkv, R, max_new);
+}
+
+int svd_paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,
+                        int max_new, const int32_t *table, int width, const void *pages, int page,
+                        int64_t n_pages, int Hq, int Hkv, float scale, void *out, int out_dtype, void *ws,
+                        size_t ws_bytes, svd_stream_t stream) {
+    return svd::paged_attention(q, T, kv_len, q_start, R, max_new, table, width, pages, page, n_pages, Hq,
+                                Hkv, scale, out, out_dtype, ws, ws_bytes, (cudaStream_t)stream);
 }
 
 int svd_graph_begin(svd_stream_t stream) {

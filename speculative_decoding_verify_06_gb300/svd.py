@@ -40,6 +40,19 @@ SVD_KV_HEAD_DIM = 128
 SVD_KV_UNIT_POSITIONS = 16
 SVD_KV_UNIT_BYTES = 3328
 
+SVD_ST_BAD_REQUEST = 32
+SVD_ST_NO_PAGES = 64
+SVD_ST_NO_TOKENS = 128
+SVD_ST_NONFINITE = 256
+SVD_ST_BAD_SLOT = 512
+SVD_F32 = 0
+SVD_BF16 = 1
+SVD_PAGED_UNIT_BYTES = 2304
+SVD_PAGED_PAGE_MAX = 256
+SVD_PAGED_MAX_REQUESTS = 4096
+SVD_ROPE_MAX_PAIRS = 64
+SVD_ROPE_MAX_AXES = 4
+
 # Every symbol include/svd.h declares (checked by the CPU test suite).
 EXPORTS = (
     "svd_error_string", "svd_last_cuda_error", "svd_native_sizes", "svd_q4k_native_sizes",
@@ -56,6 +69,8 @@ EXPORTS = (
     "svd_ngram_length", "svd_ngram_destroy",
     "svd_kv_cache_bytes", "svd_kv_repack", "svd_kv_unpack", "svd_kv_append",
     "svd_kv_attention_workspace_bytes", "svd_kv_attention", "svd_kv_attention_append",
+    "svd_paged_cache_bytes", "svd_paged_tables", "svd_paged_append", "svd_paged_read",
+    "svd_paged_attention_workspace_bytes", "svd_paged_attention",
 )
 
 
@@ -93,6 +108,28 @@ class QWeight:
 
 class _LinearOp(ctypes.Structure):
     _fields_ = [("W", _QWeight), ("X", ctypes.c_void_p), ("Y", ctypes.c_void_p)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_double * SVD_ROPE_MAX_PAIRS),
+                ("axis", ctypes.c_uint8 * SVD_ROPE_MAX_PAIRS), ("n_pairs", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class Rope:
+    """Rotary positions: radians per position and the axis of every pair of dimensions (host
+    sequences), and how pairs are formed: (i, i + n_pairs), or interleaved (2i, 2i + 1)."""
+
+    def __init__(self, inv_freq, axis=None, n_axes: int = 1, interleaved: bool = False):
+        inv = [float(f) for f in inv_freq]
+        axis = [0] * len(inv) if axis is None else [int(a) for a in axis]
+        if len(inv) > SVD_ROPE_MAX_PAIRS or len(axis) != len(inv) or any(not 0 <= a < 256 for a in axis):
+            raise ValueError(f"at most {SVD_ROPE_MAX_PAIRS} pairs, one axis for each")
+        self._s = _Rope()
+        self._s.inv_freq[:len(inv)] = inv
+        self._s.axis[:len(inv)] = axis
+        self._s.n_pairs, self._s.n_axes, self._s.interleaved = len(inv), int(n_axes), int(bool(interleaved))
+        self._p = ctypes.addressof(self._s)
 
 
 class Sampler:
@@ -165,6 +202,15 @@ def load(path: str = LIB_PATH):
                                               ctypes.c_float, P, P, sz, P]),
             "svd_kv_attention": (i32, [P, P, i32, i32, i32, i32, i32, ctypes.c_float, P, P, sz,
                                        P]),
+            "svd_paged_cache_bytes": (sz, [i32, i32, i64]),
+            "svd_paged_tables": (i32, [P, P, P, P, i32, i32, P, i32, P, P, i64, P, P, P, P, P, P, P,
+                                       i64, P, P]),
+            "svd_paged_append": (i32, [P, i32, i64, i32, i32, i32, P, P, i64, P, P, i32, i64, P, P,
+                                       P]),
+            "svd_paged_read": (i32, [P, i32, i32, P, i32, i64, P, P, P]),
+            "svd_paged_attention_workspace_bytes": (sz, [i32, i32, i32, i32]),
+            "svd_paged_attention": (i32, [P, i32, P, P, i32, i32, P, i32, P, i32, i64, i32, i32,
+                                          ctypes.c_float, P, i32, P, sz, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -509,3 +555,51 @@ def svd_kv_attention_append(q, k, v, ld: int, cache, capacity: int, n_q_heads: i
         _ptr(q), _ptr(k), _ptr(v), int(ld), _ptr(cache), int(capacity), int(n_q_heads),
         int(n_kv_heads), int(n_past), int(C), float(scale), _ptr(out), _ptr(workspace),
         int(workspace_bytes), _stream(stream)))
+
+
+def svd_paged_cache_bytes(n_kv_heads: int, page_size: int, n_pages: int) -> int:
+    return int(load().svd_paged_cache_bytes(int(n_kv_heads), int(page_size), int(n_pages)))
+
+
+def svd_paged_tables(held, window, emitted, n_new, n_requests: int, page_size: int, table,
+                     max_pages: int, free_ids, n_free, n_pages: int, table_out, free_out, n_free_out,
+                     kv_len, q_start, slots, positions, max_tokens: int, status, stream=None):
+    _check("svd_paged_tables", load().svd_paged_tables(
+        _ptr(held), _ptr(window), _ptr(emitted), _ptr(n_new), n_requests, page_size, _ptr(table),
+        max_pages, _ptr(free_ids), _ptr(n_free), n_pages, _ptr(table_out), _ptr(free_out),
+        _ptr(n_free_out), _ptr(kv_len), _ptr(q_start), _ptr(slots), _ptr(positions), max_tokens,
+        _ptr(status), _stream(stream)))
+
+
+def svd_paged_append(qkv, ld: int, n_tokens: int, n_q_heads: int, n_kv_heads: int, slots, pages,
+                     page_size: int, n_pages: int, q, rope: Rope | None = None, positions=None,
+                     positions_ld: int = 0, dtype: int = SVD_F32, status=None, stream=None):
+    _check("svd_paged_append", load().svd_paged_append(
+        _ptr(qkv), dtype, ld, n_tokens, n_q_heads, n_kv_heads, None if rope is None else rope._p,
+        _ptr(positions), positions_ld, _ptr(slots), _ptr(pages), page_size, n_pages, _ptr(q),
+        _ptr(status), _stream(stream)))
+
+
+def svd_paged_read(slots, n_tokens: int, n_kv_heads: int, pages, page_size: int, n_pages: int, k, v,
+                   stream=None):
+    _check("svd_paged_read", load().svd_paged_read(
+        _ptr(slots), n_tokens, n_kv_heads, _ptr(pages), page_size, n_pages, _ptr(k), _ptr(v),
+        _stream(stream)))
+
+
+def svd_paged_attention_workspace_bytes(n_q_heads: int, n_kv_heads: int, n_requests: int,
+                                        max_new: int) -> int:
+    return int(load().svd_paged_attention_workspace_bytes(
+        int(n_q_heads), int(n_kv_heads), int(n_requests), int(max_new)))
+
+
+def svd_paged_attention(q, n_tokens: int, kv_len, q_start, n_requests: int, max_new: int, table,
+                        max_pages: int, pages, page_size: int, n_pages: int, n_q_heads: int,
+                        n_kv_heads: int, scale: float, out, out_dtype: int, workspace,
+                        workspace_bytes: int = 0, stream=None):
+    if not workspace_bytes and workspace is not None and not isinstance(workspace, int):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("svd_paged_attention", load().svd_paged_attention(
+        _ptr(q), n_tokens, _ptr(kv_len), _ptr(q_start), n_requests, max_new, _ptr(table), max_pages,
+        _ptr(pages), page_size, n_pages, n_q_heads, n_kv_heads, scale, _ptr(out), out_dtype,
+        _ptr(workspace), workspace_bytes, _stream(stream)))
