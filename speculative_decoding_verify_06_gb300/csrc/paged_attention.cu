@@ -3,103 +3,823 @@
 // "Decode is memory-bound ..." ("The ceiling"): at long context the cache joins the weights on
 // every pass; "100 tokens per second ..." ("Why a hiring company is writing this"): several
 // sequences share the pass.
+//
+//   o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c <q, k_j> - ref),   c = scale log2(e)
+//
+// Work.  Query rows of one request and kv head (token-major, then head in the group) form row tiles
+// of up to RP rows; a row tile reads the cache positions its last token sees in tiles of 128.  All
+// tiles, ordered by request, kv head, row tile and position, are split into equal contiguous
+// ranges, one per CTA, so that ragged lengths balance without the host knowing them.  The part of a
+// range within one row tile is a segment.  A segment that is a whole row tile writes the output;
+// others leave (sums, reference, unnormalised o) in the workspace, at most two per CTA, and a
+// second kernel joins them.
+//
+// One tile.  Bulk copies bring up to eight units into a ring stage.  Four warps turn K into fp16 in
+// tensor memory (lane = position) and four others V (lane = dimension, two positions per column):
+// every d (c - 8) is exact in fp16.  S^T = K Q^T (M = 128 positions, N = query rows) and
+// O^T += V^T P^T (M = 128 dimensions) run on tcgen05 with A in tensor memory and fp32 accumulators;
+// the K warps turn S into P, with the next tile's K written before that, so the next S runs
+// meanwhile.  A lane holds one position of S for all rows, so the softmax needs no lane exchange:
+// the reference of a row changes only when a score exceeds it by 15 (p <= 2^15 in between), checked
+// by one vote of the four warps, and starts 7 below the first tile's maximum.  p keeps fp16's eleven
+// bits from 2^22 down below the maximum and loses them gradually to 2^31 below.  For fp32 outputs P
+// is split into two fp16 parts (relative 2^-22) and V^T P^T runs over both.
+//
+// Rows a mask leaves empty get zeros.  Positions past the length, or on a page outside the pool,
+// are cut out of S, and their V scales are replaced by 0, whatever their bytes.
 #include "paged.cuh"
 
 namespace svd {
 
-// One CTA per (token, query head), four warps over the positions in chunks of 32: a lane scores one
-// position, then owns four dimensions of the weighted sum; the warps merge at the end.
+constexpr int kPaTile = 128;
+constexpr int kPaTileUnits = kPaTile / kPgUnitPos;
+constexpr int kPaStageBytes = kPaTileUnits * kPgUnitBytes;
+constexpr int kPaMaxStages = 4;
+constexpr int kPaRing = 8;           // tile and segment descriptors in flight (see producer)
+constexpr int kPaThreads = 320;      // K/softmax 4 warps, V 4 warps, copies, MMA
+constexpr float kPaOver = 15.f;      // a score this far above the reference moves it ...
+constexpr float kPaUnder = 7.f;      // ... to this far below the new maximum
+constexpr int kPaHeader = 256;       // workspace: status word, tile count, then the prefix sums
+
 struct PaArgs {
     const __nv_bfloat16 *q;
     const int32_t *kv_len, *q_start, *table;
     const uint8_t *pages;
     void *out;
+    uint32_t *status;
+    int32_t *prefix;  // [R + 1] tiles before each request
+    float *part;      // [2 CTAs][RP][128]
+    float2 *part_ml;  // [2 CTAs][RP] (reference, sum)
     int64_t n_pages;
-    int T, R, max_new, width, page, Hq, Hkv, out_bf16;
-    float scale;
+    int T, R, max_new, width, page, Hq, Hkv, G, stages;
+    float c;          // scale * log2(e) * 8 (the K operand is K / 8)
 };
 
-__global__ void __launch_bounds__(128) paged_attention_plain_kernel(const PaArgs A) {
-    __shared__ float s_q[kPgDim], s_o[4][kPgDim], s_m[4], s_l[4];
-    const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    griddep_wait();
-    if (t >= A.q_start[A.R]) return;
-    int lo = 0, hi = A.R;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (A.q_start[mid] <= t) lo = mid; else hi = mid;
-    }
-    const int r = lo, n = A.q_start[r + 1] - A.q_start[r], i = t - A.q_start[r];
-    if (i < 0 || i >= n || i >= A.max_new) return;
-    const int len = min(max(A.kv_len[r], 0), A.width * A.page);
-    const int seen = len - n + i + 1;  // positions this token sees
-    s_q[tid] = __bfloat162float(A.q[((int64_t)t * A.Hq + h) * kPgDim + tid]) * A.scale;
-    __syncthreads();
-    const int g = h / (A.Hq / A.Hkv);
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int base = warp * 32; base < seen; base += 128) {
-        const int p = base + lane;
-        float s = -INFINITY;
-        int64_t unit_off = -1;
-        if (p < seen) {
-            const int pg = A.table[(int64_t)r * A.width + p / A.page];
-            if (pg >= 0 && pg < A.n_pages)
-                unit_off = (((int64_t)pg * A.Hkv + g) * (A.page >> 4) + ((p % A.page) >> 4)) * kPgUnitBytes;
-        }
-        if (unit_off >= 0) {
-            const uint8_t *u = A.pages + unit_off;
-            s = 0.f;
-            for (int b = 0; b < 4; ++b) {
-                float x = 0.f;
-                for (int j = 0; j < 16; ++j) {
-                    const int c = u[b * 256 + (p & 15) * 16 + j];
-                    x += s_q[32 * b + 2 * j] * ((c & 15) - 8) + s_q[32 * b + 2 * j + 1] * ((c >> 4) - 8);
-                }
-                s += x * __half2float(*reinterpret_cast<const __half *>(u + kPgKScales + (p & 15) * 8 + 2 * b));
-            }
-        }
-        float mx = s;
-        for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
-        mx = fmaxf(mx, m);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        const float pr = expf(s - ref), f = expf(m - ref);
-        float sum = pr;
-        for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
-        l = l * f + sum;
-        m = mx;
-        for (int k = 0; k < 4; ++k) o[k] *= f;
-        for (int j = 0; j < 32; ++j) {
-            const float pj = __shfl_sync(~0u, pr, j);
-            const int64_t uj = __shfl_sync(~0u, unit_off, j);
-            if (uj < 0) continue;
-            const uint8_t *u = A.pages + uj;
-            const int pos = (base + j) & 15;
-            const float d = pj * __half2float(*reinterpret_cast<const __half *>(u + kPgVScales + (lane >> 3) * 32 + 2 * pos));
-            for (int k = 0; k < 4; ++k) {
-                const int c = u[kPgVCodes + ((4 * lane + k) & 63) * 16 + pg_v_byte(pos)];
-                o[k] += d * ((lane < 16 ? c & 15 : c >> 4) - 8);
-            }
-        }
-    }
-    for (int k = 0; k < 4; ++k) s_o[warp][4 * lane + k] = o[k];
-    if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
-    __syncthreads();
-    float mm = -INFINITY, ll = 0.f, oo = 0.f;
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, s_m[w]);
-    for (int w = 0; w < 4; ++w) {
-        const float f = s_m[w] == -INFINITY ? 0.f : expf(s_m[w] - mm);
-        ll += s_l[w] * f;
-        oo += s_o[w][tid] * f;
-    }
-    oo = ll > 0.f ? oo / ll : mm == -INFINITY ? 0.f : oo / ll;
-    const int64_t at = ((int64_t)t * A.Hq + h) * kPgDim + tid;
-    if (A.out_bf16) ((__nv_bfloat16 *)A.out)[at] = __float2bfloat16_rn(oo);
-    else ((float *)A.out)[at] = oo;
+// ---- geometry shared by the two kernels -----------------------------------------------------
+struct PaReq {
+    int q0, n, base, len, rows;  // first token, tokens, position of token 0, positions, query rows
+};
+__device__ __forceinline__ PaReq pa_req(const PaArgs &A, int r) {
+    PaReq x;
+    const int a = A.q_start[r], b = A.q_start[r + 1], kv = A.kv_len[r];
+    x.q0 = min(max(a, 0), A.T);
+    const int n = max(b - a, 0);
+    x.n = min(min(n, A.max_new), A.T - x.q0);
+    x.base = kv - n;
+    x.len = min(max(kv, 0), A.width * A.page);
+    x.rows = x.n * A.G;
+    return x;
+}
+// Tiles of row tile rt (one at least, so that every row gets written).
+template <int RP>
+__device__ __forceinline__ int pa_row_tiles(const PaArgs &A, const PaReq &x, int rt) {
+    const int last = (min((rt + 1) * RP, x.rows) - 1) / A.G;
+    const int see = min(x.base + last + 1, x.len);
+    return max(1, (see + kPaTile - 1) / kPaTile);
+}
+template <int RP>
+__device__ __forceinline__ int pa_head_tiles(const PaArgs &A, const PaReq &x) {
+    int s = 0;
+    for (int rt = 0; rt * RP < x.rows; ++rt) s += pa_row_tiles<RP>(A, x, rt);
+    return s;
+}
+// CTA b's range of n tiles, and the CTA of tile u (G CTAs, those past n idle).
+__device__ __forceinline__ int pa_lo(int n, int G, int b) {
+    const int g = min(G, n);
+    return b >= g ? n : (int)((int64_t)b * n / g);
+}
+__device__ __forceinline__ int pa_cta_of(int n, int G, int u) {
+    const int g = min(G, n);
+    return (int)((((int64_t)u + 1) * g - 1) / n);
 }
 
+// ---- tcgen05, TMEM, waits -------------------------------------------------------------------
+struct PaCtl {
+    uint32_t stop;
+    uint32_t limit;
+    uint32_t *status;
+};
+__device__ __forceinline__ bool pa_stopped(const PaCtl *c) {
+    return *reinterpret_cast<const volatile uint32_t *>(&c->stop) != 0u;
+}
+// Bounded wait; one that gives up stops the CTA (every later wait returns soon) and is recorded.
+__device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity, PaCtl *c) {
+    const uint32_t limit = c->limit;
+    const bool blocking = limit >= kDefaultPolls;
+    for (uint32_t it = 0; it < limit; ++it) {
+        if (mbar_poll(bar, parity, blocking)) return true;
+        if ((it & 15u) == 15u && pa_stopped(c)) return false;
+    }
+    *reinterpret_cast<volatile uint32_t *>(&c->stop) = 1u;
+    atomicOr(c->status, 1u);
+    return false;
+}
+__device__ __forceinline__ void pa_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pa_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void pa_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void pa_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pa_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void pa_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] B[smem]^T, fp16 operands, fp32 accumulators.
+__device__ __forceinline__ void pa_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void pa_st8(uint32_t t, const uint32_t *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void pa_ld8(uint32_t t, float *f) {
+    uint32_t *v = reinterpret_cast<uint32_t *>(f);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(t)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pa_h2add(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pa_h2mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pa_h2fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ float pa_ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Nibbles moved to fraction bits 6..9 under the exponent of 16: 16 + c in each half, exactly.
+__device__ __forceinline__ uint32_t pa_16plus(uint32_t moved) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(moved), "r"(0x03C003C0u), "r"(0x4C004C00u));
+    return r;
+}
+// Ordered integers of floats (NaN above +inf), for a warp-wide maximum.
+__device__ __forceinline__ int pa_order(float x) {
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float pa_unorder(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
+
+// Shared-memory descriptors: Q, K-major with the 128-byte swizzle (rows of 64 fp16, 8-row groups
+// 1024 bytes apart); P, row-major in positions (MN-major, no swizzle: 8 x 8 blocks of 16-byte lines
+// of eight rows, the next eight positions 128 bytes on, the next eight rows 2048).
+__device__ __forceinline__ uint64_t pa_desc_q(uint32_t a) {
+    return (uint64_t)((a & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t pa_desc_p(uint32_t a) {
+    return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)(128u >> 4) << 16) | ((uint64_t)(2048u >> 4) << 32) | (1ull << 46);
+}
+
+struct PaTileInfo {
+    uint32_t mask;    // units present, one bit each
+    int n_pos;        // positions of the request in the tile (may exceed 128)
+    int tile;         // index along the cache
+    uint32_t flags;   // 1 first, 2 last tile of the segment; segment ring entry above
+};
+struct PaSeg {
+    int token0, head0, row0, rows;  // first token of the request, first query head, rows of the tile
+    int base, len, slot;            // position of token 0; workspace slot, or -1: write the output
+    int tok, off;                   // token of row 0, and row 0 among its heads
+};
+
+template <int RP, bool F32>
+struct PaCfg {
+    static constexpr int N = RP < 16 ? 16 : (RP + 15) / 16 * 16;
+    static constexpr int kCtas = RP <= 24 ? 2 : 1;           // per SM
+    static constexpr int kVBufs = 192 + 2 * N <= 256 ? 2 : 1;  // V operands in tensor memory
+    static constexpr uint32_t kColK = 0, kColV = 64, kColS = 64 + 64 * kVBufs, kColO = kColS + N;
+    static constexpr uint32_t kCols = 256;
+    static_assert(kColO + N <= kCols, "tensor memory");
+    static constexpr int kQ = N * 256, kP = N * 256;
+    static constexpr size_t smem(int stages, int R) {
+        return 1024 + (size_t)stages * kPaStageBytes + kQ + kP * (F32 ? 2 : 1) + ((size_t)R + 1) * 4;
+    }
+};
+
+template <int RP, bool F32>
+__global__ void __launch_bounds__(kPaThreads, PaCfg<RP, F32>::kCtas)
+paged_attention_kernel(const __grid_constant__ PaArgs A) {
+    using Cfg = PaCfg<RP, F32>;
+    constexpr int N = Cfg::N;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t s_bar[2 * kPaMaxStages + 9];
+    __shared__ PaTileInfo s_info[kPaRing];
+    __shared__ PaSeg s_seg[kPaRing];
+    __shared__ __align__(16) float s_ref[RP], s_fac[RP], s_sum[4][RP];
+    __shared__ int s_max[4][RP];
+    __shared__ int s_scan[kPaThreads / 32];
+    __shared__ uint32_t s_tmem;
+    __shared__ PaCtl s_ctl;
+    uint8_t *const sm0 = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
+    uint8_t *const s_q = sm0 + A.stages * kPaStageBytes, *const s_p = s_q + Cfg::kQ;
+    int *const s_pre = reinterpret_cast<int *>(s_p + Cfg::kP * (F32 ? 2 : 1));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t bar0 = smem_u32(s_bar);
+    const uint32_t b_full = bar0, b_empty = bar0 + 8 * kPaMaxStages, b_k = bar0 + 16 * kPaMaxStages;
+    const uint32_t b_s = b_k + 8, b_p = b_k + 16, b_pv = b_k + 24, b_end = b_k + 32;
+    const uint32_t b_v = b_k + 40, b_vfree = b_k + 56;  // one for each V buffer
+
+    if (tid == 0) {
+        for (int i = 0; i < A.stages; ++i) {
+            mbar_init(b_full + 8 * i, 1);
+            mbar_init(b_empty + 8 * i, 8);
+        }
+        mbar_init(b_k, 4);
+        mbar_init(b_s, 1);
+        mbar_init(b_p, 4);
+        mbar_init(b_pv, 1);
+        mbar_init(b_end, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b_v + 8 * i, 4);
+            mbar_init(b_vfree + 8 * i, 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid < kPaRing) {
+        s_info[tid] = PaTileInfo{};
+        s_seg[tid] = PaSeg{};
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // Tiles before every request.
+    int n_tiles = 0;
+    for (int r0 = 0; r0 < A.R; r0 += kPaThreads) {
+        const int r = r0 + tid;
+        int mine = 0;
+        if (r < A.R) {
+            const PaReq x = pa_req(A, r);
+            mine = A.Hkv * pa_head_tiles<RP>(A, x);
+        }
+        int v = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(~0u, v, o);
+            if (lane >= o) v += u;
+        }
+        __syncthreads();
+        if (lane == 31) s_scan[warp] = v;
+        __syncthreads();
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kPaThreads / 32; ++w) {
+            const int y = s_scan[w];
+            if (w < warp) v += y;
+            all += y;
+        }
+        if (r < A.R) s_pre[r] = n_tiles + v - mine;
+        n_tiles += all;
+    }
+    if (tid == 0) {
+        s_pre[A.R] = n_tiles;
+        s_ctl.stop = 0u;
+        const uint32_t lim = reinterpret_cast<volatile uint32_t *>(A.status)[1];
+        s_ctl.limit = lim ? lim - 1u : kDefaultPolls;
+        s_ctl.status = A.status;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int r = tid; r <= A.R; r += kPaThreads) A.prefix[r] = s_pre[r];
+    const int lo = pa_lo(n_tiles, gridDim.x, blockIdx.x), hi = pa_lo(n_tiles, gridDim.x, blockIdx.x + 1);
+    const int count = hi - lo;
+    if (n_tiles == 0 || count <= 0) return;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(Cfg::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pa_fence_before();
+    __syncthreads();
+    pa_fence_after();
+    const uint32_t tmem = s_tmem;
+    const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
+
+    if (warp == 8) {
+        // ---- copies: lane j < 8 brings unit j of each tile ---------------------------------
+        // Descriptors of tile t (and its segment) go into ring entry t mod 8.  The slowest reader
+        // is at tile t - 6 at most: a stage is refilled after both dequantisations of its tile, and
+        // those run at most two tiles ahead of the last use of a descriptor.
+        int r = 0;
+        {
+            int a = 0, b = A.R;
+            while (b - a > 1) {
+                const int mid = (a + b) >> 1;
+                if (s_pre[mid] <= lo) a = mid; else b = mid;
+            }
+            r = a;
+        }
+        int u = lo, k = 0, n_seg = 0;
+        PaReq x = pa_req(A, r);
+        int head_tiles = pa_head_tiles<RP>(A, x);
+        while (u < hi) {
+            while (s_pre[r + 1] <= u) {
+                ++r;
+                if (s_pre[r + 1] > u) {
+                    x = pa_req(A, r);
+                    head_tiles = pa_head_tiles<RP>(A, x);
+                }
+            }
+            const int h = (u - s_pre[r]) / head_tiles;
+            int s0 = s_pre[r] + h * head_tiles, rt = 0, nt = pa_row_tiles<RP>(A, x, 0);
+            while (s0 + nt <= u) {
+                s0 += nt;
+                nt = pa_row_tiles<RP>(A, x, ++rt);
+            }
+            int end = min(hi, s0 + nt);
+            const int si = n_seg % kPaRing;
+            if (lane == 0) {
+                PaSeg g;
+                g.token0 = x.q0;
+                g.head0 = h * A.G;
+                g.row0 = rt * RP;
+                g.rows = min(RP, x.rows - rt * RP);
+                g.base = x.base;
+                g.len = x.len;
+                g.slot = u == s0 && end == s0 + nt ? -1 : 2 * (int)blockIdx.x + (u == s0 ? 1 : 0);
+                g.tok = g.row0 / A.G;
+                g.off = g.row0 - g.tok * A.G;
+                s_seg[si] = g;
+            }
+            const int32_t *const row = A.table + (int64_t)r * A.width;
+            auto lookup = [&](int tile) -> int {
+                const int p = (tile * kPaTileUnits + lane) * kPgUnitPos;
+                return lane < kPaTileUnits && p < x.len ? row[p / A.page] : -1;
+            };
+            int pg = lookup(u - s0);
+            for (; u < end; ++u, ++k) {
+                const int tile = u - s0, st = k % A.stages;
+                const int pg_next = u + 1 < end ? lookup(tile + 1) : -1;
+                // a wait that gave up ends the copies: no descriptor in use is overwritten
+                if (k >= A.stages && !pa_wait(b_empty + 8 * st, (uint32_t)(k / A.stages - 1) & 1u, &s_ctl)) {
+                    end = u = hi;
+                    break;
+                }
+                const bool ok = pg >= 0 && pg < A.n_pages;
+                const uint32_t mask = __ballot_sync(~0u, ok);
+                if (lane == 0) {
+                    PaTileInfo t;
+                    t.mask = mask;
+                    t.n_pos = x.len - tile * kPaTile;
+                    t.tile = tile;
+                    const bool first = tile == 0 || u == lo;
+                    t.flags = (first ? 1u : 0u) | (u + 1 == end ? 2u : 0u) | ((uint32_t)si << 2);
+                    s_info[k % kPaRing] = t;
+                    mbar_expect_tx(b_full + 8 * st, __popc(mask) * kPgUnitBytes);
+                }
+                __syncwarp();
+                if (ok) {
+                    const int unit = (tile * kPaTileUnits + lane) % (A.page / kPgUnitPos);
+                    bulk_g2s(smem_u32(sm0 + st * kPaStageBytes + lane * kPgUnitBytes),
+                             A.pages + (((int64_t)pg * A.Hkv + h) * (A.page / kPgUnitPos) + unit) * kPgUnitBytes,
+                             kPgUnitBytes, b_full + 8 * st);
+                }
+                pg = pg_next;
+            }
+            ++n_seg;
+        }
+        // After a give-up: the copies in flight land before the CTA ends.
+        if (pa_stopped(&s_ctl))
+            for (int j = max(0, k - A.stages); j < k; ++j)
+                mbar_wait_ok(b_full + 8 * (j % A.stages), (uint32_t)(j / A.stages) & 1u);
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---- MMAs: S of tile t + 1 before O of tile t --------------------------------------
+        constexpr uint32_t kId = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+        const uint32_t qa = smem_u32(s_q), pa = smem_u32(s_p);
+        auto issue_s = [&](int t) {
+            pa_wait(b_k, (uint32_t)t & 1u, &s_ctl);
+            if (lane == 0) {
+                pa_fence_after();
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    pa_mma(tmem + Cfg::kColS, tmem + Cfg::kColK + 8 * s,
+                           pa_desc_q(qa + (s >> 2) * (N * 128) + (s & 3) * 32), kId, s ? 1u : 0u);
+                pa_commit(b_s);
+            }
+            __syncwarp();
+        };
+        issue_s(0);
+        for (int t = 0; t < count; ++t) {
+            if (t + 1 < count) issue_s(t + 1);
+            const uint32_t first = s_info[t % kPaRing].flags & 1u;
+            pa_wait(b_p, (uint32_t)t & 1u, &s_ctl);
+            pa_wait(b_v + 8 * (t % Cfg::kVBufs), (uint32_t)(t / Cfg::kVBufs) & 1u, &s_ctl);
+            if (lane == 0) {
+                pa_fence_after();
+                const uint32_t va = tmem + Cfg::kColV + 64 * (t % Cfg::kVBufs);
+#pragma unroll
+                for (int part = 0; part < (F32 ? 2 : 1); ++part)
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        pa_mma(tmem + Cfg::kColO, va + 8 * s, pa_desc_p(pa + part * Cfg::kP + s * 256), kId | (1u << 16),
+                               s || part || !first ? 1u : 0u);
+                pa_commit(b_pv);
+                pa_commit(b_vfree + 8 * (t % Cfg::kVBufs));
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {
+            pa_commit(b_end);
+            mbar_wait_ok(b_end, 0u);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---- V: lane = dimension, columns of two positions ---------------------------------
+        const int dim = tid - 128;
+        const uint32_t up = dim < 64 ? 6u : 2u, down = 8u - up;  // to fraction bits 6..9
+        const uint8_t *const vrow = sm0 + kPgVCodes + (dim & 63) * 16;
+        const uint8_t *const vsc = sm0 + kPgVScales + (warp & 3) * 32;
+        for (int t = 0; t < count; ++t) {
+            const int st = t % A.stages;
+            pa_wait(b_full + 8 * st, (uint32_t)(t / A.stages) & 1u, &s_ctl);
+            const uint32_t mask = s_info[t % kPaRing].mask;
+            const int n_pos = s_info[t % kPaRing].n_pos;
+            const bool whole = mask == 0xFFu && n_pos >= kPaTile;
+            const int vb = t % Cfg::kVBufs;
+            if (t >= Cfg::kVBufs) pa_wait(b_vfree + 8 * vb, (uint32_t)(t / Cfg::kVBufs - 1) & 1u, &s_ctl);
+            pa_fence_after();
+            const uint32_t col = tmem + quarter + Cfg::kColV + 64 * vb;
+#pragma unroll
+            for (int j = 0; j < kPaTileUnits; ++j) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(vrow + st * kPaStageBytes + j * kPgUnitBytes);
+                uint32_t d[8];
+                *reinterpret_cast<uint4 *>(d) = *reinterpret_cast<const uint4 *>(vsc + st * kPaStageBytes + j * kPgUnitBytes);
+                *reinterpret_cast<uint4 *>(d + 4) =
+                    *reinterpret_cast<const uint4 *>(vsc + st * kPaStageBytes + j * kPgUnitBytes + 16);
+                if (!whole) {
+                    const int left = (mask >> j) & 1u ? n_pos - j * kPgUnitPos : 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        d[i] = 2 * i >= left ? 0u : 2 * i + 1 >= left ? d[i] & 0xFFFFu : d[i];
+                }
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[2 * i] = pa_h2mul(pa_h2add(pa_16plus(ww[i] << up), 0xCE00CE00u), d[2 * i]);
+                    o[2 * i + 1] = pa_h2mul(pa_h2add(pa_16plus(ww[i] >> down), 0xCE00CE00u), d[2 * i + 1]);
+                }
+                pa_st8(col + 8 * j, o);
+            }
+            pa_wait_st();
+            pa_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                pa_arrive(b_empty + 8 * st);
+                pa_arrive(b_v + 8 * vb);
+            }
+        }
+    } else {
+        // ---- K and the softmax: lane = position --------------------------------------------
+        const float c = A.c;
+        auto put_k = [&](int t) {
+            const int st = t % A.stages;
+            pa_wait(b_full + 8 * st, (uint32_t)(t / A.stages) & 1u, &s_ctl);
+            const uint32_t flags = s_info[t % kPaRing].flags;
+            if (flags & 1u) {  // a new segment: its query rows (the S products so far are done)
+                const PaSeg g = s_seg[flags >> 2];
+                for (int i = tid; i < RP * 16; i += 128) {
+                    const int row = i >> 4, ch = i & 15;
+                    uint4 o = {0u, 0u, 0u, 0u};
+                    if (row < g.rows) {
+                        const int rr = g.row0 + row, tok = rr / A.G;
+                        const uint4 w = *reinterpret_cast<const uint4 *>(
+                            A.q + ((int64_t)(g.token0 + tok) * A.Hq + g.head0 + rr - tok * A.G) * kPgDim + ch * 8);
+                        // dims 0 4 | 1 5 | 2 6 | 3 7, as the K words give them
+                        const uint32_t lo4[2] = {w.x, w.y}, hi4[2] = {w.z, w.w};
+                        uint32_t r4[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a = lo4[j >> 1], b = hi4[j >> 1];
+                            r4[j] = pa_pack(__uint_as_float(j & 1 ? a & 0xFFFF0000u : a << 16),
+                                            __uint_as_float(j & 1 ? b & 0xFFFF0000u : b << 16));
+                        }
+                        o = make_uint4(r4[0], r4[1], r4[2], r4[3]);
+                    }
+                    *reinterpret_cast<uint4 *>(s_q + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) * 16)) = o;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            const uint8_t *const unit = sm0 + st * kPaStageBytes + (tid >> 4) * kPgUnitBytes;
+            const uint2 sc = *reinterpret_cast<const uint2 *>(unit + kPgKScales + (lane & 15) * 8);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(unit + b * 256 + (lane & 15) * 16);
+                const uint32_t s1 = b < 2 ? sc.x : sc.y;
+                const uint32_t d = __byte_perm(s1, s1, b & 1 ? 0x3232 : 0x1010);
+                const uint32_t d8 = pa_h2mul(d, 0x30003000u), d3 = pa_h2mul(d, 0xC200C200u);  // d / 8, -3 d
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t o[8];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t y = ww[2 * half + i];
+                        o[4 * i + 0] = pa_h2fma(pa_16plus(y << 6), d8, d3);
+                        o[4 * i + 1] = pa_h2fma(pa_16plus(y << 2), d8, d3);
+                        o[4 * i + 2] = pa_h2fma(pa_16plus(y >> 2), d8, d3);
+                        o[4 * i + 3] = pa_h2fma(pa_16plus(y >> 6), d8, d3);
+                    }
+                    pa_st8(tmem + quarter + Cfg::kColK + 16 * b + 8 * half, o);
+                }
+            }
+            pa_wait_st();
+            pa_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                pa_arrive(b_empty + 8 * st);
+                pa_arrive(b_k);
+            }
+        };
+        auto group_sync = [&]() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); };
+
+        float l[RP];
+        put_k(0);
+        for (int t = 0; t < count; ++t) {
+            const PaTileInfo ti = s_info[t % kPaRing];
+            const bool first = ti.flags & 1u, last = ti.flags & 2u;
+            const PaSeg &g = s_seg[ti.flags >> 2];
+            float s[RP];
+            pa_wait(b_s, (uint32_t)t & 1u, &s_ctl);
+            pa_fence_after();
+#pragma unroll
+            for (int j = 0; j < RP; j += 8) pa_ld8(tmem + quarter + Cfg::kColS + j, s + j);
+            pa_wait_ld();
+            pa_fence_before();
+            if (t + 1 < count) put_k(t + 1);
+
+            if (first) {
+                if (tid < RP) s_ref[tid] = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < RP; ++j) l[j] = 0.f;
+                group_sync();
+            }
+            // What a row does not see is cut out (its first row sees the fewest positions).
+            const int pos = ti.tile * kPaTile + tid, see0 = g.base + g.tok + 1;
+            if (ti.mask != 0xFFu || ti.tile * kPaTile + kPaTile > min(see0, g.len)) {
+                const bool here = ((ti.mask >> (tid >> 4)) & 1u) && pos < g.len;
+                // row j is token tok + (off + j) / G: it sees the position once j reaches this
+                const int from = here ? (pos - (g.base + g.tok)) * A.G - g.off : RP;
+#pragma unroll
+                for (int j = 0; j < RP; ++j)
+                    if (j < from) s[j] = -INFINITY;
+            }
+            bool over = false;  // also of NaN: a row that has seen nothing yet, or a score that is none
+#pragma unroll
+            for (int j = 0; j < RP; j += 4) {
+                const float4 ref = *reinterpret_cast<const float4 *>(s_ref + j);
+                over |= !(fmaf(s[j], c, -ref.x) <= kPaOver);
+                over |= !(fmaf(s[j + 1], c, -ref.y) <= kPaOver);
+                over |= !(fmaf(s[j + 2], c, -ref.z) <= kPaOver);
+                over |= !(fmaf(s[j + 3], c, -ref.w) <= kPaOver);
+            }
+            uint32_t any;
+            asm volatile(
+                "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+                : "=r"(any)
+                : "r"((uint32_t)over)
+                : "memory");
+            if (any) {
+                // New references: 7 below the largest score so far, where that is higher.
+#pragma unroll
+                for (int j = 0; j < RP; ++j) {
+                    const int m = __reduce_max_sync(~0u, pa_order(s[j] * c));
+                    if (lane == 0) s_max[warp][j] = m;
+                }
+                group_sync();
+                if (tid < RP) {
+                    const int m = max(max(s_max[0][tid], s_max[1][tid]), max(s_max[2][tid], s_max[3][tid]));
+                    const float old = s_ref[tid], top = pa_unorder(m) - kPaUnder;
+                    const float ref = top > old || top != top ? top : old;
+                    s_fac[tid] = ref == old ? 1.f : pa_ex2(old - ref);
+                    s_ref[tid] = ref;
+                }
+                group_sync();
+                if (!first) {
+                    pa_wait(b_pv, (uint32_t)(t - 1) & 1u, &s_ctl);
+                    pa_fence_after();
+#pragma unroll
+                    for (int j = 0; j < RP; j += 8) {
+                        float o[8];
+                        pa_ld8(tmem + quarter + Cfg::kColO + j, o);
+                        pa_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            o[i] *= s_fac[j + i];
+                            l[j + i] *= s_fac[j + i];
+                        }
+                        pa_st8(tmem + quarter + Cfg::kColO + j, reinterpret_cast<const uint32_t *>(o));
+                    }
+                    pa_wait_st();
+                    pa_fence_before();
+                }
+            }
+            if (t > 0) pa_wait(b_pv, (uint32_t)(t - 1) & 1u, &s_ctl);  // P is read
+            uint8_t *const prow = s_p + (tid >> 3) * 128 + (tid & 7) * 16;
+#pragma unroll
+            for (int j = 0; j < RP; j += 8) {
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float ref = s_ref[j + i];
+                    // a row that has seen nothing has reference -inf and only scores of -inf
+                    p[i] = pa_ex2(fmaf(s[j + i], c, ref == -INFINITY ? 0.f : -ref));
+                    l[j + i] += p[i];
+                }
+                uint4 w = make_uint4(pa_pack(p[0], p[1]), pa_pack(p[2], p[3]), pa_pack(p[4], p[5]), pa_pack(p[6], p[7]));
+                *reinterpret_cast<uint4 *>(prow + (j >> 3) * 2048) = w;
+                if (F32) {
+                    const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t lo2[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = __half22float2(reinterpret_cast<const __half2 &>(h[i]));
+                        lo2[i] = pa_pack(p[2 * i] - f.x, p[2 * i + 1] - f.y);
+                    }
+                    *reinterpret_cast<uint4 *>(prow + Cfg::kP + (j >> 3) * 2048) = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) pa_arrive(b_p);
+
+            if (last) {
+                // The segment's sums over positions, then o.
+#pragma unroll
+                for (int j = 0; j < RP; ++j) {
+                    float v = l[j];
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+                    if (lane == 0) s_sum[warp][j] = v;
+                }
+                group_sync();
+                pa_wait(b_pv, (uint32_t)t & 1u, &s_ctl);
+                pa_fence_after();
+                const int slot = g.slot, rows = g.rows;
+#pragma unroll
+                for (int j = 0; j < RP; j += 8) {
+                    float o[8];
+                    pa_ld8(tmem + quarter + Cfg::kColO + j, o);
+                    pa_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = j + i;
+                        if (row < rows) {
+                            const float sum = s_sum[0][row] + s_sum[1][row] + s_sum[2][row] + s_sum[3][row];
+                            if (slot < 0) {
+                                const int rr = g.row0 + row, tok = rr / A.G;
+                                const int64_t at =
+                                    ((int64_t)(g.token0 + tok) * A.Hq + g.head0 + rr - tok * A.G) * kPgDim + tid;
+                                const float y = s_ref[row] == -INFINITY ? 0.f : __fdividef(o[i], sum);
+                                if (F32) reinterpret_cast<float *>(A.out)[at] = y;
+                                else reinterpret_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16_rn(y);
+                            } else {
+                                A.part[((int64_t)slot * RP + row) * kPgDim + tid] = o[i];
+                                if (tid == 0) A.part_ml[(int64_t)slot * RP + row] = make_float2(s_ref[row], sum);
+                            }
+                        }
+                    }
+                }
+                pa_fence_before();
+                group_sync();  // s_ref, s_sum and the O columns are free again
+            }
+        }
+    }
+    pa_fence_before();
+    __syncthreads();
+    pa_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Cfg::kCols) : "memory");
+}
+
+// Joins the segments of a row that several CTAs hold: one warp per (token, query head).
+template <int RP, bool F32>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PaArgs A, int ctas) {
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    griddep_wait();
+    const int t = (int)(w / A.Hq), head = (int)(w - (int64_t)t * A.Hq);
+    if (t >= A.T || t >= A.q_start[A.R]) return;
+    const int n_tiles = A.prefix[A.R];
+    if (n_tiles == 0) return;
+    int r = 0, b = A.R;
+    while (b - r > 1) {
+        const int mid = (r + b) >> 1;
+        if (A.q_start[mid] <= t) r = mid; else b = mid;
+    }
+    const PaReq x = pa_req(A, r);
+    const int i = t - x.q0;
+    if (i < 0 || i >= x.n) return;
+    const int h = head / A.G, rr = i * A.G + head - h * A.G, rt = rr / RP, row = rr - rt * RP;
+    int before = 0;
+    for (int j = 0; j < rt; ++j) before += pa_row_tiles<RP>(A, x, j);
+    const int nt = pa_row_tiles<RP>(A, x, rt);
+    const int per = (A.prefix[r + 1] - A.prefix[r]) / A.Hkv;
+    const int s0 = A.prefix[r] + h * per + before;
+    const int f = pa_cta_of(n_tiles, ctas, s0), e = pa_cta_of(n_tiles, ctas, s0 + nt - 1);
+    if (f == e) return;
+    auto slot = [&](int c) { return (int64_t)(c == f ? 2 * f + 1 : 2 * c) * RP + row; };
+    float ref = -INFINITY;
+    bool nan = false;
+    for (int c = f + lane; c <= e; c += 32) {
+        const float2 ml = A.part_ml[slot(c)];
+        nan |= ml.x != ml.x;
+        ref = fmaxf(ref, ml.x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(~0u, ref, o));
+    const bool empty = ref == -INFINITY && !__any_sync(~0u, nan);
+    float sum = 0.f;
+    float4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = f; c0 <= e; c0 += 8) {
+        float4 o[8];
+        float2 ml[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c0 + j <= e) {
+                ml[j] = A.part_ml[slot(c0 + j)];
+                o[j] = *reinterpret_cast<const float4 *>(A.part + slot(c0 + j) * kPgDim + 4 * lane);
+            }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c0 + j <= e) {
+                if (ml[j].x == -INFINITY) continue;  // saw nothing: its sums are zero
+                const float k = pa_ex2(ml[j].x - ref);
+                sum += ml[j].y * k;
+                acc.x += o[j].x * k;
+                acc.y += o[j].y * k;
+                acc.z += o[j].z * k;
+                acc.w += o[j].w * k;
+            }
+    }
+    const float inv = empty ? 0.f : 1.f / sum;
+    const int64_t at = w * kPgDim + 4 * lane;
+    if (F32) {
+        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(A.out) + at) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 q = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        uint2 v;
+        v.x = reinterpret_cast<const uint32_t &>(p);
+        v.y = reinterpret_cast<const uint32_t &>(q);
+        *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(A.out) + at) = v;
+    }
+}
+
+// Rows per tile: the fewest that hold a window's rows, 64 for longer ones.
+static int pa_rows(int G, int max_new) {
+    const int64_t rows = (int64_t)G * max_new;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows <= 32 ? 32 : 64;
+}
+static int pa_ctas(int rp) { return (rp <= 24 ? 2 : 1) * sm_count(); }
+
+template <int RP, bool F32>
+static int pa_launch(PaArgs A, cudaStream_t stream) {
+    using Cfg = PaCfg<RP, F32>;
+    const size_t most = Cfg::kCtas == 2 ? 110 * 1024 : 220 * 1024;  // with the static part and 1 KB reserved a CTA
+    A.stages = kPaMaxStages;
+    while (A.stages > 2 && Cfg::smem(A.stages, A.R) > most) --A.stages;
+    const size_t smem = Cfg::smem(A.stages, A.R);
+    const int grid = Cfg::kCtas * sm_count();
+    SVD_CUDA_TRY(cudaFuncSetAttribute(paged_attention_kernel<RP, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)smem));
+    SVD_CUDA_TRY(launch(paged_attention_kernel<RP, F32>, dim3(grid), dim3(kPaThreads), smem, stream, true, A));
+    const int64_t warps = (int64_t)A.T * A.Hq;
+    SVD_CUDA_TRY(launch(paged_merge_kernel<RP, F32>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, stream, true, A, grid));
+    return SVD_OK;
+}
+
+static size_t pa_prefix_bytes(int R) { return align_up(kPaHeader + ((size_t)R + 1) * 4, 256); }
+
 size_t paged_attention_ws_bytes(int Hq, int Hkv, int R, int max_new) {
-    if (Hq < 1 || Hkv < 1 || Hq % Hkv || R < 1 || R > SVD_PAGED_MAX_REQUESTS || max_new < 1) return 0;
-    return 256;
+    if (Hq < 1 || Hq > 4096 || Hkv < 1 || Hq % Hkv || R < 1 || R > SVD_PAGED_MAX_REQUESTS || max_new < 1 || sm_count() < 1)
+        return 0;
+    const int rp = pa_rows(Hq / Hkv, max_new);
+    return pa_prefix_bytes(R) + (size_t)2 * pa_ctas(rp) * rp * (kPgDim + 2) * 4;
 }
 
 int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,
@@ -109,17 +829,48 @@ int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32
     if (!q || !kv_len || !q_start || !table || !pages || !out || !aligned16(q) || !aligned16(pages) ||
         !aligned16(out) || !aligned16(ws) || (out_dtype != SVD_F32 && out_dtype != SVD_BF16))
         return SVD_ERR_INVALID_ARG;
-    if (T < 0 || R < 1 || R > SVD_PAGED_MAX_REQUESTS || max_new < 1 || width < 1 ||
-        !pg_pool_ok(Hkv, page, n_pages) || (int64_t)width * page > INT32_MAX || Hq < 1 || Hq > 4096 ||
-        Hq % Hkv || !(scale > 0.f) || scale > 3.4e38f)
+    if (T < 0 || R < 1 || R > SVD_PAGED_MAX_REQUESTS || max_new < 1 || max_new > 1 << 20 || width < 1 ||
+        !pg_pool_ok(Hkv, page, n_pages) || (int64_t)width * page > INT32_MAX - kPaTile || Hq < 1 || Hq > 4096 ||
+        Hq % Hkv || (int64_t)T * Hq > INT32_MAX || !(scale > 0.f) || scale > 3.4e38f)
         return SVD_ERR_INVALID_ARG;
-    const size_t need = paged_attention_ws_bytes(Hq, Hkv, R, max_new);
-    if (!ws || ws_bytes < need) return SVD_ERR_WORKSPACE;
+    if (!ws || ws_bytes < paged_attention_ws_bytes(Hq, Hkv, R, max_new)) return SVD_ERR_WORKSPACE;
     if (T == 0) return SVD_OK;
-    const PaArgs A = {(const __nv_bfloat16 *)q, kv_len, q_start, table, (const uint8_t *)pages, out, n_pages,
-                      T, R, max_new, width, page, Hq, Hkv, out_dtype == SVD_BF16, scale};
-    SVD_CUDA_TRY(launch(paged_attention_plain_kernel, dim3(T, Hq), dim3(128), 0, stream, true, A));
-    return SVD_OK;
+    const int G = Hq / Hkv, rp = pa_rows(G, max_new);
+    // the tiles of the largest call that these arguments allow are counted in 31 bits
+    const int64_t row_tiles = ((int64_t)G * (max_new < T ? max_new : T) + rp - 1) / rp;
+    const double most = (double)R * Hkv * row_tiles * (((int64_t)width * page + kPaTile - 1) / kPaTile);
+    if (most > 2.0e9) return SVD_ERR_UNSUPPORTED;
+    uint8_t *const w = (uint8_t *)ws + pa_prefix_bytes(R);
+    PaArgs A = {};
+    A.q = (const __nv_bfloat16 *)q;
+    A.kv_len = kv_len;
+    A.q_start = q_start;
+    A.table = table;
+    A.pages = (const uint8_t *)pages;
+    A.out = out;
+    A.status = (uint32_t *)ws;
+    A.prefix = (int32_t *)((uint8_t *)ws + kPaHeader);
+    A.part = (float *)w;
+    A.part_ml = (float2 *)(w + (size_t)2 * pa_ctas(rp) * rp * kPgDim * 4);
+    A.n_pages = n_pages;
+    A.T = T;
+    A.R = R;
+    A.max_new = max_new;
+    A.width = width;
+    A.page = page;
+    A.Hq = Hq;
+    A.Hkv = Hkv;
+    A.G = G;
+    A.c = scale * 1.4426950408889634f * 8.f;
+#define SVD_PA(RP) (out_dtype == SVD_F32 ? pa_launch<RP, true>(A, stream) : pa_launch<RP, false>(A, stream))
+    switch (rp) {
+        case 8: return SVD_PA(8);
+        case 16: return SVD_PA(16);
+        case 24: return SVD_PA(24);
+        case 32: return SVD_PA(32);
+        default: return SVD_PA(64);
+    }
+#undef SVD_PA
 }
 
 }  // namespace svd
