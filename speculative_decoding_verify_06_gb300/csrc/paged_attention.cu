@@ -143,9 +143,31 @@ __device__ __forceinline__ void pa_ld8(uint32_t t, float *f) {
                  : "r"(t)
                  : "memory");
 }
-__device__ __forceinline__ uint32_t pa_h2add(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+// Pairs of fp32.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pa_f2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 pa_un2(f2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ f2 pa_fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 pa_add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 pa_mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint32_t pa_h2mul(uint32_t a, uint32_t b) {
@@ -206,7 +228,7 @@ struct PaSeg {
 template <int RP, bool F32>
 struct PaCfg {
     static constexpr int N = RP < 16 ? 16 : (RP + 15) / 16 * 16;
-    static constexpr int kCtas = RP <= 24 ? 2 : 1;           // per SM
+    static constexpr int kCtas = RP <= (F32 ? 16 : 24) ? 2 : 1;  // per SM
     static constexpr int kVBufs = 192 + 2 * N <= 256 ? 2 : 1;  // V operands in tensor memory
     static constexpr uint32_t kColK = 0, kColV = 64, kColS = 64 + 64 * kVBufs, kColO = kColS + N;
     static constexpr uint32_t kCols = 256;
@@ -226,7 +248,9 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
     __shared__ __align__(8) uint64_t s_bar[2 * kPaMaxStages + 9];
     __shared__ PaTileInfo s_info[kPaRing];
     __shared__ PaSeg s_seg[kPaRing];
-    __shared__ __align__(16) float s_ref[RP], s_fac[RP], s_sum[4][RP];
+    __shared__ __align__(16) float s_nref[RP], s_del[RP], s_fac[RP], s_sum[4][RP];
+    __shared__ int s_unset[1];  // whether a row has no reference yet (s_seen: each row's)
+    __shared__ uint8_t s_seen[RP];
     __shared__ int s_max[4][RP];
     __shared__ int s_scan[kPaThreads / 32];
     __shared__ uint32_t s_tmem;
@@ -434,8 +458,8 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                 for (int part = 0; part < (F32 ? 2 : 1); ++part)
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        pa_mma(tmem + Cfg::kColO, va + 8 * s, pa_desc_p(pa + part * Cfg::kP + s * 256), kId | (1u << 16),
-                               s || part || !first ? 1u : 0u);
+                        pa_mma(tmem + Cfg::kColO, va + 8 * s, pa_desc_p(pa + (F32 ? 1 - part : 0) * Cfg::kP + s * 256),
+                               kId | (1u << 16), s || part || (!F32 && !first) ? 1u : 0u);
                 pa_commit(b_pv);
                 pa_commit(b_vfree + 8 * (t % Cfg::kVBufs));
             }
@@ -449,7 +473,9 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
     } else if (warp >= 4) {
         // ---- V: lane = dimension, columns of two positions ---------------------------------
         const int dim = tid - 128;
-        const uint32_t up = dim < 64 ? 6u : 2u, down = 8u - up;  // to fraction bits 6..9
+        // low nibbles: (1024 + c) - 1032; high ones: (1024 + 16 c) / 16 - 72; both c - 8 exactly
+        const uint32_t nib = dim < 64 ? 0x000F000Fu : 0x00F000F0u;
+        const uint32_t mul = dim < 64 ? 0x3C003C00u : 0x2C002C00u, add = dim < 64 ? 0xE408E408u : 0xD480D480u;
         const uint8_t *const vrow = sm0 + kPgVCodes + (dim & 63) * 16;
         const uint8_t *const vsc = sm0 + kPgVScales + (warp & 3) * 32;
         for (int t = 0; t < count; ++t) {
@@ -462,7 +488,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             if (t >= Cfg::kVBufs) pa_wait(b_vfree + 8 * vb, (uint32_t)(t / Cfg::kVBufs - 1) & 1u, &s_ctl);
             pa_fence_after();
             const uint32_t col = tmem + quarter + Cfg::kColV + 64 * vb;
-#pragma unroll
+#pragma unroll 2
             for (int j = 0; j < kPaTileUnits; ++j) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(vrow + st * kPaStageBytes + j * kPgUnitBytes);
                 uint32_t d[8];
@@ -479,8 +505,8 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                 uint32_t o[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    o[2 * i] = pa_h2mul(pa_h2add(pa_16plus(ww[i] << up), 0xCE00CE00u), d[2 * i]);
-                    o[2 * i + 1] = pa_h2mul(pa_h2add(pa_16plus(ww[i] >> down), 0xCE00CE00u), d[2 * i + 1]);
+                    o[2 * i] = pa_h2mul(pa_h2fma((ww[i] & nib) | 0x64006400u, mul, add), d[2 * i]);
+                    o[2 * i + 1] = pa_h2mul(pa_h2fma(((ww[i] >> 8) & nib) | 0x64006400u, mul, add), d[2 * i + 1]);
                 }
                 pa_st8(col + 8 * j, o);
             }
@@ -525,7 +551,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             }
             const uint8_t *const unit = sm0 + st * kPaStageBytes + (tid >> 4) * kPgUnitBytes;
             const uint2 sc = *reinterpret_cast<const uint2 *>(unit + kPgKScales + (lane & 15) * 8);
-#pragma unroll
+#pragma unroll 1
             for (int b = 0; b < 4; ++b) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(unit + b * 256 + (lane & 15) * 16);
                 const uint32_t s1 = b < 2 ? sc.x : sc.y;
@@ -556,26 +582,49 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         };
         auto group_sync = [&]() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); };
 
-        float l[RP];
+        // l: sums of p over this lane's positions.  acc (fp32 outputs): o, added up here tile by tile,
+        // since the tensor core truncates what it adds to its accumulators (2^-24 a time).
+        f2 l[RP / 2], acc[F32 ? RP / 2 : 1];
+        const f2 c2 = pa_f2(c, c);
         put_k(0);
         for (int t = 0; t < count; ++t) {
             const PaTileInfo ti = s_info[t % kPaRing];
             const bool first = ti.flags & 1u, last = ti.flags & 2u;
             const PaSeg &g = s_seg[ti.flags >> 2];
-            float s[RP];
+            f2 s[RP / 2];
             pa_wait(b_s, (uint32_t)t & 1u, &s_ctl);
             pa_fence_after();
+            {
+                float f[RP];
 #pragma unroll
-            for (int j = 0; j < RP; j += 8) pa_ld8(tmem + quarter + Cfg::kColS + j, s + j);
-            pa_wait_ld();
+                for (int j = 0; j < RP; j += 8) pa_ld8(tmem + quarter + Cfg::kColS + j, f + j);
+                pa_wait_ld();
+#pragma unroll
+                for (int j = 0; j < RP / 2; ++j) s[j] = pa_f2(f[2 * j], f[2 * j + 1]);
+            }
             pa_fence_before();
             if (t + 1 < count) put_k(t + 1);
 
             if (first) {
-                if (tid < RP) s_ref[tid] = -INFINITY;
+                if (tid < RP) {
+                    s_nref[tid] = 0.f;
+                    s_seen[tid] = 0;
+                }
+                if (tid == 0) s_unset[0] = 1;
 #pragma unroll
-                for (int j = 0; j < RP; ++j) l[j] = 0.f;
+                for (int j = 0; j < RP / 2; ++j) l[j] = 0ull;
+                if (F32) {
+#pragma unroll
+                    for (int j = 0; j < RP / 2; ++j) acc[j] = 0ull;
+                }
                 group_sync();
+            }
+            // s = score - reference, in powers of two.
+#pragma unroll
+            for (int j = 0; j < RP / 2; j += 2) {
+                const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_nref + 2 * j);
+                s[j] = pa_fma2(s[j], c2, r.x);
+                s[j + 1] = pa_fma2(s[j + 1], c2, r.y);
             }
             // What a row does not see is cut out (its first row sees the fewest positions).
             const int pos = ti.tile * kPaTile + tid, see0 = g.base + g.tok + 1;
@@ -584,70 +633,112 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                 // row j is token tok + (off + j) / G: it sees the position once j reaches this
                 const int from = here ? (pos - (g.base + g.tok)) * A.G - g.off : RP;
 #pragma unroll
-                for (int j = 0; j < RP; ++j)
-                    if (j < from) s[j] = -INFINITY;
+                for (int j = 0; j < RP / 2; ++j) {
+                    float2 v = pa_un2(s[j]);
+                    if (2 * j < from) v.x = -INFINITY;
+                    if (2 * j + 1 < from) v.y = -INFINITY;
+                    s[j] = pa_f2(v.x, v.y);
+                }
             }
-            bool over = false;  // also of NaN: a row that has seen nothing yet, or a score that is none
+            float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < RP; j += 4) {
-                const float4 ref = *reinterpret_cast<const float4 *>(s_ref + j);
-                over |= !(fmaf(s[j], c, -ref.x) <= kPaOver);
-                over |= !(fmaf(s[j + 1], c, -ref.y) <= kPaOver);
-                over |= !(fmaf(s[j + 2], c, -ref.z) <= kPaOver);
-                over |= !(fmaf(s[j + 3], c, -ref.w) <= kPaOver);
+            for (int j = 0; j < RP / 2; ++j) {
+                const float2 v = pa_un2(s[j]);
+                top = fmaxf(fmaxf(top, v.x), v.y);
             }
             uint32_t any;
             asm volatile(
                 "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
                 : "=r"(any)
-                : "r"((uint32_t)over)
+                : "r"((uint32_t)(top > kPaOver || s_unset[0] != 0))
                 : "memory");
             if (any) {
-                // New references: 7 below the largest score so far, where that is higher.
+                // New references, 7 below the largest score, for rows without one and for those that
+                // a score exceeds by more than 15.
 #pragma unroll
-                for (int j = 0; j < RP; ++j) {
-                    const int m = __reduce_max_sync(~0u, pa_order(s[j] * c));
-                    if (lane == 0) s_max[warp][j] = m;
+                for (int j = 0; j < RP / 2; ++j) {
+                    const float2 v = pa_un2(s[j]);
+                    const int m0 = __reduce_max_sync(~0u, pa_order(v.x)), m1 = __reduce_max_sync(~0u, pa_order(v.y));
+                    if (lane == 0) {
+                        s_max[warp][2 * j] = m0;
+                        s_max[warp][2 * j + 1] = m1;
+                    }
                 }
+                if (tid == 0) s_unset[0] = 0;
                 group_sync();
                 if (tid < RP) {
-                    const int m = max(max(s_max[0][tid], s_max[1][tid]), max(s_max[2][tid], s_max[3][tid]));
-                    const float old = s_ref[tid], top = pa_unorder(m) - kPaUnder;
-                    const float ref = top > old || top != top ? top : old;
-                    s_fac[tid] = ref == old ? 1.f : pa_ex2(old - ref);
-                    s_ref[tid] = ref;
+                    const float m =
+                        pa_unorder(max(max(s_max[0][tid], s_max[1][tid]), max(s_max[2][tid], s_max[3][tid])));
+                    const bool set = s_seen[tid];
+                    float del = 0.f, old = s_nref[tid];
+                    if (m != -INFINITY && (!set || !(m <= kPaOver))) {
+                        const float now = old + (kPaUnder - m);
+                        del = now - old;
+                        s_nref[tid] = now;
+                        s_seen[tid] = 1;
+                    } else if (!set) {
+                        s_unset[0] = 1;
+                    }
+                    s_del[tid] = del;
+                    s_fac[tid] = set ? pa_ex2(del) : 1.f;
                 }
                 group_sync();
+#pragma unroll
+                for (int j = 0; j < RP / 2; j += 2) {
+                    const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_del + 2 * j);
+                    s[j] = pa_add2(s[j], r.x);
+                    s[j + 1] = pa_add2(s[j + 1], r.y);
+                }
                 if (!first) {
-                    pa_wait(b_pv, (uint32_t)(t - 1) & 1u, &s_ctl);
-                    pa_fence_after();
 #pragma unroll
-                    for (int j = 0; j < RP; j += 8) {
-                        float o[8];
-                        pa_ld8(tmem + quarter + Cfg::kColO + j, o);
-                        pa_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            o[i] *= s_fac[j + i];
-                            l[j + i] *= s_fac[j + i];
-                        }
-                        pa_st8(tmem + quarter + Cfg::kColO + j, reinterpret_cast<const uint32_t *>(o));
+                    for (int j = 0; j < RP / 2; ++j) {
+                        const f2 f = *reinterpret_cast<const f2 *>(s_fac + 2 * j);
+                        l[j] = pa_mul2(l[j], f);
                     }
-                    pa_wait_st();
-                    pa_fence_before();
+                    if (!F32) {
+                        pa_wait(b_pv, (uint32_t)(t - 1) & 1u, &s_ctl);
+                        pa_fence_after();
+#pragma unroll
+                        for (int j = 0; j < RP; j += 8) {
+                            float o[8];
+                            pa_ld8(tmem + quarter + Cfg::kColO + j, o);
+                            pa_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] *= s_fac[j + i];
+                            pa_st8(tmem + quarter + Cfg::kColO + j, reinterpret_cast<const uint32_t *>(o));
+                        }
+                        pa_wait_st();
+                        pa_fence_before();
+                    }
                 }
             }
             if (t > 0) pa_wait(b_pv, (uint32_t)(t - 1) & 1u, &s_ctl);  // P is read
+            if (F32 && !first) {
+                pa_fence_after();
+#pragma unroll
+                for (int j = 0; j < RP; j += 8) {
+                    float o[8];
+                    pa_ld8(tmem + quarter + Cfg::kColO + j, o);
+                    pa_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j / 2 + i] = pa_add2(acc[j / 2 + i], pa_f2(o[2 * i], o[2 * i + 1]));
+                }
+                pa_fence_before();
+                if (any) {
+#pragma unroll
+                    for (int j = 0; j < RP / 2; ++j) acc[j] = pa_mul2(acc[j], *reinterpret_cast<const f2 *>(s_fac + 2 * j));
+                }
+            }
             uint8_t *const prow = s_p + (tid >> 3) * 128 + (tid & 7) * 16;
 #pragma unroll
             for (int j = 0; j < RP; j += 8) {
                 float p[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float ref = s_ref[j + i];
-                    // a row that has seen nothing has reference -inf and only scores of -inf
-                    p[i] = pa_ex2(fmaf(s[j + i], c, ref == -INFINITY ? 0.f : -ref));
-                    l[j + i] += p[i];
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = pa_un2(s[j / 2 + i]);
+                    p[2 * i] = pa_ex2(v.x);
+                    p[2 * i + 1] = pa_ex2(v.y);
+                    l[j / 2 + i] = pa_add2(l[j / 2 + i], pa_f2(p[2 * i], p[2 * i + 1]));
                 }
                 uint4 w = make_uint4(pa_pack(p[0], p[1]), pa_pack(p[2], p[3]), pa_pack(p[4], p[5]), pa_pack(p[6], p[7]));
                 *reinterpret_cast<uint4 *>(prow + (j >> 3) * 2048) = w;
@@ -670,7 +761,8 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                 // The segment's sums over positions, then o.
 #pragma unroll
                 for (int j = 0; j < RP; ++j) {
-                    float v = l[j];
+                    const float2 v2 = pa_un2(l[j / 2]);
+                    float v = j & 1 ? v2.y : v2.x;
 #pragma unroll
                     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
                     if (lane == 0) s_sum[warp][j] = v;
@@ -684,6 +776,14 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                     float o[8];
                     pa_ld8(tmem + quarter + Cfg::kColO + j, o);
                     pa_wait_ld();
+                    if (F32) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 v = pa_un2(acc[j / 2 + i]);
+                            o[2 * i] += v.x;
+                            o[2 * i + 1] += v.y;
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int row = j + i;
@@ -693,18 +793,19 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                                 const int rr = g.row0 + row, tok = rr / A.G;
                                 const int64_t at =
                                     ((int64_t)(g.token0 + tok) * A.Hq + g.head0 + rr - tok * A.G) * kPgDim + tid;
-                                const float y = s_ref[row] == -INFINITY ? 0.f : __fdividef(o[i], sum);
+                                const float y = s_seen[row] ? o[i] / sum : 0.f;
                                 if (F32) reinterpret_cast<float *>(A.out)[at] = y;
                                 else reinterpret_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16_rn(y);
                             } else {
                                 A.part[((int64_t)slot * RP + row) * kPgDim + tid] = o[i];
-                                if (tid == 0) A.part_ml[(int64_t)slot * RP + row] = make_float2(s_ref[row], sum);
+                                if (tid == 0) A.part_ml[(int64_t)slot * RP + row] =
+                                                  make_float2(s_seen[row] ? -s_nref[row] : -INFINITY, sum);
                             }
                         }
                     }
                 }
                 pa_fence_before();
-                group_sync();  // s_ref, s_sum and the O columns are free again
+                group_sync();  // s_nref, s_sum and the O columns are free again
             }
         }
     }
@@ -790,12 +891,13 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
     }
 }
 
-// Rows per tile: the fewest that hold a window's rows, 64 for longer ones.
-static int pa_rows(int G, int max_new) {
+// Rows per tile: the fewest that hold a window's rows, 64 for longer ones (32 for fp32 outputs,
+// whose sums live in registers beside the scores).
+static int pa_rows(int G, int max_new, bool f32) {
     const int64_t rows = (int64_t)G * max_new;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows <= 32 ? 32 : 64;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows <= 32 || f32 ? 32 : 64;
 }
-static int pa_ctas(int rp) { return (rp <= 24 ? 2 : 1) * sm_count(); }
+static int pa_ctas(int rp) { return (rp <= 24 ? 2 : 1) * sm_count(); }  // at most
 
 template <int RP, bool F32>
 static int pa_launch(PaArgs A, cudaStream_t stream) {
@@ -818,7 +920,7 @@ static size_t pa_prefix_bytes(int R) { return align_up(kPaHeader + ((size_t)R + 
 size_t paged_attention_ws_bytes(int Hq, int Hkv, int R, int max_new) {
     if (Hq < 1 || Hq > 4096 || Hkv < 1 || Hq % Hkv || R < 1 || R > SVD_PAGED_MAX_REQUESTS || max_new < 1 || sm_count() < 1)
         return 0;
-    const int rp = pa_rows(Hq / Hkv, max_new);
+    const int rp = pa_rows(Hq / Hkv, max_new, false);  // no fewer bytes than the fp32 variant takes
     return pa_prefix_bytes(R) + (size_t)2 * pa_ctas(rp) * rp * (kPgDim + 2) * 4;
 }
 
@@ -835,7 +937,7 @@ int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32
         return SVD_ERR_INVALID_ARG;
     if (!ws || ws_bytes < paged_attention_ws_bytes(Hq, Hkv, R, max_new)) return SVD_ERR_WORKSPACE;
     if (T == 0) return SVD_OK;
-    const int G = Hq / Hkv, rp = pa_rows(G, max_new);
+    const int G = Hq / Hkv, rp = pa_rows(G, max_new, out_dtype == SVD_F32);
     // the tiles of the largest call that these arguments allow are counted in 31 bits
     const int64_t row_tiles = ((int64_t)G * (max_new < T ? max_new : T) + rp - 1) / rp;
     const double most = (double)R * Hkv * row_tiles * (((int64_t)width * page + kPaTile - 1) / kPaTile);
@@ -868,7 +970,7 @@ int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32
         case 16: return SVD_PA(16);
         case 24: return SVD_PA(24);
         case 32: return SVD_PA(32);
-        default: return SVD_PA(64);
+        default: return pa_launch<64, false>(A, stream);
     }
 #undef SVD_PA
 }
