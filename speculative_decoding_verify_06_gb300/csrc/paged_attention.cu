@@ -36,7 +36,6 @@ constexpr int kPaTileUnits = kPaTile / kPgUnitPos;
 constexpr int kPaStageBytes = kPaTileUnits * kPgUnitBytes;
 constexpr int kPaMaxStages = 4;
 constexpr int kPaRing = 8;           // tile and segment descriptors in flight (see producer)
-constexpr int kPaThreads = 320;      // K/softmax 4 warps, V 4 warps, copies, MMA
 constexpr float kPaOver = 15.f;      // a score this far above the reference moves it ...
 constexpr float kPaUnder = 7.f;      // ... to this far below the new maximum
 constexpr int kPaHeader = 256;       // workspace: status word, tile count, then the prefix sums
@@ -52,6 +51,7 @@ struct PaArgs {
     float2 *part_ml;  // [2 CTAs][RP] (reference, sum)
     int64_t n_pages;
     int T, R, max_new, width, page, Hq, Hkv, G, stages;
+    uint32_t upp_magic;  // ceil(2^32 / units of a page)
     float c;          // scale * log2(e) * 8 (the K operand is K / 8)
 };
 
@@ -94,6 +94,7 @@ __device__ __forceinline__ int pa_cta_of(int n, int G, int u) {
 }
 
 // ---- tcgen05, TMEM, waits -------------------------------------------------------------------
+constexpr uint32_t kPaPolls = 1u << 18;  // blocking polls, about a second
 struct PaCtl {
     uint32_t stop;
     uint32_t limit;
@@ -104,15 +105,21 @@ __device__ __forceinline__ bool pa_stopped(const PaCtl *c) {
 }
 // Bounded wait; one that gives up stops the CTA (every later wait returns soon) and is recorded.
 __device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity, PaCtl *c) {
-    const uint32_t limit = c->limit;
-    const bool blocking = limit >= kDefaultPolls;
-    for (uint32_t it = 0; it < limit; ++it) {
-        if (mbar_poll(bar, parity, blocking)) return true;
-        if ((it & 15u) == 15u && pa_stopped(c)) return false;
+    bool ok = mbar_poll(bar, parity, true);
+    if (!ok) {
+        const uint32_t limit = c->limit;
+#pragma unroll 1
+        for (uint32_t it = 0; it < limit; ++it) {
+            ok = mbar_poll(bar, parity, true);
+            if (ok || pa_stopped(c)) break;
+        }
+        if (!ok && !pa_stopped(c)) {
+            *reinterpret_cast<volatile uint32_t *>(&c->stop) = 1u;
+            atomicOr(c->status, 1u);
+        }
     }
-    *reinterpret_cast<volatile uint32_t *>(&c->stop) = 1u;
-    atomicOr(c->status, 1u);
-    return false;
+    __syncwarp();
+    return ok;
 }
 __device__ __forceinline__ void pa_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -225,71 +232,94 @@ struct PaSeg {
     int tok, off;                   // token of row 0, and row 0 among its heads
 };
 
+// Warps: four for K, four for V, four for each softmax group (of up to 32 rows), one that copies and
+// two that issue the MMAs of S and of O.  Two CTAs to an SM where registers and tensor memory allow, so that
+// one's waits are filled by the other.
 template <int RP, bool F32>
 struct PaCfg {
     static constexpr int N = RP < 16 ? 16 : (RP + 15) / 16 * 16;
+    static constexpr int kGroups = RP > 32 ? 2 : 1, RG = RP / kGroups;  // softmax groups, rows of each
+    static constexpr int kThreads = (8 + 4 * kGroups + 3) * 32;
     static constexpr int kCtas = RP <= (F32 ? 16 : 24) ? 2 : 1;  // per SM
-    static constexpr int kVBufs = 192 + 2 * N <= 256 ? 2 : 1;  // V operands in tensor memory
-    static constexpr uint32_t kColK = 0, kColV = 64, kColS = 64 + 64 * kVBufs, kColO = kColS + N;
-    static constexpr uint32_t kCols = 256;
+    // operands and scores in flight, in tensor memory: 256 columns for each of two CTAs, or 512
+    static constexpr int KB = kCtas == 2 ? 1 : 2, VB = 2, SB = 64 * (KB + VB) + 3 * N <= (kCtas == 2 ? 256 : 512) ? 2 : 1;
+    static constexpr uint32_t kColK = 0, kColV = 64 * KB, kColS = kColV + 64 * VB, kColO = kColS + SB * N;
+    static constexpr uint32_t kCols = kCtas == 2 ? 256 : 512;
     static_assert(kColO + N <= kCols, "tensor memory");
+    static constexpr int PB = F32 ? 1 : 2;  // P buffers (of two parts for fp32 outputs)
     static constexpr int kQ = N * 256, kP = N * 256;
     static constexpr size_t smem(int stages, int R) {
-        return 1024 + (size_t)stages * kPaStageBytes + kQ + kP * (F32 ? 2 : 1) + ((size_t)R + 1) * 4;
+        return 1024 + (size_t)stages * kPaStageBytes + 2 * kQ + 2 * kP + ((size_t)R + 1) * 4;
     }
+    // Registers: two CTAs of 480 threads leave 64 each; the K and V warps hand 16 of theirs to the
+    // softmax warps, 8 x 48 + 4 x 96 = 12 x 64.
+    static constexpr bool kSplit = kCtas == 2 && RP >= 16;
+    static_assert(!kSplit || (kThreads == 480 && kGroups == 1), "the register split is for this shape");
 };
 
 template <int RP, bool F32>
-__global__ void __launch_bounds__(kPaThreads, PaCfg<RP, F32>::kCtas)
+__global__ void __launch_bounds__(PaCfg<RP, F32>::kThreads, PaCfg<RP, F32>::kCtas)
 paged_attention_kernel(const __grid_constant__ PaArgs A) {
     using Cfg = PaCfg<RP, F32>;
-    constexpr int N = Cfg::N;
+    constexpr int N = Cfg::N, KB = Cfg::KB, VB = Cfg::VB, SB = Cfg::SB, RG = Cfg::RG, kThreads = Cfg::kThreads;
+    constexpr int kCopyWarp = 8 + 4 * Cfg::kGroups, kSWarp = kCopyWarp + 1, kOWarp = kCopyWarp + 2;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t s_bar[2 * kPaMaxStages + 9];
+    __shared__ __align__(8) uint64_t s_bar[2 * kPaMaxStages + 17 + kPaRing];
     __shared__ PaTileInfo s_info[kPaRing];
     __shared__ PaSeg s_seg[kPaRing];
     __shared__ __align__(16) float s_nref[RP], s_del[RP], s_fac[RP], s_sum[4][RP];
-    __shared__ int s_unset[1];  // whether a row has no reference yet (s_seen: each row's)
+    __shared__ int s_unset[Cfg::kGroups];  // whether a row has no reference yet (s_seen: each row's)
     __shared__ uint8_t s_seen[RP];
+    __shared__ int s_quit[Cfg::kGroups][2];  // a wait of the group gave up (tile parity)
     __shared__ int s_max[4][RP];
-    __shared__ int s_scan[kPaThreads / 32];
+    __shared__ int s_scan[kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ PaCtl s_ctl;
     uint8_t *const sm0 = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
-    uint8_t *const s_q = sm0 + A.stages * kPaStageBytes, *const s_p = s_q + Cfg::kQ;
-    int *const s_pre = reinterpret_cast<int *>(s_p + Cfg::kP * (F32 ? 2 : 1));
+    uint8_t *const s_q = sm0 + A.stages * kPaStageBytes, *const s_p = s_q + 2 * Cfg::kQ;
+    int *const s_pre = reinterpret_cast<int *>(s_p + 2 * Cfg::kP);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bar0 = smem_u32(s_bar);
-    const uint32_t b_full = bar0, b_empty = bar0 + 8 * kPaMaxStages, b_k = bar0 + 16 * kPaMaxStages;
-    const uint32_t b_s = b_k + 8, b_p = b_k + 16, b_pv = b_k + 24, b_end = b_k + 32;
-    const uint32_t b_v = b_k + 40, b_vfree = b_k + 56;  // one for each V buffer
+    // Barriers come in pairs where what they guard has two buffers; tile t uses number t mod 2.
+    const uint32_t b_full = bar0, b_empty = bar0 + 8 * kPaMaxStages;
+    // What S(t) waits for: the first half of K(t) and the columns of S(t - SB) read (b_s0), the second
+    // half (b_s1); what O(t) waits for: V(t) and P(t) (b_o).
+    const uint32_t b_s0 = bar0 + 16 * kPaMaxStages, b_s1 = b_s0 + 16, b_o = b_s0 + 32;
+    const uint32_t b_s = b_s0 + 48, b_pv = b_s0 + 64;             // S(t), O(t) complete
+    const uint32_t b_kfree = b_s0 + 80, b_vfree = b_s0 + 112;     // K (by buffer and half), V read
+    const uint32_t b_end = b_s0 + 128, b_seg = b_s0 + 136;        // segment descriptors (kPaRing of them)
 
     if (tid == 0) {
         for (int i = 0; i < A.stages; ++i) {
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 8);
         }
-        mbar_init(b_k, 4);
-        mbar_init(b_s, 1);
-        mbar_init(b_p, 4);
-        mbar_init(b_pv, 1);
-        mbar_init(b_end, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(b_v + 8 * i, 4);
+            mbar_init(b_s0 + 8 * i, 4 + 4 * Cfg::kGroups);
+            mbar_init(b_s1 + 8 * i, 4);
+            mbar_init(b_o + 8 * i, 4 + 4 * Cfg::kGroups);
+            mbar_init(b_s + 8 * i, 1);
+            mbar_init(b_pv + 8 * i, 1);
+            mbar_init(b_kfree + 16 * i, 1);
+            mbar_init(b_kfree + 16 * i + 8, 1);
             mbar_init(b_vfree + 8 * i, 1);
         }
+        mbar_init(b_end, 2);
+        for (int i = 0; i < kPaRing; ++i) mbar_init(b_seg + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid < kPaRing) {
         s_info[tid] = PaTileInfo{};
         s_seg[tid] = PaSeg{};
+        if (tid < 2 * Cfg::kGroups) s_quit[tid >> 1][tid & 1] = 0;
     }
     griddep_wait();
     griddep_launch_dependents();
 
     // Tiles before every request.
+    const uint32_t lim = tid ? 0u : reinterpret_cast<volatile uint32_t *>(A.status)[1];
     int n_tiles = 0;
-    for (int r0 = 0; r0 < A.R; r0 += kPaThreads) {
+    for (int r0 = 0; r0 < A.R; r0 += kThreads) {
         const int r = r0 + tid;
         int mine = 0;
         if (r < A.R) {
@@ -307,7 +337,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         __syncthreads();
         int all = 0;
 #pragma unroll
-        for (int w = 0; w < kPaThreads / 32; ++w) {
+        for (int w = 0; w < kThreads / 32; ++w) {
             const int y = s_scan[w];
             if (w < warp) v += y;
             all += y;
@@ -318,16 +348,15 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
     if (tid == 0) {
         s_pre[A.R] = n_tiles;
         s_ctl.stop = 0u;
-        const uint32_t lim = reinterpret_cast<volatile uint32_t *>(A.status)[1];
-        s_ctl.limit = lim ? lim - 1u : kDefaultPolls;
+        s_ctl.limit = lim ? lim - 1u : kPaPolls;
         s_ctl.status = A.status;
     }
     __syncthreads();
     if (blockIdx.x == 0)
-        for (int r = tid; r <= A.R; r += kPaThreads) A.prefix[r] = s_pre[r];
+        for (int r = tid; r <= A.R; r += kThreads) A.prefix[r] = s_pre[r];
     const int lo = pa_lo(n_tiles, gridDim.x, blockIdx.x), hi = pa_lo(n_tiles, gridDim.x, blockIdx.x + 1);
-    const int count = hi - lo;
-    if (n_tiles == 0 || count <= 0) return;
+    if (n_tiles == 0 || hi <= lo) return;
+    const uint32_t count = hi - lo;
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
@@ -341,7 +370,11 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
     const uint32_t tmem = s_tmem;
     const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
 
-    if (warp == 8) {
+    constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    // Tile t's phase of a barrier that counts the tiles of one of two buffers, or of n.
+    auto phase = [](uint32_t t, uint32_t n) { return (t / n) & 1u; };
+
+    if (warp == kCopyWarp) {
         // ---- copies: lane j < 8 brings unit j of each tile ---------------------------------
         // Descriptors of tile t (and its segment) go into ring entry t mod 8.  The slowest reader
         // is at tile t - 6 at most: a stage is refilled after both dequantisations of its tile, and
@@ -355,7 +388,8 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             }
             r = a;
         }
-        int u = lo, k = 0, n_seg = 0;
+        int u = lo, k = 0, n_seg = 0, st = 0;
+        uint32_t st_phase = 0;
         PaReq x = pa_req(A, r);
         int head_tiles = pa_head_tiles<RP>(A, x);
         while (u < hi) {
@@ -386,18 +420,22 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                 g.tok = g.row0 / A.G;
                 g.off = g.row0 - g.tok * A.G;
                 s_seg[si] = g;
+                pa_arrive(b_seg + 8 * si);
             }
+            const int upp = A.page / kPgUnitPos;
+            // j / upp for j < 2^28 (upp <= 16)
+            auto page_of = [&](int j) { return upp == 1 ? j : (int)__umulhi((uint32_t)j, A.upp_magic); };
             const int32_t *const row = A.table + (int64_t)r * A.width;
             auto lookup = [&](int tile) -> int {
-                const int p = (tile * kPaTileUnits + lane) * kPgUnitPos;
-                return lane < kPaTileUnits && p < x.len ? row[p / A.page] : -1;
+                const int j = tile * kPaTileUnits + lane;
+                return lane < kPaTileUnits && j * kPgUnitPos < x.len ? row[page_of(j)] : -1;
             };
             int pg = lookup(u - s0);
             for (; u < end; ++u, ++k) {
-                const int tile = u - s0, st = k % A.stages;
+                const int tile = u - s0;
                 const int pg_next = u + 1 < end ? lookup(tile + 1) : -1;
                 // a wait that gave up ends the copies: no descriptor in use is overwritten
-                if (k >= A.stages && !pa_wait(b_empty + 8 * st, (uint32_t)(k / A.stages - 1) & 1u, &s_ctl)) {
+                if (k >= A.stages && !pa_wait(b_empty + 8 * st, st_phase ^ 1u, &s_ctl)) {
                     end = u = hi;
                     break;
                 }
@@ -415,12 +453,16 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                 }
                 __syncwarp();
                 if (ok) {
-                    const int unit = (tile * kPaTileUnits + lane) % (A.page / kPgUnitPos);
+                    const int j = tile * kPaTileUnits + lane, unit = j - page_of(j) * upp;
                     bulk_g2s(smem_u32(sm0 + st * kPaStageBytes + lane * kPgUnitBytes),
-                             A.pages + (((int64_t)pg * A.Hkv + h) * (A.page / kPgUnitPos) + unit) * kPgUnitBytes,
+                             A.pages + (((int64_t)pg * A.Hkv + h) * upp + unit) * kPgUnitBytes,
                              kPgUnitBytes, b_full + 8 * st);
                 }
                 pg = pg_next;
+                if (++st == A.stages) {
+                    st = 0;
+                    st_phase ^= 1u;
+                }
             }
             ++n_seg;
         }
@@ -429,39 +471,52 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             for (int j = max(0, k - A.stages); j < k; ++j)
                 mbar_wait_ok(b_full + 8 * (j % A.stages), (uint32_t)(j / A.stages) & 1u);
         __syncwarp();
-    } else if (warp == 9) {
-        // ---- MMAs: S of tile t + 1 before O of tile t --------------------------------------
-        constexpr uint32_t kId = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
-        const uint32_t qa = smem_u32(s_q), pa = smem_u32(s_p);
-        auto issue_s = [&](int t) {
-            pa_wait(b_k, (uint32_t)t & 1u, &s_ctl);
-            if (lane == 0) {
-                pa_fence_after();
+    } else if (warp == kSWarp) {
+        // ---- S = K Q^T ---------------------------------------------------------------------
+        const uint64_t q0 = pa_desc_q(smem_u32(s_q));
+        for (uint32_t t = 0; t < count; ++t) {
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    pa_mma(tmem + Cfg::kColS, tmem + Cfg::kColK + 8 * s,
-                           pa_desc_q(qa + (s >> 2) * (N * 128) + (s & 3) * 32), kId, s ? 1u : 0u);
-                pa_commit(b_s);
+            for (int half = 0; half < 2; ++half) {
+                pa_wait((half ? b_s1 : b_s0) + 8 * (t % SB), phase(t, SB), &s_ctl);
+                const uint32_t qb = (s_info[t % kPaRing].flags >> 2) & 1u;
+                if (lane == 0) {
+                    pa_fence_after();
+                    const uint64_t q = q0 + (qb * Cfg::kQ + half * (N * 128)) / 16;
+                    const uint32_t d = tmem + Cfg::kColS + N * (t % SB);
+                    const uint32_t ka = tmem + Cfg::kColK + 64 * (t % KB) + 32 * half;
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) pa_mma(d, ka + 8 * s, q + 2 * s, kIdesc, s || half ? 1u : 0u);
+                    pa_commit(b_kfree + 16 * (t % KB) + 8 * half);
+                    if (half) pa_commit(b_s + 8 * (t % SB));
+                }
+                __syncwarp();
             }
-            __syncwarp();
-        };
-        issue_s(0);
-        for (int t = 0; t < count; ++t) {
-            if (t + 1 < count) issue_s(t + 1);
+        }
+        if (lane == 0) {
+            pa_commit(b_end);
+            mbar_wait_ok(b_end, 0u);
+        }
+        __syncwarp();
+    } else if (warp == kOWarp) {
+        // ---- O += V^T P^T ------------------------------------------------------------------
+        const uint64_t p0 = pa_desc_p(smem_u32(s_p));
+        for (uint32_t t = 0; t < count; ++t) {
+            pa_wait(b_o + 8 * (t & 1), phase(t, 2), &s_ctl);
             const uint32_t first = s_info[t % kPaRing].flags & 1u;
-            pa_wait(b_p, (uint32_t)t & 1u, &s_ctl);
-            pa_wait(b_v + 8 * (t % Cfg::kVBufs), (uint32_t)(t / Cfg::kVBufs) & 1u, &s_ctl);
             if (lane == 0) {
                 pa_fence_after();
-                const uint32_t va = tmem + Cfg::kColV + 64 * (t % Cfg::kVBufs);
+                const uint32_t va = tmem + Cfg::kColV + 64 * (t % VB);
 #pragma unroll
-                for (int part = 0; part < (F32 ? 2 : 1); ++part)
+                for (int part = 0; part < (F32 ? 2 : 1); ++part) {
+                    // the small part first, so that fewer bits of it fall off
+                    const uint64_t pb = p0 + (F32 ? 1 - part : t % Cfg::PB) * (Cfg::kP / 16);
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        pa_mma(tmem + Cfg::kColO, va + 8 * s, pa_desc_p(pa + (F32 ? 1 - part : 0) * Cfg::kP + s * 256),
-                               kId | (1u << 16), s || part || (!F32 && !first) ? 1u : 0u);
-                pa_commit(b_pv);
-                pa_commit(b_vfree + 8 * (t % Cfg::kVBufs));
+                        pa_mma(tmem + Cfg::kColO, va + 8 * s, pb + 16 * s, kIdesc | (1u << 16),
+                               s || part || (!F32 && !first) ? 1u : 0u);
+                }
+                pa_commit(b_pv + 8 * (t & 1));
+                pa_commit(b_vfree + 8 * (t % VB));
             }
             __syncwarp();
         }
@@ -470,7 +525,8 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             mbar_wait_ok(b_end, 0u);
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
+        if (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         // ---- V: lane = dimension, columns of two positions ---------------------------------
         const int dim = tid - 128;
         // low nibbles: (1024 + c) - 1032; high ones: (1024 + 16 c) / 16 - 72; both c - 8 exactly
@@ -478,14 +534,15 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         const uint32_t mul = dim < 64 ? 0x3C003C00u : 0x2C002C00u, add = dim < 64 ? 0xE408E408u : 0xD480D480u;
         const uint8_t *const vrow = sm0 + kPgVCodes + (dim & 63) * 16;
         const uint8_t *const vsc = sm0 + kPgVScales + (warp & 3) * 32;
-        for (int t = 0; t < count; ++t) {
-            const int st = t % A.stages;
-            pa_wait(b_full + 8 * st, (uint32_t)(t / A.stages) & 1u, &s_ctl);
+        int st = 0;
+        uint32_t st_phase = 0;
+        for (uint32_t t = 0; t < count; ++t) {
+            pa_wait(b_full + 8 * st, st_phase, &s_ctl);
             const uint32_t mask = s_info[t % kPaRing].mask;
             const int n_pos = s_info[t % kPaRing].n_pos;
             const bool whole = mask == 0xFFu && n_pos >= kPaTile;
-            const int vb = t % Cfg::kVBufs;
-            if (t >= Cfg::kVBufs) pa_wait(b_vfree + 8 * vb, (uint32_t)(t / Cfg::kVBufs - 1) & 1u, &s_ctl);
+            const int vb = t % VB;
+            if (t >= VB) pa_wait(b_vfree + 8 * vb, phase(t - VB, VB), &s_ctl);
             pa_fence_after();
             const uint32_t col = tmem + quarter + Cfg::kColV + 64 * vb;
 #pragma unroll 2
@@ -515,18 +572,31 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             __syncwarp();
             if (lane == 0) {
                 pa_arrive(b_empty + 8 * st);
-                pa_arrive(b_v + 8 * vb);
+                pa_arrive(b_o + 8 * (t & 1));
+            }
+            if (++st == A.stages) {
+                st = 0;
+                st_phase ^= 1u;
             }
         }
-    } else {
-        // ---- K and the softmax: lane = position --------------------------------------------
-        const float c = A.c;
-        auto put_k = [&](int t) {
-            const int st = t % A.stages;
-            pa_wait(b_full + 8 * st, (uint32_t)(t / A.stages) & 1u, &s_ctl);
-            const uint32_t flags = s_info[t % kPaRing].flags;
-            if (flags & 1u) {  // a new segment: its query rows (the S products so far are done)
-                const PaSeg g = s_seg[flags >> 2];
+    } else if (warp < 4) {
+        // ---- K: lane = position, columns of two dimensions ---------------------------------
+        if (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        int st = 0;
+        uint32_t st_phase = 0, n_seg = 0;
+        bool fresh = true;
+        for (uint32_t t = 0; t < count; ++t) {
+            const int kb = t % KB;
+            if (t >= KB) pa_wait(b_kfree + 16 * kb, phase(t - KB, KB), &s_ctl);
+            if (fresh) {  // a new segment: its query rows
+                // (with S(t - KB) complete, and all before it, the buffer of the segment before the last
+                // is free)
+                if (t >= KB) pa_wait(b_kfree + 16 * kb + 8, phase(t - KB, KB), &s_ctl);
+                const uint32_t si = n_seg % kPaRing;
+                pa_wait(b_seg + 8 * si, phase(n_seg, kPaRing), &s_ctl);
+                const PaSeg g = s_seg[si];
+                uint8_t *const q = s_q + (si & 1u) * Cfg::kQ;
+                ++n_seg;
                 for (int i = tid; i < RP * 16; i += 128) {
                     const int row = i >> 4, ch = i & 15;
                     uint4 o = {0u, 0u, 0u, 0u};
@@ -545,95 +615,120 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                         }
                         o = make_uint4(r4[0], r4[1], r4[2], r4[3]);
                     }
-                    *reinterpret_cast<uint4 *>(s_q + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) * 16)) = o;
+                    *reinterpret_cast<uint4 *>(q + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) * 16)) = o;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
+            pa_wait(b_full + 8 * st, st_phase, &s_ctl);
+            pa_fence_after();
+            fresh = (s_info[t % kPaRing].flags & 2u) != 0u;
             const uint8_t *const unit = sm0 + st * kPaStageBytes + (tid >> 4) * kPgUnitBytes;
             const uint2 sc = *reinterpret_cast<const uint2 *>(unit + kPgKScales + (lane & 15) * 8);
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(unit + b * 256 + (lane & 15) * 16);
-                const uint32_t s1 = b < 2 ? sc.x : sc.y;
-                const uint32_t d = __byte_perm(s1, s1, b & 1 ? 0x3232 : 0x1010);
-                const uint32_t d8 = pa_h2mul(d, 0x30003000u), d3 = pa_h2mul(d, 0xC200C200u);  // d / 8, -3 d
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            for (int h = 0; h < 2; ++h) {
+                if (h && t >= KB) {
+                    pa_wait(b_kfree + 16 * kb + 8, phase(t - KB, KB), &s_ctl);
+                    pa_fence_after();
+                }
+                const uint32_t s1 = h ? sc.y : sc.x;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t o[8];
+                for (int b = 0; b < 2; ++b) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(unit + h * 512 + b * 256 + (lane & 15) * 16);
+                    const uint32_t d = __byte_perm(s1, s1, b ? 0x3232 : 0x1010);
+                    const uint32_t d8 = pa_h2mul(d, 0x30003000u), d3 = pa_h2mul(d, 0xC200C200u);  // d / 8, -3 d
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t y = ww[2 * half + i];
-                        o[4 * i + 0] = pa_h2fma(pa_16plus(y << 6), d8, d3);
-                        o[4 * i + 1] = pa_h2fma(pa_16plus(y << 2), d8, d3);
-                        o[4 * i + 2] = pa_h2fma(pa_16plus(y >> 2), d8, d3);
-                        o[4 * i + 3] = pa_h2fma(pa_16plus(y >> 6), d8, d3);
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t y = ww[2 * half + i];
+                            o[4 * i + 0] = pa_h2fma(pa_16plus(y << 6), d8, d3);
+                            o[4 * i + 1] = pa_h2fma(pa_16plus(y << 2), d8, d3);
+                            o[4 * i + 2] = pa_h2fma(pa_16plus(y >> 2), d8, d3);
+                            o[4 * i + 3] = pa_h2fma(pa_16plus(y >> 6), d8, d3);
+                        }
+                        pa_st8(tmem + quarter + Cfg::kColK + 64 * kb + 32 * h + 16 * b + 8 * half, o);
                     }
-                    pa_st8(tmem + quarter + Cfg::kColK + 16 * b + 8 * half, o);
+                }
+                pa_wait_st();
+                pa_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (h) pa_arrive(b_empty + 8 * st);
+                    pa_arrive((h ? b_s1 : b_s0) + 8 * (t % SB));
                 }
             }
-            pa_wait_st();
-            pa_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                pa_arrive(b_empty + 8 * st);
-                pa_arrive(b_k);
+            if (++st == A.stages) {
+                st = 0;
+                st_phase ^= 1u;
             }
-        };
-        auto group_sync = [&]() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); };
+        }
+    } else {
+        // ---- softmax: lane = position, rows rb .. rb + RG - 1 of the row tile --------------
+        if (Cfg::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        const int sg = (warp - 8) >> 2, rb = sg * RG, gt = (tid & 127), gw = warp & 3;
+        const float c = A.c;
+        auto group_sync = [&]() { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + sg) : "memory"); };
 
         // l: sums of p over this lane's positions.  acc (fp32 outputs): o, added up here tile by tile,
         // since the tensor core truncates what it adds to its accumulators (2^-24 a time).
-        f2 l[RP / 2], acc[F32 ? RP / 2 : 1];
+        int pos0 = 0, off0 = 0, whole_to = 0, len = 0;  // of the segment
+        f2 l[RG / 2], acc[F32 ? RG / 2 : 1];
         const f2 c2 = pa_f2(c, c);
-        put_k(0);
-        for (int t = 0; t < count; ++t) {
+        if (lane == 0)  // the first SB tiles find their S columns free
+            for (int i = 0; i < SB; ++i) pa_arrive(b_s0 + 8 * i);
+        for (uint32_t t = 0; t < count; ++t) {
+            f2 s[RG / 2];
+            // A wait that gave up must not let the group's threads disagree on what comes next: the
+            // vote below carries it, and then all of them leave.
+            if (!pa_wait(b_s + 8 * (t % SB), phase(t, SB), &s_ctl)) s_quit[sg][t & 1] = 1;
             const PaTileInfo ti = s_info[t % kPaRing];
             const bool first = ti.flags & 1u, last = ti.flags & 2u;
             const PaSeg &g = s_seg[ti.flags >> 2];
-            f2 s[RP / 2];
-            pa_wait(b_s, (uint32_t)t & 1u, &s_ctl);
+            if (first) {
+                pos0 = g.base + g.tok;
+                off0 = g.off + rb;
+                whole_to = min(pos0 + 1, g.len);
+                len = g.len;
+            }
             pa_fence_after();
             {
-                float f[RP];
+                float f[RG];
 #pragma unroll
-                for (int j = 0; j < RP; j += 8) pa_ld8(tmem + quarter + Cfg::kColS + j, f + j);
+                for (int j = 0; j < RG; j += 8) pa_ld8(tmem + quarter + Cfg::kColS + N * (t % SB) + rb + j, f + j);
                 pa_wait_ld();
 #pragma unroll
-                for (int j = 0; j < RP / 2; ++j) s[j] = pa_f2(f[2 * j], f[2 * j + 1]);
+                for (int j = 0; j < RG / 2; ++j) s[j] = pa_f2(f[2 * j], f[2 * j + 1]);
             }
             pa_fence_before();
-            if (t + 1 < count) put_k(t + 1);
+            __syncwarp();
+            if (lane == 0) pa_arrive(b_s0 + 8 * (t % SB));
 
             if (first) {
-                if (tid < RP) {
-                    s_nref[tid] = 0.f;
-                    s_seen[tid] = 0;
-                }
-                if (tid == 0) s_unset[0] = 1;
 #pragma unroll
-                for (int j = 0; j < RP / 2; ++j) l[j] = 0ull;
+                for (int j = 0; j < RG / 2; ++j) l[j] = 0ull;
                 if (F32) {
 #pragma unroll
-                    for (int j = 0; j < RP / 2; ++j) acc[j] = 0ull;
+                    for (int j = 0; j < RG / 2; ++j) acc[j] = 0ull;
                 }
-                group_sync();
             }
             // s = score - reference, in powers of two.
 #pragma unroll
-            for (int j = 0; j < RP / 2; j += 2) {
-                const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_nref + 2 * j);
+            for (int j = 0; j < RG / 2; j += 2) {
+                ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_nref + rb + 2 * j);
+                if (first) r.x = r.y = 0ull;
                 s[j] = pa_fma2(s[j], c2, r.x);
                 s[j + 1] = pa_fma2(s[j + 1], c2, r.y);
             }
             // What a row does not see is cut out (its first row sees the fewest positions).
-            const int pos = ti.tile * kPaTile + tid, see0 = g.base + g.tok + 1;
-            if (ti.mask != 0xFFu || ti.tile * kPaTile + kPaTile > min(see0, g.len)) {
-                const bool here = ((ti.mask >> (tid >> 4)) & 1u) && pos < g.len;
+            if (ti.mask != 0xFFu || (ti.tile + 1) * kPaTile > whole_to) {
+                const int pos = ti.tile * kPaTile + gt;
+                const bool here = ((ti.mask >> (gt >> 4)) & 1u) && pos < len;
                 // row j is token tok + (off + j) / G: it sees the position once j reaches this
-                const int from = here ? (pos - (g.base + g.tok)) * A.G - g.off : RP;
+                const int from = here ? (pos - pos0) * A.G - off0 : RG;
 #pragma unroll
-                for (int j = 0; j < RP / 2; ++j) {
+                for (int j = 0; j < RG / 2; ++j) {
                     float2 v = pa_un2(s[j]);
                     if (2 * j < from) v.x = -INFINITY;
                     if (2 * j + 1 < from) v.y = -INFINITY;
@@ -642,83 +737,86 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             }
             float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < RP / 2; ++j) {
+            for (int j = 0; j < RG / 2; ++j) {
                 const float2 v = pa_un2(s[j]);
                 top = fmaxf(fmaxf(top, v.x), v.y);
             }
             uint32_t any;
             asm volatile(
-                "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+                "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
                 : "=r"(any)
-                : "r"((uint32_t)(top > kPaOver || s_unset[0] != 0))
+                : "r"((uint32_t)(first || top > kPaOver || s_unset[sg] != 0)), "r"(1 + sg)
                 : "memory");
+            if (s_quit[sg][t & 1]) break;
             if (any) {
                 // New references, 7 below the largest score, for rows without one and for those that
                 // a score exceeds by more than 15.
 #pragma unroll
-                for (int j = 0; j < RP / 2; ++j) {
+                for (int j = 0; j < RG / 2; ++j) {
                     const float2 v = pa_un2(s[j]);
                     const int m0 = __reduce_max_sync(~0u, pa_order(v.x)), m1 = __reduce_max_sync(~0u, pa_order(v.y));
                     if (lane == 0) {
-                        s_max[warp][2 * j] = m0;
-                        s_max[warp][2 * j + 1] = m1;
+                        s_max[gw][rb + 2 * j] = m0;
+                        s_max[gw][rb + 2 * j + 1] = m1;
                     }
                 }
-                if (tid == 0) s_unset[0] = 0;
+                if (gt == 0) s_unset[sg] = 0;
                 group_sync();
-                if (tid < RP) {
+                if (gt < RG) {
                     const float m =
-                        pa_unorder(max(max(s_max[0][tid], s_max[1][tid]), max(s_max[2][tid], s_max[3][tid])));
-                    const bool set = s_seen[tid];
-                    float del = 0.f, old = s_nref[tid];
+                        pa_unorder(max(max(s_max[0][rb + gt], s_max[1][rb + gt]), max(s_max[2][rb + gt], s_max[3][rb + gt])));
+                    const bool set = !first && s_seen[rb + gt];
+                    const float old = first ? 0.f : s_nref[rb + gt];
+                    float del = 0.f, now = old;
+                    bool seen = set;
                     if (m != -INFINITY && (!set || !(m <= kPaOver))) {
-                        const float now = old + (kPaUnder - m);
+                        now = old + (kPaUnder - m);
                         del = now - old;
-                        s_nref[tid] = now;
-                        s_seen[tid] = 1;
-                    } else if (!set) {
-                        s_unset[0] = 1;
+                        seen = true;
                     }
-                    s_del[tid] = del;
-                    s_fac[tid] = set ? pa_ex2(del) : 1.f;
+                    if (!seen) s_unset[sg] = 1;
+                    s_nref[rb + gt] = now;
+                    s_seen[rb + gt] = seen;
+                    s_del[rb + gt] = del;
+                    s_fac[rb + gt] = set ? pa_ex2(del) : 1.f;
                 }
                 group_sync();
 #pragma unroll
-                for (int j = 0; j < RP / 2; j += 2) {
-                    const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_del + 2 * j);
+                for (int j = 0; j < RG / 2; j += 2) {
+                    const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_del + rb + 2 * j);
                     s[j] = pa_add2(s[j], r.x);
                     s[j + 1] = pa_add2(s[j + 1], r.y);
                 }
                 if (!first) {
 #pragma unroll
-                    for (int j = 0; j < RP / 2; ++j) {
-                        const f2 f = *reinterpret_cast<const f2 *>(s_fac + 2 * j);
+                    for (int j = 0; j < RG / 2; ++j) {
+                        const f2 f = *reinterpret_cast<const f2 *>(s_fac + rb + 2 * j);
                         l[j] = pa_mul2(l[j], f);
                     }
                     if (!F32) {
-                        pa_wait(b_pv, (uint32_t)(t - 1) & 1u, &s_ctl);
+                        pa_wait(b_pv + 8 * ((t - 1) & 1), phase(t - 1, 2), &s_ctl);
                         pa_fence_after();
 #pragma unroll
-                        for (int j = 0; j < RP; j += 8) {
+                        for (int j = 0; j < RG; j += 8) {
                             float o[8];
-                            pa_ld8(tmem + quarter + Cfg::kColO + j, o);
+                            pa_ld8(tmem + quarter + Cfg::kColO + rb + j, o);
                             pa_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] *= s_fac[j + i];
-                            pa_st8(tmem + quarter + Cfg::kColO + j, reinterpret_cast<const uint32_t *>(o));
+                            for (int i = 0; i < 8; ++i) o[i] *= s_fac[rb + j + i];
+                            pa_st8(tmem + quarter + Cfg::kColO + rb + j, reinterpret_cast<const uint32_t *>(o));
                         }
                         pa_wait_st();
                         pa_fence_before();
                     }
                 }
             }
-            if (t > 0) pa_wait(b_pv, (uint32_t)(t - 1) & 1u, &s_ctl);  // P is read
+            if (t >= Cfg::PB) pa_wait(b_pv + 8 * ((t - Cfg::PB) & 1), phase(t - Cfg::PB, 2), &s_ctl);  // P is read
             if (F32 && !first) {
                 pa_fence_after();
 #pragma unroll
-                for (int j = 0; j < RP; j += 8) {
+                for (int j = 0; j < RG; j += 8) {
                     float o[8];
-                    pa_ld8(tmem + quarter + Cfg::kColO + j, o);
+                    pa_ld8(tmem + quarter + Cfg::kColO + rb + j, o);
                     pa_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j / 2 + i] = pa_add2(acc[j / 2 + i], pa_f2(o[2 * i], o[2 * i + 1]));
@@ -726,12 +824,12 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                 pa_fence_before();
                 if (any) {
 #pragma unroll
-                    for (int j = 0; j < RP / 2; ++j) acc[j] = pa_mul2(acc[j], *reinterpret_cast<const f2 *>(s_fac + 2 * j));
+                    for (int j = 0; j < RG / 2; ++j) acc[j] = pa_mul2(acc[j], *reinterpret_cast<const f2 *>(s_fac + rb + 2 * j));
                 }
             }
-            uint8_t *const prow = s_p + (tid >> 3) * 128 + (tid & 7) * 16;
+            uint8_t *const prow = s_p + (F32 ? 0 : t % Cfg::PB) * Cfg::kP + (gt >> 3) * 128 + (gt & 7) * 16 + (rb >> 3) * 2048;
 #pragma unroll
-            for (int j = 0; j < RP; j += 8) {
+            for (int j = 0; j < RG; j += 8) {
                 float p[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -755,57 +853,76 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) pa_arrive(b_p);
+            if (lane == 0) pa_arrive(b_o + 8 * (t & 1));
 
             if (last) {
-                // The segment's sums over positions, then o.
+                // The segment's sums over positions (each step of the exchange halves the rows a lane
+                // holds, so that lane i ends with row i), then o.
+                constexpr int RX = RG == 24 ? 32 : RG;
+                float v[RX];
 #pragma unroll
-                for (int j = 0; j < RP; ++j) {
-                    const float2 v2 = pa_un2(l[j / 2]);
-                    float v = j & 1 ? v2.y : v2.x;
+                for (int j = 0; j < RX; j += 2) {
+                    const float2 x = j < RG ? pa_un2(l[j / 2 < RG / 2 ? j / 2 : 0]) : make_float2(0.f, 0.f);
+                    v[j] = x.x;
+                    v[j + 1] = x.y;
+                }
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-                    if (lane == 0) s_sum[warp][j] = v;
+                for (int o = 16; o; o >>= 1) {
+                    if (o >= RX) {
+#pragma unroll
+                        for (int j = 0; j < RX; ++j) v[j] += __shfl_xor_sync(~0u, v[j], o);
+                    } else {
+                        const bool up = lane & o;
+#pragma unroll
+                        for (int j = 0; j < o; ++j) {
+                            const float send = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
+                            v[j] = keep + __shfl_xor_sync(~0u, send, o);
+                        }
+                    }
+                }
+                if (lane < RG) s_sum[gw][rb + lane] = v[0];
+                group_sync();
+                const int slot = g.slot, rows = g.rows;
+                if (gt < RG) {
+                    const int row = rb + gt, rr = g.row0 + row, tok = rr / A.G;
+                    const float sum = s_sum[0][row] + s_sum[1][row] + s_sum[2][row] + s_sum[3][row];
+                    const bool seen = s_seen[row];
+                    s_fac[row] = seen ? 1.f / sum : 0.f;
+                    s_max[0][row] = (g.token0 + tok) * A.Hq + g.head0 + rr - tok * A.G;
+                    if (slot >= 0 && row < rows)
+                        A.part_ml[(int64_t)slot * RP + row] = make_float2(seen ? -s_nref[row] : -INFINITY, sum);
                 }
                 group_sync();
-                pa_wait(b_pv, (uint32_t)t & 1u, &s_ctl);
+                pa_wait(b_pv + 8 * (t & 1), phase(t, 2), &s_ctl);
                 pa_fence_after();
-                const int slot = g.slot, rows = g.rows;
+                float o[RG];
 #pragma unroll
-                for (int j = 0; j < RP; j += 8) {
-                    float o[8];
-                    pa_ld8(tmem + quarter + Cfg::kColO + j, o);
-                    pa_wait_ld();
-                    if (F32) {
+                for (int j = 0; j < RG; j += 8) pa_ld8(tmem + quarter + Cfg::kColO + rb + j, o + j);
+                pa_wait_ld();
+                if (F32) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 v = pa_un2(acc[j / 2 + i]);
-                            o[2 * i] += v.x;
-                            o[2 * i + 1] += v.y;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = j + i;
-                        if (row < rows) {
-                            const float sum = s_sum[0][row] + s_sum[1][row] + s_sum[2][row] + s_sum[3][row];
-                            if (slot < 0) {
-                                const int rr = g.row0 + row, tok = rr / A.G;
-                                const int64_t at =
-                                    ((int64_t)(g.token0 + tok) * A.Hq + g.head0 + rr - tok * A.G) * kPgDim + tid;
-                                const float y = s_seen[row] ? o[i] / sum : 0.f;
-                                if (F32) reinterpret_cast<float *>(A.out)[at] = y;
-                                else reinterpret_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16_rn(y);
-                            } else {
-                                A.part[((int64_t)slot * RP + row) * kPgDim + tid] = o[i];
-                                if (tid == 0) A.part_ml[(int64_t)slot * RP + row] =
-                                                  make_float2(s_seen[row] ? -s_nref[row] : -INFINITY, sum);
-                            }
-                        }
+                    for (int j = 0; j < RG / 2; ++j) {
+                        const float2 x = pa_un2(acc[j]);
+                        o[2 * j] += x.x;
+                        o[2 * j + 1] += x.y;
                     }
                 }
-                pa_fence_before();
-                group_sync();  // s_nref, s_sum and the O columns are free again
+                if (slot >= 0) {
+                    float *const to = A.part + ((int64_t)slot * RP + rb) * kPgDim + gt;
+#pragma unroll
+                    for (int j = 0; j < RG; ++j)
+                        if (rb + j < rows) to[j * kPgDim] = o[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < RG; ++j)
+                        if (rb + j < rows) {
+                            const int64_t at = (int64_t)s_max[0][rb + j] * kPgDim + gt;
+                            const float f = s_fac[rb + j], y = f == 0.f ? 0.f : o[j] * f;
+                            if (F32) reinterpret_cast<float *>(A.out)[at] = y;
+                            else reinterpret_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16_rn(y);
+                        }
+                }
+                pa_fence_before();  // (the next tile's vote comes before anything read here is written again)
             }
         }
     }
@@ -816,67 +933,78 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Cfg::kCols) : "memory");
 }
 
-// Joins the segments of a row that several CTAs hold: one warp per (token, query head).
-template <int RP, bool F32>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PaArgs A, int ctas) {
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    griddep_wait();
+// Joins the segments of a row that several CTAs hold: W warps per (token, query head), each over
+// every W-th segment, all of its loads in flight together.  What the requests' lengths alone decide
+// is worked out before the main kernel's end is waited for (the lengths were complete before it began).
+template <int RP, bool F32, int W>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) paged_merge_kernel(const __grid_constant__ PaArgs A, int ctas) {
+    constexpr int kRows = W == 1 ? 4 : 1;  // rows of a CTA
+    __shared__ float4 s_acc[W][32];
+    __shared__ float2 s_ml[W];
+    const int lane = threadIdx.x & 31, wj = W == 1 ? 0 : threadIdx.x >> 5;
+    const int64_t w = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x >> 5 : 0);
     const int t = (int)(w / A.Hq), head = (int)(w - (int64_t)t * A.Hq);
-    if (t >= A.T || t >= A.q_start[A.R]) return;
-    const int n_tiles = A.prefix[A.R];
-    if (n_tiles == 0) return;
     int r = 0, b = A.R;
+    const bool there = t < A.T && t < A.q_start[A.R];
     while (b - r > 1) {
         const int mid = (r + b) >> 1;
         if (A.q_start[mid] <= t) r = mid; else b = mid;
     }
     const PaReq x = pa_req(A, r);
     const int i = t - x.q0;
-    if (i < 0 || i >= x.n) return;
     const int h = head / A.G, rr = i * A.G + head - h * A.G, rt = rr / RP, row = rr - rt * RP;
-    int before = 0;
-    for (int j = 0; j < rt; ++j) before += pa_row_tiles<RP>(A, x, j);
-    const int nt = pa_row_tiles<RP>(A, x, rt);
-    const int per = (A.prefix[r + 1] - A.prefix[r]) / A.Hkv;
-    const int s0 = A.prefix[r] + h * per + before;
+    int before = 0, nt = 0;
+    const bool mine = there && i >= 0 && i < x.n;
+    if (mine) {
+        for (int j = 0; j < rt; ++j) before += pa_row_tiles<RP>(A, x, j);
+        nt = pa_row_tiles<RP>(A, x, rt);
+    }
+    griddep_wait();
+    if (!mine) return;  // (the same for all warps of a row)
+    const int n_tiles = A.prefix[A.R], pre = A.prefix[r], per = (A.prefix[r + 1] - pre) / A.Hkv;
+    if (n_tiles == 0) return;
+    const int s0 = pre + h * per + before;
     const int f = pa_cta_of(n_tiles, ctas, s0), e = pa_cta_of(n_tiles, ctas, s0 + nt - 1);
     if (f == e) return;
-    auto slot = [&](int c) { return (int64_t)(c == f ? 2 * f + 1 : 2 * c) * RP + row; };
-    float ref = -INFINITY;
-    bool nan = false;
-    for (int c = f + lane; c <= e; c += 32) {
-        const float2 ml = A.part_ml[slot(c)];
-        nan |= ml.x != ml.x;
-        ref = fmaxf(ref, ml.x);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(~0u, ref, o));
-    const bool empty = ref == -INFINITY && !__any_sync(~0u, nan);
-    float sum = 0.f;
+    // (ref, sum, acc) += (r, l, o), a part that saw nothing (r = -inf) left out.
+    float ref = -INFINITY, sum = 0.f;
     float4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int c0 = f; c0 <= e; c0 += 8) {
+    auto join = [&](float r1, float l1, const float4 &o1) {
+        if (r1 == -INFINITY) return;
+        const float top = ref > r1 ? ref : r1;  // (NaN: r1)
+        const float k0 = ref == -INFINITY ? 0.f : pa_ex2(ref - top), k1 = pa_ex2(r1 - top);
+        sum = sum * k0 + l1 * k1;
+        acc.x = acc.x * k0 + o1.x * k1;
+        acc.y = acc.y * k0 + o1.y * k1;
+        acc.z = acc.z * k0 + o1.z * k1;
+        acc.w = acc.w * k0 + o1.w * k1;
+        ref = top;
+    };
+    for (int c0 = f + wj; c0 <= e; c0 += 8 * W) {
         float4 o[8];
         float2 ml[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j <= e) {
-                ml[j] = A.part_ml[slot(c0 + j)];
-                o[j] = *reinterpret_cast<const float4 *>(A.part + slot(c0 + j) * kPgDim + 4 * lane);
+        for (int j = 0; j < 8; ++j) {
+            const int c = c0 + j * W;
+            ml[j] = make_float2(-INFINITY, 0.f);
+            if (c <= e) {
+                const int64_t slot = (int64_t)(c == f ? 2 * f + 1 : 2 * c) * RP + row;
+                ml[j] = A.part_ml[slot];
+                o[j] = *reinterpret_cast<const float4 *>(A.part + slot * kPgDim + 4 * lane);
             }
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j <= e) {
-                if (ml[j].x == -INFINITY) continue;  // saw nothing: its sums are zero
-                const float k = pa_ex2(ml[j].x - ref);
-                sum += ml[j].y * k;
-                acc.x += o[j].x * k;
-                acc.y += o[j].y * k;
-                acc.z += o[j].z * k;
-                acc.w += o[j].w * k;
-            }
+        for (int j = 0; j < 8; ++j) join(ml[j].x, ml[j].y, o[j]);
     }
-    const float inv = empty ? 0.f : 1.f / sum;
+    if (W > 1) {
+        s_acc[wj][lane] = acc;
+        if (lane == 0) s_ml[wj] = make_float2(ref, sum);
+        __syncthreads();
+        if (wj) return;
+#pragma unroll
+        for (int j = 1; j < W; ++j) join(s_ml[j].x, s_ml[j].y, s_acc[j][lane]);
+    }
+    const float inv = ref == -INFINITY ? 0.f : 1.f / sum;
     const int64_t at = w * kPgDim + 4 * lane;
     if (F32) {
         *reinterpret_cast<float4 *>(reinterpret_cast<float *>(A.out) + at) =
@@ -909,9 +1037,13 @@ static int pa_launch(PaArgs A, cudaStream_t stream) {
     const int grid = Cfg::kCtas * sm_count();
     SVD_CUDA_TRY(cudaFuncSetAttribute(paged_attention_kernel<RP, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       (int)smem));
-    SVD_CUDA_TRY(launch(paged_attention_kernel<RP, F32>, dim3(grid), dim3(kPaThreads), smem, stream, true, A));
-    const int64_t warps = (int64_t)A.T * A.Hq;
-    SVD_CUDA_TRY(launch(paged_merge_kernel<RP, F32>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, stream, true, A, grid));
+    SVD_CUDA_TRY(launch(paged_attention_kernel<RP, F32>, dim3(grid), dim3(Cfg::kThreads), smem, stream, true, A));
+    // Few rows are split over many CTAs each, and then eight warps join one; many rows over few.
+    const int64_t rows = (int64_t)A.T * A.Hq;
+    if (rows <= 2048)
+        SVD_CUDA_TRY(launch(paged_merge_kernel<RP, F32, 8>, dim3((unsigned)rows), dim3(256), 0, stream, true, A, grid));
+    else
+        SVD_CUDA_TRY(launch(paged_merge_kernel<RP, F32, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, true, A, grid));
     return SVD_OK;
 }
 
@@ -960,6 +1092,7 @@ int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32
     A.max_new = max_new;
     A.width = width;
     A.page = page;
+    A.upp_magic = (uint32_t)(((1ull << 32) + page / kPgUnitPos - 1) / (page / kPgUnitPos));
     A.Hq = Hq;
     A.Hkv = Hkv;
     A.G = G;
