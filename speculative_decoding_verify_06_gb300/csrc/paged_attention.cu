@@ -118,8 +118,7 @@ __device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity, PaCtl *c)
             atomicOr(c->status, 1u);
         }
     }
-    __syncwarp();
-    return ok;
+    return __all_sync(~0u, ok);  // one answer for the warp, which stays together
 }
 __device__ __forceinline__ void pa_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
