@@ -222,20 +222,21 @@ int paged_tables(const int32_t *held, const int32_t *window, const int32_t *emit
 //
 // Angles.  position * inv_freq reaches 10^6 radians; reduced in fp32 it would be off by 0.06.
 // The host turns each frequency into turns per position as a 64-bit fraction, so that one 64-bit
-// integer product gives the angle modulo a turn to 2^-33 turns for any 31-bit position, and cos
-// and sin of the remaining eighth of a turn are cheap in fp32 (absolute error below 2^-22).
+// integer product gives the angle modulo a turn to 2^-33 turns for any 31-bit position; cos and sin of
+// what is left come from a small table and one short turn, as sums of two floats.
 //
 // Codes.  A key next to the border of two codes must get the code that exact arithmetic gives, or
-// the cache would depend on how the angle was rounded.  Each fp32 key carries an error bound (0 for
-// values and for unrotated dimensions); when a block's scale or one of its codes could change
-// within it, the block's eight lanes redo it in fp64 with fp64 angles (about one block in 10^3).
-// Borders are (n - 8.5) d, exact in fp32 because d has eight significant bits, so a code is
-// settled by comparing against them and no division is rounded.
+// the cache would depend on how the angle was rounded.  Keys are therefore carried as sums of two
+// floats with an error bound of 2^-27 (|x_a| + |x_b|) (none for values and for unrotated dimensions);
+// where a block's scale or one of its codes could still change within it, about once in 10^4 key heads,
+// the warp redoes the head in fp64 from the same integer angle.  (With plain fp32 keys it was once
+// in 10^3, and a batch of 256 tokens waited 6 to 9 us for the one or two warps concerned.)  Borders are
+// (n - 8.5) d, exact in fp32 because d has eight significant bits, so a code is settled by comparing
+// against them and no division is rounded.
 constexpr int kApWarps = 8;
 
 struct RopeArgs {
     uint64_t phase[SVD_ROPE_MAX_PAIRS];  // turns per position, as a fraction of 2^64
-    double inv[SVD_ROPE_MAX_PAIRS];      // radians per position (the fp64 path)
     uint8_t axis[SVD_ROPE_MAX_PAIRS];
     int pairs, interleaved;
 };
@@ -253,14 +254,64 @@ struct ApArgs {
     RopeArgs rope;
 };
 
-__device__ __forceinline__ void ap_load4(const float *p, float x[4]) {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
+// Four values as they lie in memory, and as floats.
+__device__ __forceinline__ float4 ap_raw(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ uint2 ap_raw(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
+__device__ __forceinline__ void ap_floats(const float4 &v, float x[4]) {
     x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
-__device__ __forceinline__ void ap_load4(const __nv_bfloat16 *p, float x[4]) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+__device__ __forceinline__ void ap_floats(const uint2 &v, float x[4]) {
     x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
     x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+
+// Pair i's angle at token t, less the nearest multiple of a quarter turn (*quad): 2^-64 turns.
+__device__ __forceinline__ int64_t ap_phase(const ApArgs &A, int t, int i, uint32_t *quad) {
+    const int64_t pos = A.positions[A.rope.axis[i] * A.positions_ld + t];
+    const uint64_t ph = (uint64_t)pos * A.rope.phase[i], q = (ph + (1ull << 61)) >> 62;
+    *quad = (uint32_t)q;
+    return (int64_t)(ph - (q << 62));
+}
+
+// cos and sin of k / 256 turns (high and low parts), k = 0..32.
+__constant__ float4 kApTurn[33] = {
+    {1.0f, 0.0f, 0.0f, 0.0f}, {0.999698818f, 9.66254299e-10f, 0.024541229f, -4.86716001e-10f},
+    {0.99879545f, 6.47143805e-09f, 0.0490676761f, -1.73993431e-09f}, {0.997290432f, 2.42255354e-08f, 0.0735645667f, -3.07218095e-09f},
+    {0.99518472f, 7.10966619e-09f, 0.0980171412f, -8.93393193e-10f}, {0.992479563f, -2.81606898e-08f, 0.122410677f, -2.17419305e-09f},
+    {0.989176512f, -1.79974535e-09f, 0.146730468f, 6.77824552e-09f}, {0.985277653f, -1.03515374e-08f, 0.170961887f, 2.11593787e-09f},
+    {0.980785251f, 2.97394731e-08f, 0.195090324f, -1.67047143e-09f}, {0.975702107f, 2.30858621e-08f, 0.219101235f, 4.88636953e-09f},
+    {0.970031261f, -8.24954771e-09f, 0.242980182f, -2.2676041e-09f}, {0.963776052f, 1.37973011e-08f, 0.266712755f, 2.51006993e-09f},
+    {0.956940353f, -1.7184508e-08f, 0.290284663f, 1.38156651e-08f}, {0.949528158f, 2.28820074e-08f, 0.313681751f, -1.10907479e-08f},
+    {0.941544056f, 9.24430044e-09f, 0.336889863f, -9.62200097e-09f}, {0.932992816f, -1.71366352e-08f, 0.359895051f, -1.39906771e-08f},
+    {0.923879504f, 2.83074897e-08f, 0.382683426f, 6.22335072e-09f}, {0.914209783f, -2.73737086e-08f, 0.405241311f, 3.40852391e-09f},
+    {0.903989315f, -2.1909516e-08f, 0.427555084f, 9.20176646e-09f}, {0.893224299f, 2.2415052e-09f, 0.449611336f, -6.3382064e-09f},
+    {0.881921291f, -2.70029634e-08f, 0.471396744f, -7.42525375e-09f}, {0.870086968f, 2.31636132e-08f, 0.492898196f, -3.75219544e-09f},
+    {0.857728601f, 9.49825818e-09f, 0.514102757f, -1.27838593e-08f}, {0.84485358f, -1.47483092e-08f, 0.534997642f, -2.21531558e-08f},
+    {0.831469595f, 1.68702634e-08f, 0.555570245f, -1.17695214e-08f}, {0.817584813f, 5.10439913e-10f, 0.575808167f, 2.39602649e-08f},
+    {0.803207517f, 1.48104178e-08f, 0.59569931f, -5.81030113e-09f}, {0.78834641f, 1.78289383e-08f, 0.615231574f, 1.6998932e-08f},
+    {0.773010433f, 2.06425526e-08f, 0.634393275f, 9.37955758e-09f}, {0.757208824f, 2.23487699e-08f, 0.653172851f, -7.65504904e-09f},
+    {0.740951121f, 4.50153514e-09f, 0.671558976f, -2.13263824e-08f}, {0.724247098f, -1.5017589e-08f, 0.689540565f, -2.02768184e-08f},
+    {0.707106769f, 1.21016175e-08f, 0.707106769f, 1.21016175e-08f},
+};
+// cos and sin of the pair's angle as sums of two floats, to 2^-28: an entry of the table, turned by what
+// is left (at most a 512th of a turn), whose fp32 errors count for an 80th.
+__device__ __forceinline__ float4 ap_cos_sin(const ApArgs &A, int t, int i) {
+    uint32_t quad;
+    const int64_t r = ap_phase(A, t, i, &quad);
+    const int k = (int)((r + (1ll << 55)) >> 56);
+    const float a = __ll2float_rn(r - ((int64_t)k << 56)) * (6.283185307f * 0x1p-64f), z = a * a;
+    float4 e = kApTurn[k < 0 ? -k : k];
+    if (k < 0) { e.z = -e.z; e.w = -e.w; }
+    const float sa = a * fmaf(z, -1.f / 6.f, 1.f), ca = z * fmaf(z, 1.f / 24.f, -0.5f);  // sin a, cos a - 1
+    const float dc = fmaf(e.x, ca, -e.z * sa) + e.y, ds = fmaf(e.z, ca, e.x * sa) + e.w;
+    float4 o;
+    o.x = e.x + dc;
+    o.y = dc - (o.x - e.x);
+    o.z = e.z + ds;
+    o.w = fabsf(e.z) >= fabsf(ds) ? ds - (o.z - e.z) : e.z - (o.z - ds);
+    if (quad & 1) o = make_float4(-o.z, -o.w, o.x, o.y);
+    if (quad & 2) o = make_float4(-o.x, -o.y, -o.z, -o.w);
+    return o;
 }
 
 // d = round8(m / -8) as fp16 bits.
@@ -276,7 +327,7 @@ __device__ __forceinline__ uint16_t ap_scale(double m) {
 
 // The value of largest magnitude among the block's eight lanes (the lowest dimension on ties).
 template <typename F>
-__device__ __forceinline__ F ap_extreme(const F y[4], int lane, uint32_t mask) {
+__device__ __forceinline__ F ap_extreme(const F y[4], int lane) {
     F m = y[0];
     int at = 0;
 #pragma unroll
@@ -285,94 +336,184 @@ __device__ __forceinline__ F ap_extreme(const F y[4], int lane, uint32_t mask) {
     at += (lane & 7) * 4;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
-        const F om = __shfl_xor_sync(mask, m, o);
-        const int oa = __shfl_xor_sync(mask, at, o);
+        const F om = __shfl_xor_sync(~0u, m, o);
+        const int oa = __shfl_xor_sync(~0u, at, o);
         if (fabs(om) > fabs(m) || (fabs(om) == fabs(m) && oa < at)) { m = om; at = oa; }
     }
     return m;
 }
 
-// The four codes of a lane from keys in fp64, and the block's scale.
-__device__ __noinline__ uint32_t ap_block_f64(const ApArgs &A, int t, int d0, const float *xa4,
-                                              const float *xb4, int lane, uint32_t mask, uint16_t *scale) {
-    double y[4];
-    const int pairs = A.rope.pairs;
+// (Arguments and results of the two rare paths go by value: an array whose address is passed would
+// live in local memory on the common path too.)
+struct ApOut {
+    uint32_t codes, scale;
+};
+
+// Rotated keys in fp64, for a warp in which one is in doubt.  cos and sin of the reduced angle,
+// |x| <= pi / 4, by their Taylor series (the first terms left out are below 2^-58); the four pairs side
+// by side, since this GPU issues one fp64 instruction of a warp in sixteen cycles and what counts is
+// that they follow each other closely.  The whole path takes about 2 us, and a batch waits for it.
+__device__ __noinline__ ApOut ap_keys_f64(const ApArgs &A, int t, float4 xa, float4 xo, int lane) {
+    const float xa4[4] = {xa.x, xa.y, xa.z, xa.w}, xb4[4] = {xo.x, xo.y, xo.z, xo.w};
+    const int pairs = A.rope.pairs, d0 = 4 * lane;
+    const bool on = d0 < 2 * pairs, up = !A.rope.interleaved && d0 >= pairs;
+    double x[4], z[4], c[4], sn[4], y[4];
+    uint32_t quad[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int d = d0 + j;
-        double v = xa4[j];
-        if (d < 2 * pairs) {
-            const bool second = A.rope.interleaved ? (d & 1) : d >= pairs;
-            const int i = A.rope.interleaved ? d >> 1 : second ? d - pairs : d;
-            double s, c;
-            sincos((double)A.positions[A.rope.axis[i] * A.positions_ld + t] * A.rope.inv[i], &s, &c);
-            const double own = __dmul_rn(v, c), other = __dmul_rn((double)xb4[j], s);
-            v = second ? __dadd_rn(own, other) : __dsub_rn(own, other);
-        }
-        y[j] = fmin(fmax(v, -kPgMaxAbs), kPgMaxAbs);
+        const int i = A.rope.interleaved ? 2 * lane + (j >> 1) : d0 + j - (up ? pairs : 0);
+        x[j] = (double)(on ? ap_phase(A, t, i, &quad[j]) : 0) * (3.14159265358979323846 * 0x1p-63);
+        z[j] = x[j] * x[j];
+        c[j] = 1.0 / 20922789888000.0;   // 1 / 16!
+        sn[j] = 1.0 / 355687428096000.0;  // 1 / 17!
     }
-    const uint16_t db = ap_scale(ap_extreme(y, lane, mask));
-    const double d = (double)__half2float(__ushort_as_half(db));
+    const double fc[8] = {-1.0 / 87178291200.0, 1.0 / 479001600.0, -1.0 / 3628800.0, 1.0 / 40320.0, -1.0 / 720.0, 1.0 / 24.0, -0.5, 1.0};
+    const double fs[8] = {-1.0 / 1307674368000.0, 1.0 / 6227020800.0, -1.0 / 39916800.0, 1.0 / 362880.0, -1.0 / 5040.0,
+                          1.0 / 120.0, -1.0 / 6.0, 1.0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            c[j] = fma(c[j], z[j], fc[k]);
+            sn[j] = fma(sn[j], z[j], fs[k]);
+        }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        double cc = c[j], ss = sn[j] * x[j];
+        if (on && (quad[j] & 1)) { const double w = ss; ss = cc; cc = -w; }
+        if (on && (quad[j] & 2)) { ss = -ss; cc = -cc; }
+        if (!(A.rope.interleaved ? (j & 1) : up)) ss = -ss;
+        const double r = __dadd_rn(__dmul_rn((double)xa4[j], cc), __dmul_rn((double)xb4[j], ss));
+        y[j] = on ? r : (double)xa4[j];
+        if (fabs(y[j]) > kPgMaxAbs) y[j] = y[j] < 0.0 ? -kPgMaxAbs : kPgMaxAbs;
+    }
+    const uint16_t db = ap_scale(ap_extreme(y, lane));
+    const float df = __half2float(__ushort_as_half((uint16_t)(db & 0x7FFFu)));
+    const double d = (double)df;
     uint32_t codes = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const double c = d != 0.0 ? floor(y[j] / d + 8.5) : 8.0;
-        codes |= (uint32_t)fmin(fmax(c, 0.0), 15.0) << (8 * j);
+        const double v = (db & 0x8000u) ? -y[j] : y[j];
+        float n = floorf(fminf(fmaxf((float)v * (1.f / df) + 8.5f, 0.f), 15.f));  // this or a neighbour
+        const double gap = fma((double)(8.5f - n), d, v);                          // v - (n - 8.5) d
+        if (gap < 0.0) n -= 1.f;
+        else if (gap >= d) n += 1.f;
+        codes |= (df == 0.f ? 8u : (uint32_t)fminf(fmaxf(n, 0.f), 15.f)) << (8 * j);
     }
-    *scale = db;
-    return codes;
+    return {codes, db};
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kApWarps * 32) paged_append_kernel(const __grid_constant__ ApArgs A) {
-    __shared__ float2 s_cs[SVD_ROPE_MAX_PAIRS];
-    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int pairs = A.rope.pairs;
-    griddep_wait();
-    if ((int)threadIdx.x < pairs) {
-        const int i = threadIdx.x;
-        const int64_t pos = A.positions[A.rope.axis[i] * A.positions_ld + t];
-        const uint64_t ph = (uint64_t)pos * A.rope.phase[i];
-        const uint64_t quad = (ph + (1ull << 61)) >> 62;  // nearest quarter turn
-        const float r = __ll2float_rn((long long)(ph - (quad << 62))) * 0x1p-63f;  // half turns
-        float s, c;
-        sincospif(r, &s, &c);
-        if (quad & 1) { const float x = s; s = c; c = -x; }
-        if (quad & 2) { s = -s; c = -c; }
-        s_cs[i] = make_float2(c, s);
-    }
-    __syncthreads();
-    const int head = blockIdx.y * kApWarps + warp;
-    if (head >= A.Hq + 2 * A.Hkv) return;
-    const T *const row = reinterpret_cast<const T *>(A.qkv) + t * A.ld + (int64_t)head * kPgDim;
-    const int d0 = 4 * lane;
-    const bool is_v = head >= A.Hq + A.Hkv;
-    float x[4], xb[4] = {0.f, 0.f, 0.f, 0.f}, y[4], err[4] = {0.f, 0.f, 0.f, 0.f};
-    ap_load4(row + d0, x);
-    if (!is_v && d0 < 2 * pairs) {  // pairs is a multiple of four: a lane's dimensions turn alike
-        float2 cs[4];
-        bool second[4];
-        if (A.rope.interleaved) {
-            const float2 c0 = s_cs[2 * lane], c1 = s_cs[2 * lane + 1];
-            cs[0] = cs[1] = c0;
-            cs[2] = cs[3] = c1;
-            xb[0] = x[1]; xb[1] = x[0]; xb[2] = x[3]; xb[3] = x[2];
-            second[0] = second[2] = false;
-            second[1] = second[3] = true;
-        } else {
-            const bool up = d0 >= pairs;
-            ap_load4(row + (up ? d0 - pairs : d0 + pairs), xb);
+// Values as they came, with anything in them: not finite, too large, all zero, ties, scales among
+// fp16's subnormals.  What is not finite is noted and stored as 0 or the largest magnitude: a cache
+// byte never stands for a NaN that a masked position could spread.
+__device__ __noinline__ ApOut ap_general(int32_t *status, float4 y4, int lane) {
+    float y[4] = {y4.x, y4.y, y4.z, y4.w};
+    bool odd = false;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                cs[j] = s_cs[(up ? d0 - pairs : d0) + j];
-                second[j] = up;
-            }
-        }
+    for (int j = 0; j < 4; ++j) {
+        odd |= !(fabsf(y[j]) <= 3.4028235e38f);
+        if (y[j] != y[j]) y[j] = 0.f;
+        y[j] = fminf(fmaxf(y[j], -(float)kPgMaxAbs), (float)kPgMaxAbs);
+    }
+    if (__any_sync(~0u, odd) && status && lane == 0) atomicOr(status, SVD_ST_NONFINITE);
+    const uint16_t db = ap_scale(ap_extreme(y, lane));
+    const float d = __half2float(__ushort_as_half((uint16_t)(db & 0x7FFFu)));
+    uint32_t codes = 0x08080808u;
+    if (d != 0.f) {
+        codes = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float own = __fmul_rn(x[j], cs[j].x), other = __fmul_rn(xb[j], cs[j].y);
-            y[j] = second[j] ? __fadd_rn(own, other) : __fsub_rn(own, other);
-            err[j] = (fabsf(x[j]) + fabsf(xb[j])) * 0x1p-20f;  // angle, products and sum
+            const float v = (db & 0x8000u) ? -y[j] : y[j];
+            float n = floorf(fminf(fmaxf(v * (1.f / d) + 8.5f, 0.f), 15.f));
+            if (v < (n - 8.5f) * d) n -= 1.f;  // borders are exact: eight bits and five
+            else if (v >= (n - 7.5f) * d) n += 1.f;
+            codes |= (uint32_t)fminf(fmaxf(n, 0.f), 15.f) << (8 * j);
+        }
+    }
+    return {codes, db};
+}
+
+// The scale and codes of a lane's block where nothing is in doubt; false where something is.  With the
+// sign of d taken out, z = v / |d| + 8 rounds to the code or to one more (its error is below 2^-18),
+// and the exact distance v - (n - 8.5) |d| from the border decides; a rotated key is in doubt when it
+// lies within its error of a border.
+template <bool ROT>
+__device__ __forceinline__ bool ap_quick(const float y[4], const float low[4], const float err[4], uint16_t *scale,
+                                         uint32_t *codes) {
+    float hi = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), lo = fminf(fminf(y[0], y[1]), fminf(y[2], y[3]));
+    const float none = (y[0] + y[1]) * 0.f + (y[2] + y[3]) * 0.f;  // NaN if one is not finite
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
+        lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
+    }
+    const float m = hi > -lo ? hi : lo, big = fabsf(m);
+    const uint16_t db = ap_scale(m);
+    const float d = __half2float(__ushort_as_half((uint16_t)(db & 0x7FFFu)));
+    // (& and not &&: no branches)
+    bool sure = (none == 0.f) & (hi != -lo) & (big <= (float)kPgMaxAbs) & (d >= 0x1p-14f);
+    if (ROT) {
+        const float e4 = fmaxf(fmaxf(err[0], err[1]), fmaxf(err[2], err[3]));
+        const float e = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(e4)));
+        // the other extreme as large, or a scale next to a border: within the error, or m (which stands
+        // for what rounds to it) on one
+        const bool clear_m = (fabsf(hi + lo) > 2.f * e + 0x1p-22f * big) & ((__float_as_uint(m) & 0xFFFFu) != 0x8000u) &
+                             (__bfloat16_as_ushort(__float2bfloat16_rn(big - e)) ==
+                              __bfloat16_as_ushort(__float2bfloat16_rn(big + e)));
+        sure &= clear_m | (e == 0.f);
+    }
+    const uint32_t flip = (uint32_t)(db & 0x8000u) << 16;
+    const float inv = __fdividef(1.f, d), half = 0.5f * d, clear = half - 0x1p-23f * d;
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float v = __uint_as_float(__float_as_uint(y[j]) ^ flip);
+        float n = fmaf(v, inv, 8.f + 0x1p-18f) + 0x1p23f;  // to a whole number, in the low bits
+        float gap = v - fmaf(n - 0x1p23f, d, -8.5f * d);   // (the border is exact: eight bits and five)
+        if (ROT) gap += __uint_as_float(__float_as_uint(low[j]) ^ flip);
+        const bool below = gap < 0.f;
+        n -= below ? 1.f : 0.f;
+        if (ROT) {
+            gap += below ? d : 0.f;
+            sure &= (err[j] == 0.f) | (fabsf(gap - half) < clear - err[j]);
+        }
+        c[j] = __float_as_uint(fminf(n, 0x1p23f + 15.f));
+    }
+    *scale = db;
+    *codes = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    return sure;
+}
+
+// What a lane's four dimensions turn by, the same for every head of a token.
+struct ApTurn {
+    float c[4], s[4];  // y = x c + xb s, xb the other dimension of the pair (s carries the sign)
+    float cl[4], sl[4];  // their low parts
+    bool on;           // the dimensions are rotated
+    int mate;          // the lane of the other dimensions of half-split pairs; -1: interleaved
+};
+
+// One head of one token: a warp, four dimensions to a lane.  unit0, pos: the token's unit of kv head
+// 0 and its place there; unit0 is null when it is not stored.
+__device__ __forceinline__ void ap_head(const ApArgs &A, int t, int head, int lane, uint8_t *unit0, int pos,
+                                        const ApTurn &turn, const float x[4]) {
+    const int d0 = 4 * lane;
+    const bool is_v = head >= A.Hq + A.Hkv;
+    float xb[4] = {0.f, 0.f, 0.f, 0.f}, y[4], low[4] = {0.f, 0.f, 0.f, 0.f}, err[4] = {0.f, 0.f, 0.f, 0.f};
+    if (!is_v) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xb[j] = turn.mate < 0 ? x[j ^ 1] : __shfl_sync(~0u, x[j], turn.mate);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float p = __fmul_rn(x[j], turn.c[j]), q = __fmul_rn(xb[j], turn.s[j]), r = __fadd_rn(p, q);
+            y[j] = turn.on ? r : x[j];
+            if (head >= A.Hq && turn.on) {  // a key: what the products and the sum dropped, and cos' and sin's low parts
+                const float b = __fsub_rn(r, p), lost = __fadd_rn(__fsub_rn(p, __fsub_rn(r, b)), __fsub_rn(q, b));
+                const float rest = fmaf(x[j], turn.c[j], -p) + fmaf(xb[j], turn.s[j], -q) + lost +
+                                   fmaf(x[j], turn.cl[j], xb[j] * turn.sl[j]);
+                y[j] = __fadd_rn(r, rest);
+                low[j] = __fsub_rn(rest, __fsub_rn(y[j], r));
+                err[j] = (fabsf(x[j]) + fabsf(xb[j])) * 0x1p-27f;
+            }
         }
     } else {
 #pragma unroll
@@ -386,72 +527,26 @@ __global__ void __launch_bounds__(kApWarps * 32) paged_append_kernel(const __gri
         *reinterpret_cast<uint2 *>(A.q + ((int64_t)t * A.Hq + head) * kPgDim + d0) = o;
         return;
     }
-    const int64_t slot = A.slots[t];
-    if (slot < 0 || slot >= A.n_slots) {
-        if (slot >= 0 && A.status && lane == 0) atomicOr(A.status + t, SVD_ST_BAD_SLOT);
-        return;
-    }
-    // What is not finite is noted and stored as 0 or the largest magnitude: a cache byte never
-    // stands for a NaN that a masked position could spread.
-    bool odd = false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (!(fabsf(y[j]) <= 3.4028235e38f)) {
-            odd = true;
-            if (y[j] != y[j]) y[j] = 0.f;
-            if (x[j] != x[j] || fabsf(x[j]) > 3.4028235e38f || xb[j] != xb[j] || fabsf(xb[j]) > 3.4028235e38f)
-                err[j] = 0.f;
-        }
-        if (fabsf(y[j]) > (float)kPgMaxAbs && fabsf(y[j]) - err[j] > (float)kPgMaxAbs) err[j] = 0.f;
-        y[j] = fminf(fmaxf(y[j], -(float)kPgMaxAbs), (float)kPgMaxAbs);
-    }
-    const uint32_t bad = __ballot_sync(~0u, odd);
-    if (bad && A.status && lane == 0) atomicOr(A.status + t, SVD_ST_NONFINITE);
-
-    // The block's scale, and whether another one lies within the keys' error.
-    const uint32_t grp = 0xFFu << (lane & 24);
-    float e = fmaxf(fmaxf(err[0], err[1]), fmaxf(err[2], err[3]));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) e = fmaxf(e, __shfl_xor_sync(~0u, e, o));
-    const float m = ap_extreme(y, lane, ~0u);
-    uint16_t db = ap_scale(m);
-    const float d = __half2float(__ushort_as_half(db));
-    bool unsure = false;
-    if (e > 0.f) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)  // a value of the other sign that could be the larger one
-            unsure |= (y[j] < 0.f) != (m < 0.f) && fabsf(y[j]) + 2.f * e >= fabsf(m);
-        // m within its error of the border of two scales, or a scale among fp16's subnormals
-        const float lo = __bfloat162float(__float2bfloat16_rn(fabsf(m) - e));
-        const float hi = __bfloat162float(__float2bfloat16_rn(fabsf(m) + e));
-        unsure |= lo != hi || fabsf(d) < 0x1p-14f;
-    }
-    uint32_t codes = 0x08080808u;
-    if (d != 0.f) {
-        const float inv = 1.f / d;
-        const float s = d < 0.f ? -1.f : 1.f;
-        codes = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            int n = (int)fminf(fmaxf(floorf(y[j] * inv + 8.5f), 0.f), 15.f);
-            // below the border (n - 8.5) d, or on or above the next one (signs taken out by s)
-            if (n > 0 && s * y[j] < s * ((float)n - 8.5f) * d) --n;
-            else if (n < 15 && s * y[j] >= s * ((float)n - 7.5f) * d) ++n;
-            if (err[j] > 0.f) {
-                unsure |= n > 0 && fabsf(y[j] - ((float)n - 8.5f) * d) <= err[j];
-                unsure |= n < 15 && fabsf(y[j] - ((float)n - 7.5f) * d) <= err[j];
-            }
-            codes |= (uint32_t)n << (8 * j);
+    if (!unit0) return;
+    // The common case; whatever it cannot settle goes the general way.
+    uint16_t db;
+    uint32_t codes;
+    const bool sure = is_v ? ap_quick<false>(y, low, err, &db, &codes) : ap_quick<true>(y, low, err, &db, &codes);
+    if (!__all_sync(~0u, sure)) {
+        // Rotated blocks in doubt need the angle again; others only their values.
+        const bool turned = !is_v && 4 * (lane & 24) < 2 * A.rope.pairs;
+        const bool finite = (y[0] + y[1]) * 0.f + (y[2] + y[3]) * 0.f == 0.f;
+        const bool angle = __any_sync(~0u, !sure && turned) && __all_sync(~0u, finite);
+        const ApOut o =
+            angle ? ap_keys_f64(A, t, make_float4(x[0], x[1], x[2], x[3]), make_float4(xb[0], xb[1], xb[2], xb[3]), lane)
+                  : ap_general(A.status ? A.status + t : nullptr, make_float4(y[0], y[1], y[2], y[3]), lane);
+        if (angle || !turned || !sure) {
+            codes = o.codes;
+            db = (uint16_t)o.scale;
         }
     }
-    if (__ballot_sync(~0u, unsure && !bad) & grp) codes = ap_block_f64(A, t, d0, x, xb, lane, grp, &db);
-    __syncwarp();
 
-    const int64_t page = slot / A.page;
-    const int off = (int)(slot - page * A.page), pos = off & 15;
-    const int kvh = head - A.Hq - (is_v ? A.Hkv : 0);
-    uint8_t *const unit =
-        A.pages + ((page * A.Hkv + kvh) * (A.page >> 4) + (off >> 4)) * (int64_t)kPgUnitBytes;
+    uint8_t *const unit = unit0 + (int64_t)(head - A.Hq - (is_v ? A.Hkv : 0)) * ((A.page >> 4) * kPgUnitBytes);
     if (!is_v) {
         const uint32_t c2 = codes | (codes >> 4);  // nibbles of dims 0, 1 in byte 0, of 2, 3 in byte 2
         const uint16_t two = (uint16_t)((c2 & 0xFFu) | ((c2 >> 8) & 0xFF00u));
@@ -466,6 +561,65 @@ __global__ void __launch_bounds__(kApWarps * 32) paged_append_kernel(const __gri
             for (int j = 0; j < 4; ++j) v[j * 16] = (uint8_t)(both >> (8 * j));
         }
         if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(unit + kPgVScales + (lane >> 3) * 32 + pos * 2) = db;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kApWarps * 32, 4) paged_append_kernel(const __grid_constant__ ApArgs A) {
+    __shared__ float4 s_cs[SVD_ROPE_MAX_PAIRS];
+    __shared__ uint8_t *s_unit;
+    __shared__ int s_pos;
+    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pairs = A.rope.pairs, heads = A.Hq + 2 * A.Hkv, step = kApWarps * gridDim.y, d0 = 4 * lane;
+    const T *const row = reinterpret_cast<const T *>(A.qkv) + t * A.ld + d0;
+    int head = blockIdx.y * kApWarps + warp;
+    griddep_wait();
+    // A CTA lives for a few microseconds, most of them loads: four heads are fetched ahead, the
+    // first ones before the angles.
+    decltype(ap_raw(row)) ahead[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (head + k * step < heads) ahead[k] = ap_raw(row + (int64_t)(head + k * step) * kPgDim);
+    if ((int)threadIdx.x < pairs) s_cs[threadIdx.x] = ap_cos_sin(A, t, threadIdx.x);
+    if (threadIdx.x == kApWarps * 32 - 1) {
+        const int64_t slot = A.slots[t];
+        uint8_t *unit = nullptr;
+        int pos = 0;
+        if (slot >= 0 && slot < A.n_slots) {
+            const int64_t page = slot / A.page;
+            const int off = (int)(slot - page * A.page);
+            pos = off & 15;
+            unit = A.pages + (page * A.Hkv * (A.page >> 4) + (off >> 4)) * (int64_t)kPgUnitBytes;
+        } else if (slot >= 0 && A.status && blockIdx.y == 0) {
+            atomicOr(A.status + t, SVD_ST_BAD_SLOT);
+        }
+        s_unit = unit;
+        s_pos = pos;
+    }
+    __syncthreads();
+    uint8_t *const unit0 = s_unit;
+    const int pos = s_pos;
+    ApTurn turn;
+    turn.on = d0 < 2 * pairs;  // pairs is a multiple of four: a lane's dimensions turn alike
+    const bool up = !A.rope.interleaved && d0 >= pairs;
+    turn.mate = A.rope.interleaved ? -1 : turn.on ? (up ? lane - (pairs >> 2) : lane + (pairs >> 2)) : lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int i = A.rope.interleaved ? 2 * lane + (j >> 1) : d0 + j - (up ? pairs : 0);
+        const float4 cs = turn.on ? s_cs[i] : make_float4(1.f, 0.f, 0.f, 0.f);
+        const bool plus = A.rope.interleaved ? (j & 1) : up;
+        turn.c[j] = cs.x;
+        turn.cl[j] = cs.y;
+        turn.s[j] = plus ? cs.z : -cs.z;
+        turn.sl[j] = plus ? cs.w : -cs.w;
+    }
+    for (; head < heads; head += step) {
+        float x[4];
+        ap_floats(ahead[0], x);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) ahead[k] = ahead[k + 1];
+        if (head + 4 * step < heads) ahead[3] = ap_raw(row + (int64_t)(head + 4 * step) * kPgDim);
+        ap_head(A, t, head, lane, unit0, pos, turn, x);
     }
 }
 
@@ -510,13 +664,16 @@ int paged_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv,
         A.rope.interleaved = r.interleaved != 0;
         for (int i = 0; i < r.n_pairs; ++i) {
             if (!(fabs(r.inv_freq[i]) < 4294967296.0) || r.axis[i] >= r.n_axes) return SVD_ERR_INVALID_ARG;
-            A.rope.inv[i] = r.inv_freq[i];
             A.rope.phase[i] = rope_phase(r.inv_freq[i]);
             A.rope.axis[i] = r.axis[i];
         }
     }
     if (T == 0) return SVD_OK;
-    const dim3 grid((unsigned)T, (unsigned)((heads + kApWarps - 1) / kApWarps));
+    // One CTA to a token once there are several tokens to an SM; fewer tokens' heads are spread.
+    const int sms = sm_count();
+    if (sms < 1) return SVD_ERR_CUDA;
+    const int most = (int)((heads + kApWarps - 1) / kApWarps), want = (4 * sms + T - 1) / T;
+    const dim3 grid((unsigned)T, (unsigned)(want < most ? want : most));
     if (dtype == SVD_F32)
         SVD_CUDA_TRY(launch(paged_append_kernel<float>, grid, dim3(kApWarps * 32), 0, stream, true, A));
     else

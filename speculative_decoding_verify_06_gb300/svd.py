@@ -221,9 +221,7 @@ def load(path: str = LIB_PATH):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
     return t.data_ptr()
 
