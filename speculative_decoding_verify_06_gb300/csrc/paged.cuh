@@ -15,6 +15,8 @@
 
 #include "svd_common.cuh"
 
+#include <atomic>
+
 namespace svd {
 
 constexpr int kPgDim = 128;
@@ -29,6 +31,21 @@ constexpr double kPgMaxAbs = 65280.0;  // magnitudes end here: d <= 8160, and -8
 // mask of a 32-bit word yields two neighbouring positions as an fp16 pair.
 __host__ __device__ __forceinline__ int pg_v_byte(int i) {
     return (i & 12) | ((i & 1) << 1) | ((i >> 1) & 1);
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory: asked once for each kernel and device (the
+// call costs as much as a tenth of a launch).
+template <auto *kernel>
+inline cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<uint64_t> asked{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (asked.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) asked.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 inline bool pg_page_size_ok(int ps) { return ps >= 16 && ps <= SVD_PAGED_PAGE_MAX && ps % 16 == 0; }

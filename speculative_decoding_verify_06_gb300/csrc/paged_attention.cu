@@ -1034,8 +1034,7 @@ static int pa_launch(PaArgs A, cudaStream_t stream) {
     while (A.stages > 2 && Cfg::smem(A.stages, A.R) > most) --A.stages;
     const size_t smem = Cfg::smem(A.stages, A.R);
     const int grid = Cfg::kCtas * sm_count();
-    SVD_CUDA_TRY(cudaFuncSetAttribute(paged_attention_kernel<RP, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)smem));
+    SVD_CUDA_TRY((allow_smem<paged_attention_kernel<RP, F32>>(most)));
     SVD_CUDA_TRY(launch(paged_attention_kernel<RP, F32>, dim3(grid), dim3(Cfg::kThreads), smem, stream, true, A));
     // Few rows are split over many CTAs each, and then eight warps join one; many rows over few.
     const int64_t rows = (int64_t)A.T * A.Hq;

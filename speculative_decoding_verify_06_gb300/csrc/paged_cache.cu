@@ -206,8 +206,7 @@ int paged_tables(const int32_t *held, const int32_t *window, const int32_t *emit
                       kv_len, q_start, positions, status, slots, R, page, width, (int)n_pages, (int)tokens};
     const size_t smem = (size_t)R * 25 + 8;
     if (smem > 48 * 1024)
-        SVD_CUDA_TRY(cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)smem));
+        SVD_CUDA_TRY(allow_smem<paged_tables_kernel>((size_t)SVD_PAGED_MAX_REQUESTS * 25 + 8));
     auto items = [](int64_t n) { return (n + kTbChunk - 1) / kTbChunk; };
     const int64_t work = (int64_t)R * items(width) + items(n_pages) + items(tokens);
     const int grid = (int)(work < 2 * sms ? work : 2 * sms);

@@ -148,6 +148,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Open libsvd.so (once).  Raises when it is missing: there is no fallback path."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -228,11 +230,26 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream():
+    """The current device's current stream.  torch builds a Stream object for each question (about
+    3 us on a Grace core, as long as a launch); its raw handle is asked for where torch has it."""
+    global _current_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        def ask():
+            return torch.cuda.current_stream().cuda_stream
+    else:
+        def ask():
+            return raw(torch.cuda.current_device())
+    _current_stream = ask
+    return ask()
 
 
 def _check(fn: str, rc: int):
