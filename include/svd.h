@@ -472,7 +472,8 @@ int svd_kv_attention(const uint16_t *q, const void *cache, int capacity, int n_q
  *   writes no others).
  * Errors: SVD_ERR_INVALID_ARG for null or misaligned (16 bytes) pointers, sizes out of range, Hq %
  * Hkv != 0; SVD_ERR_WORKSPACE for a short workspace.  The workspace is zero-filled before its first
- * use and serves any number of calls in stream order; its first word gets bit 0 set if a bounded wait
+ * use and serves any number of calls in stream order, with the same heads and no more requests or
+ * max_new than it was asked for; its first word gets bit 0 set if a bounded wait
  * of the kernel gave up (the output is then undefined); its second word, when non-zero, is one more
  * than the number of polls after which a wait gives up (a test hook, as for svd_kv_attention).
  * SVD_ERR_UNSUPPORTED when n_requests * max_new * max_pages allow 2^31 tiles of 128 positions. */

@@ -237,18 +237,20 @@ struct PaSeg {
 template <int RP, bool F32>
 struct PaCfg {
     static constexpr int N = RP < 16 ? 16 : (RP + 15) / 16 * 16;
+    // columns of O: for fp32 outputs P's two parts stand side by side, rows j and RP + j
+    static constexpr int NO = F32 ? 2 * RP : N;
     static constexpr int kGroups = RP > 32 ? 2 : 1, RG = RP / kGroups;  // softmax groups, rows of each
     static constexpr int kThreads = (8 + 4 * kGroups + 3) * 32;
     static constexpr int kCtas = RP <= (F32 ? 16 : 24) ? 2 : 1;  // per SM
     // operands and scores in flight, in tensor memory: 256 columns for each of two CTAs, or 512
-    static constexpr int KB = kCtas == 2 ? 1 : 2, VB = 2, SB = 64 * (KB + VB) + 3 * N <= (kCtas == 2 ? 256 : 512) ? 2 : 1;
+    static constexpr int KB = kCtas == 2 ? 1 : 2, VB = 2, SB = 64 * (KB + VB) + 2 * N + NO <= (kCtas == 2 ? 256 : 512) ? 2 : 1;
     static constexpr uint32_t kColK = 0, kColV = 64 * KB, kColS = kColV + 64 * VB, kColO = kColS + SB * N;
     static constexpr uint32_t kCols = kCtas == 2 ? 256 : 512;
-    static_assert(kColO + N <= kCols, "tensor memory");
-    static constexpr int PB = F32 ? 1 : 2;  // P buffers (of two parts for fp32 outputs)
-    static constexpr int kQ = N * 256, kP = N * 256;
+    static_assert(kColO + NO <= kCols && NO % 16 == 0, "tensor memory");
+    static constexpr int PB = F32 ? 1 : 2;  // P buffers
+    static constexpr int kQ = N * 256, kP = NO * 256;
     static constexpr size_t smem(int stages, int R) {
-        return 1024 + (size_t)stages * kPaStageBytes + 2 * kQ + 2 * kP + ((size_t)R + 1) * 4;
+        return 1024 + (size_t)stages * kPaStageBytes + 2 * kQ + PB * kP + ((size_t)R + 1) * 4;
     }
     // Registers: two CTAs of 480 threads leave 64 each; the K and V warps hand 16 of theirs to the
     // softmax warps, 8 x 48 + 4 x 96 = 12 x 64.
@@ -276,7 +278,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
     __shared__ PaCtl s_ctl;
     uint8_t *const sm0 = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
     uint8_t *const s_q = sm0 + A.stages * kPaStageBytes, *const s_p = s_q + 2 * Cfg::kQ;
-    int *const s_pre = reinterpret_cast<int *>(s_p + 2 * Cfg::kP);
+    int *const s_pre = reinterpret_cast<int *>(s_p + Cfg::PB * Cfg::kP);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bar0 = smem_u32(s_bar);
     // Barriers come in pairs where what they guard has two buffers; tile t uses number t mod 2.
@@ -369,7 +371,9 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
     const uint32_t tmem = s_tmem;
     const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
 
+    // S: N columns, both operands K-major; O: NO columns, P's rows the fast index
     constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(Cfg::NO >> 3) << 17) | (8u << 24);
     // Tile t's phase of a barrier that counts the tiles of one of two buffers, or of n.
     auto phase = [](uint32_t t, uint32_t n) { return (t / n) & 1u; };
 
@@ -505,15 +509,10 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             if (lane == 0) {
                 pa_fence_after();
                 const uint32_t va = tmem + Cfg::kColV + 64 * (t % VB);
+                const uint64_t pb = p0 + t % Cfg::PB * (Cfg::kP / 16);
 #pragma unroll
-                for (int part = 0; part < (F32 ? 2 : 1); ++part) {
-                    // the small part first, so that fewer bits of it fall off
-                    const uint64_t pb = p0 + (F32 ? 1 - part : t % Cfg::PB) * (Cfg::kP / 16);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        pa_mma(tmem + Cfg::kColO, va + 8 * s, pb + 16 * s, kIdesc | (1u << 16),
-                               s || part || (!F32 && !first) ? 1u : 0u);
-                }
+                for (int s = 0; s < 8; ++s)
+                    pa_mma(tmem + Cfg::kColO, va + 8 * s, pb + 16 * s, kIdescO, s || (!F32 && !first) ? 1u : 0u);
                 pa_commit(b_pv + 8 * (t & 1));
                 pa_commit(b_vfree + 8 * (t % VB));
             }
@@ -814,11 +813,13 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                 pa_fence_after();
 #pragma unroll
                 for (int j = 0; j < RG; j += 8) {
-                    float o[8];
+                    float o[8], lo[8];
                     pa_ld8(tmem + quarter + Cfg::kColO + rb + j, o);
+                    pa_ld8(tmem + quarter + Cfg::kColO + RP + rb + j, lo);
                     pa_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j / 2 + i] = pa_add2(acc[j / 2 + i], pa_f2(o[2 * i], o[2 * i + 1]));
+                    for (int i = 0; i < 4; ++i)
+                        acc[j / 2 + i] = pa_add2(acc[j / 2 + i], pa_add2(pa_f2(o[2 * i], o[2 * i + 1]), pa_f2(lo[2 * i], lo[2 * i + 1])));
                 }
                 pa_fence_before();
                 if (any) {
@@ -826,7 +827,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                     for (int j = 0; j < RG / 2; ++j) acc[j] = pa_mul2(acc[j], *reinterpret_cast<const f2 *>(s_fac + rb + 2 * j));
                 }
             }
-            uint8_t *const prow = s_p + (F32 ? 0 : t % Cfg::PB) * Cfg::kP + (gt >> 3) * 128 + (gt & 7) * 16 + (rb >> 3) * 2048;
+            uint8_t *const prow = s_p + t % Cfg::PB * Cfg::kP + (gt >> 3) * 128 + (gt & 7) * 16 + (rb >> 3) * 2048;
 #pragma unroll
             for (int j = 0; j < RG; j += 8) {
                 float p[8];
@@ -847,7 +848,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                         const float2 f = __half22float2(reinterpret_cast<const __half2 &>(h[i]));
                         lo2[i] = pa_pack(p[2 * i] - f.x, p[2 * i + 1] - f.y);
                     }
-                    *reinterpret_cast<uint4 *>(prow + Cfg::kP + (j >> 3) * 2048) = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
+                    *reinterpret_cast<uint4 *>(prow + (RP >> 3) * 2048 + (j >> 3) * 2048) = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -900,10 +901,15 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                 pa_wait_ld();
                 if (F32) {
 #pragma unroll
-                    for (int j = 0; j < RG / 2; ++j) {
-                        const float2 x = pa_un2(acc[j]);
-                        o[2 * j] += x.x;
-                        o[2 * j + 1] += x.y;
+                    for (int j = 0; j < RG; j += 8) {
+                        float lo[8];
+                        pa_ld8(tmem + quarter + Cfg::kColO + RP + rb + j, lo);
+                        pa_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 x = pa_un2(acc[(j + i) / 2]);
+                            o[j + i] = (o[j + i] + lo[i]) + (i & 1 ? x.y : x.x);
+                        }
                     }
                 }
                 if (slot >= 0) {
@@ -1035,6 +1041,14 @@ static int pa_launch(PaArgs A, cudaStream_t stream) {
     const size_t smem = Cfg::smem(A.stages, A.R);
     const int grid = Cfg::kCtas * sm_count();
     SVD_CUDA_TRY((allow_smem<paged_attention_kernel<RP, F32>>(most)));
+    // A register split above what the launch has would wait forever: refuse to launch one.
+    static std::atomic<int> regs{0};
+    if (Cfg::kSplit && regs.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes at;
+        SVD_CUDA_TRY(cudaFuncGetAttributes(&at, paged_attention_kernel<RP, F32>));
+        regs.store(at.numRegs, std::memory_order_relaxed);
+    }
+    if (Cfg::kSplit && regs.load(std::memory_order_relaxed) < 64) return SVD_ERR_UNSUPPORTED;
     SVD_CUDA_TRY(launch(paged_attention_kernel<RP, F32>, dim3(grid), dim3(Cfg::kThreads), smem, stream, true, A));
     // Few rows are split over many CTAs each, and then eight warps join one; many rows over few.
     const int64_t rows = (int64_t)A.T * A.Hq;
@@ -1050,8 +1064,12 @@ static size_t pa_prefix_bytes(int R) { return align_up(kPaHeader + ((size_t)R + 
 size_t paged_attention_ws_bytes(int Hq, int Hkv, int R, int max_new) {
     if (Hq < 1 || Hq > 4096 || Hkv < 1 || Hq % Hkv || R < 1 || R > SVD_PAGED_MAX_REQUESTS || max_new < 1 || sm_count() < 1)
         return 0;
-    const int rp = pa_rows(Hq / Hkv, max_new, false);  // no fewer bytes than the fp32 variant takes
-    return pa_prefix_bytes(R) + (size_t)2 * pa_ctas(rp) * rp * (kPgDim + 2) * 4;
+    // enough for every variant up to the one that max_new takes, so that shorter windows fit too
+    const int most = pa_rows(Hq / Hkv, max_new, false);
+    size_t parts = 0;
+    for (int rp : {8, 16, 24, 32, 64})
+        if (rp <= most && parts < (size_t)pa_ctas(rp) * rp) parts = (size_t)pa_ctas(rp) * rp;
+    return pa_prefix_bytes(R) + 2 * parts * (kPgDim + 2) * 4;
 }
 
 int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,

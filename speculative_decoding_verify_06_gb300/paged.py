@@ -1,0 +1,135 @@
+"""Verify passes of several requests over a paged 4-bit cache, with the lengths kept on the GPU.
+
+A step is what "100 tokens per second ..." ("How speculative decoding gets past a per-token wall")
+describes for one sequence, for a batch of them ("Why a hiring company is writing this"): the tables
+follow the tokens that the last acceptance kept (svd_paged_tables), every layer's queries and keys are
+rotated and its keys and values appended (svd_paged_append), and the window's tokens attend to
+their requests' caches (svd_paged_attention).  Nothing of a step waits for the host: acceptance
+counts, lengths, page ids and free pages stay in device memory, so a step can be recorded.
+
+    python -m speculative_decoding_verify_06_gb300.paged [requests] [window] [steps]
+
+runs a two-layer stand-in for a model on synthetic weights, accepting drafts and growing the caches.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import svd
+
+
+class PagedBatch:
+    """The caches of `requests` requests in `layers` pools of n_pages pages, one table for all layers.
+
+    begin() opens a step, layer() runs one layer's append and attention.  Between two begin() calls
+    the device tensors q_start, kv_len, slots, positions and status describe the step's tokens."""
+
+    def __init__(self, requests: int, layers: int, n_pages: int, page_size: int = 64, max_len: int = 32768,
+                 max_window: int = 8, n_q_heads: int = 40, n_kv_heads: int = 8, rope: svd.Rope | None = None,
+                 out_dtype: int = svd.SVD_BF16, max_tokens: int | None = None, device="cuda"):
+        dev = torch.device(device)
+        self.device, self.R, self.page, self.n_pages = dev, requests, page_size, n_pages
+        self.Hq, self.Hkv, self.rope, self.out_dtype = n_q_heads, n_kv_heads, rope, out_dtype
+        self.width = -(-max_len // page_size)
+        self.max_window = max_window
+        self.max_tokens = max_tokens or requests * max_window
+        nbytes = svd.svd_paged_cache_bytes(n_kv_heads, page_size, n_pages)
+        if nbytes == 0:
+            raise ValueError("no such pool: see svd_paged_cache_bytes")
+        self.pools = [torch.zeros(nbytes, dtype=torch.uint8, device=dev) for _ in range(layers)]
+        i32 = dict(dtype=torch.int32, device=dev)
+        # the tables are read from one copy and written to the other, in turn
+        self.table = [torch.full((requests, self.width), -1, **i32) for _ in range(2)]
+        self.free = [torch.arange(n_pages - 1, -1, -1, **i32) for _ in range(2)]  # page 0 on top
+        self.n_free = [torch.full((1,), n_pages, **i32) for _ in range(2)]
+        self.held = [torch.zeros(requests, **i32) for _ in range(2)]
+        self.now = 0
+        self.q_start = torch.zeros(requests + 1, **i32)
+        self.slots = torch.full((self.max_tokens,), -1, dtype=torch.int64, device=dev)
+        self.positions = torch.full((self.max_tokens,), -1, **i32)
+        self.status = torch.zeros(requests, **i32)
+        self.window = torch.zeros(requests, **i32)  # tokens of the step before
+        self.ws = torch.zeros(svd.svd_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, requests, max_window),
+                              dtype=torch.uint8, device=dev)
+        self.q = torch.empty((self.max_tokens, n_q_heads, 128), dtype=torch.bfloat16, device=dev)
+        self.bad = torch.zeros(self.max_tokens, **i32)  # SVD_ST_* bits of the tokens appended since it was zeroed
+        self.scale = 128 ** -0.5
+
+    @property
+    def kv_len(self):
+        return self.held[self.now]
+
+    def begin(self, n_new, emitted=None, stream=None):
+        """Opens a step of n_new [R] new tokens for each request, after `emitted` [R] of the last
+        step's tokens were kept (None: all of them).  Requests that cannot be served have a status
+        and no tokens; they keep what they hold."""
+        a, b = self.now, 1 - self.now
+        svd.svd_paged_tables(self.held[a], None if emitted is None else self.window, emitted, n_new, self.R,
+                             self.page, self.table[a], self.width, self.free[a], self.n_free[a], self.n_pages,
+                             self.table[b], self.free[b], self.n_free[b], self.held[b], self.q_start, self.slots,
+                             self.positions, self.max_tokens, self.status, stream=stream)
+        torch.sub(self.q_start[1:], self.q_start[:-1], out=self.window)
+        self.now = b
+
+    def layer(self, l: int, qkv, out, n_tokens: int | None = None, positions=None, stream=None):
+        """Layer l's step: rotates and stores qkv [n_tokens][(Hq + 2 Hkv) * 128] (fp32, as
+        svd_verify_linear writes it, or bf16) and writes its attention to out [n_tokens][Hq][128].
+        positions [axes][n_tokens] replaces the requests' own positions (images: time, height, width)."""
+        T = self.max_tokens if n_tokens is None else n_tokens
+        pos = self.positions if positions is None else positions
+        pool = self.pools[l]
+        svd.svd_paged_append(qkv, qkv.stride(0), T, self.Hq, self.Hkv, self.slots, pool, self.page, self.n_pages, self.q,
+                             rope=self.rope, positions=pos, positions_ld=pos.shape[-1],
+                             dtype=svd.SVD_F32 if qkv.dtype == torch.float32 else svd.SVD_BF16, status=self.bad,
+                             stream=stream)
+        svd.svd_paged_attention(self.q, T, self.kv_len, self.q_start, self.R, self.max_window, self.table[self.now], self.width,
+                                pool, self.page, self.n_pages, self.Hq, self.Hkv, self.scale, out, self.out_dtype, self.ws,
+                                stream=stream)
+        return out
+
+
+def demo(requests: int = 8, window: int = 4, steps: int = 6, prompt: int = 200, layers: int = 2, seed: int = 0):
+    """Batched verify steps of a stand-in model: per layer q|k|v and o products of 4-bit weights
+    (svd_verify_linear over all requests' window columns) around the paged attention; acceptance counts
+    are drawn instead of sampled.  Returns the PagedBatch and the kept lengths, step by step."""
+    from . import stack, synth
+    dev = torch.device("cuda")
+    C = requests * window
+    hidden, kv = synth.HIDDEN, synth.N_KV_HEADS * 128
+    rope = svd.Rope([10000.0 ** (-i / 64) for i in range(64)])
+    b = PagedBatch(requests, layers, n_pages=requests * (prompt + (steps + 1) * window) // 64 + 2 * requests, max_len=4096,
+                   max_window=max(window, prompt), rope=rope, max_tokens=max(C, requests * prompt))
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    # the prompts: their keys and values arrive in one step of `prompt` tokens a request
+    b.begin(torch.full((requests,), prompt, dtype=torch.int32, device=dev))
+    qkv = torch.randn((requests * prompt, hidden + 2 * kv), generator=g, device=dev)
+    o = torch.empty((b.max_tokens, b.Hq, 128), dtype=torch.bfloat16, device=dev)
+    for l in range(layers):
+        b.layer(l, qkv, o, n_tokens=requests * prompt)
+    b.max_window = window
+    lin = [(stack.Linear(hidden, hidden + 2 * kv, C, seed + 10 * l, dev), stack.Linear(hidden, hidden, C, seed + 10 * l + 1, dev))
+           for l in range(layers)]
+    ws = torch.zeros(max(svd.svd_verify_linear_workspace_bytes(x.in_f, x.out_f, C) for p in lin for x in p), dtype=torch.uint8,
+                     device=dev)
+    n_new = torch.full((requests,), window, dtype=torch.int32, device=dev)
+    lengths, emitted = [b.kv_len.tolist()], None
+    for _ in range(steps):
+        b.begin(n_new, emitted)
+        x = synth.activations_torch(C, hidden, seed, dev)
+        for l, (qkv_lin, o_lin) in enumerate(lin):
+            svd.svd_verify_linear(qkv_lin.W, x, C, qkv_lin.Y, ws)
+            b.layer(l, qkv_lin.Y, o, n_tokens=C)
+            svd.svd_verify_linear(o_lin.W, o, C, o_lin.Y, ws)  # the attention's bf16 is the product's input as it is
+            x = (o_lin.Y / o_lin.Y.square().mean(-1, keepdim=True).sqrt()).to(torch.bfloat16)
+        emitted = torch.randint(1, window + 1, (requests,), generator=g, device=dev).to(torch.int32)
+        lengths.append((b.kv_len - window + emitted).tolist())
+    return b, lengths
+
+
+if __name__ == "__main__":
+    import sys
+    batch, kept = demo(*[int(a) for a in sys.argv[1:4]])
+    for n, k in enumerate(kept):
+        print(f"step {n}: kept positions {k}")
+    print(f"{int(batch.n_free[batch.now])} of {batch.n_pages} pages free, status {batch.status.tolist()}")
