@@ -239,23 +239,28 @@ struct PaCfg {
     static constexpr int N = RP < 16 ? 16 : (RP + 15) / 16 * 16;
     // columns of O: for fp32 outputs P's two parts stand side by side, rows j and RP + j
     static constexpr int NO = F32 ? 2 * RP : N;
-    static constexpr int kGroups = RP > 32 ? 2 : 1, RG = RP / kGroups;  // softmax groups, rows of each
+    static constexpr int kGroups = RP > 32 ? RP / 32 : 1, RG = RP / kGroups;  // softmax groups, rows of each
     static constexpr int kThreads = (8 + 4 * kGroups + 3) * 32;
     static constexpr int kCtas = RP <= (F32 ? 16 : 24) ? 2 : 1;  // per SM
     // operands and scores in flight, in tensor memory: 256 columns for each of two CTAs, or 512
-    static constexpr int KB = kCtas == 2 ? 1 : 2, VB = 2, SB = 64 * (KB + VB) + 2 * N + NO <= (kCtas == 2 ? 256 : 512) ? 2 : 1;
+    static constexpr int KB = kCtas == 2 || RP == 128 ? 1 : 2, VB = 2, SB = 64 * (KB + VB) + 2 * N + NO <= (kCtas == 2 ? 256 : 512) ? 2 : 1;
     static constexpr uint32_t kColK = 0, kColV = 64 * KB, kColS = kColV + 64 * VB, kColO = kColS + SB * N;
     static constexpr uint32_t kCols = kCtas == 2 ? 256 : 512;
     static_assert(kColO + NO <= kCols && NO % 16 == 0, "tensor memory");
+    // (K(t + SB) may not arrive at the barrier of S(t) before S(t) is issued)
+    static_assert(SB >= KB, "as many S buffers as K buffers");
     static constexpr int PB = F32 ? 1 : 2;  // P buffers
     static constexpr int kQ = N * 256, kP = NO * 256;
     static constexpr size_t smem(int stages, int R) {
         return 1024 + (size_t)stages * kPaStageBytes + 2 * kQ + PB * kP + ((size_t)R + 1) * 4;
     }
-    // Registers: two CTAs of 480 threads leave 64 each; the K and V warps hand 16 of theirs to the
-    // softmax warps, 8 x 48 + 4 x 96 = 12 x 64.
-    static constexpr bool kSplit = kCtas == 2 && RP >= 16;
-    static_assert(!kSplit || (kThreads == 480 && kGroups == 1), "the register split is for this shape");
+    // Registers of a thread: two CTAs of 15 warps leave 64, one of 27 warps 72; there the K and V warps
+    // hand some of theirs to the softmax warps.
+    static constexpr int kRegs = RP == 128 ? 72 : 64;
+    static constexpr bool kSplit = RP == 128 || (kCtas == 2 && RP >= 16);
+    static constexpr int kRegsKV = RP == 128 ? 40 : 48, kRegsS = RP == 128 ? 88 : 96;
+    static_assert(!kSplit || 8 * kRegsKV + 4 * kGroups * kRegsS <= (8 + 4 * kGroups) * kRegs,
+                  "a split may not ask for more than the launch has");
 };
 
 template <int RP, bool F32>
@@ -524,7 +529,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
-        if (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsKV));
         // ---- V: lane = dimension, columns of two positions ---------------------------------
         const int dim = tid - 128;
         // low nibbles: (1024 + c) - 1032; high ones: (1024 + 16 c) / 16 - 72; both c - 8 exactly
@@ -579,7 +584,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         }
     } else if (warp < 4) {
         // ---- K: lane = position, columns of two dimensions ---------------------------------
-        if (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsKV));
         int st = 0;
         uint32_t st_phase = 0, n_seg = 0;
         bool fresh = true;
@@ -664,7 +669,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         }
     } else {
         // ---- softmax: lane = position, rows rb .. rb + RG - 1 of the row tile --------------
-        if (Cfg::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        if (Cfg::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsS));
         const int sg = (warp - 8) >> 2, rb = sg * RG, gt = (tid & 127), gw = warp & 3;
         const float c = A.c;
         auto group_sync = [&]() { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + sg) : "memory"); };
@@ -1024,11 +1029,11 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) paged_merge_kernel(cons
     }
 }
 
-// Rows per tile: the fewest that hold a window's rows, 64 for longer ones (32 for fp32 outputs,
+// Rows per tile: the fewest that hold a window's rows, 128 for longer ones (32 for fp32 outputs,
 // whose sums live in registers beside the scores).
 static int pa_rows(int G, int max_new, bool f32) {
     const int64_t rows = (int64_t)G * max_new;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows <= 32 || f32 ? 32 : 64;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows <= 32 || f32 ? 32 : rows <= 64 ? 64 : 128;
 }
 static int pa_ctas(int rp) { return (rp <= 24 ? 2 : 1) * sm_count(); }  // at most
 
@@ -1048,7 +1053,7 @@ static int pa_launch(PaArgs A, cudaStream_t stream) {
         SVD_CUDA_TRY(cudaFuncGetAttributes(&at, paged_attention_kernel<RP, F32>));
         regs.store(at.numRegs, std::memory_order_relaxed);
     }
-    if (Cfg::kSplit && regs.load(std::memory_order_relaxed) < 64) return SVD_ERR_UNSUPPORTED;
+    if (Cfg::kSplit && regs.load(std::memory_order_relaxed) < Cfg::kRegs) return SVD_ERR_UNSUPPORTED;
     SVD_CUDA_TRY(launch(paged_attention_kernel<RP, F32>, dim3(grid), dim3(Cfg::kThreads), smem, stream, true, A));
     // Few rows are split over many CTAs each, and then eight warps join one; many rows over few.
     const int64_t rows = (int64_t)A.T * A.Hq;
@@ -1067,7 +1072,7 @@ size_t paged_attention_ws_bytes(int Hq, int Hkv, int R, int max_new) {
     // enough for every variant up to the one that max_new takes, so that shorter windows fit too
     const int most = pa_rows(Hq / Hkv, max_new, false);
     size_t parts = 0;
-    for (int rp : {8, 16, 24, 32, 64})
+    for (int rp : {8, 16, 24, 32, 64, 128})
         if (rp <= most && parts < (size_t)pa_ctas(rp) * rp) parts = (size_t)pa_ctas(rp) * rp;
     return pa_prefix_bytes(R) + 2 * parts * (kPgDim + 2) * 4;
 }
@@ -1119,7 +1124,8 @@ int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32
         case 16: return SVD_PA(16);
         case 24: return SVD_PA(24);
         case 32: return SVD_PA(32);
-        default: return pa_launch<64, false>(A, stream);
+        case 64: return pa_launch<64, false>(A, stream);
+        default: return pa_launch<128, false>(A, stream);
     }
 #undef SVD_PA
 }
