@@ -970,6 +970,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) paged_merge_kernel(cons
         nt = pa_row_tiles<RP>(A, x, rt);
     }
     griddep_wait();
+    griddep_launch_dependents();
     if (!mine) return;  // (the same for all warps of a row)
     const int n_tiles = A.prefix[A.R], pre = A.prefix[r], per = (A.prefix[r + 1] - pre) / A.Hkv;
     if (n_tiles == 0) return;

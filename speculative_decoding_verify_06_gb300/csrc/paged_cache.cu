@@ -437,8 +437,8 @@ __device__ __noinline__ ApOut ap_general(int32_t *status, float4 y4, int lane) {
 // and the exact distance v - (n - 8.5) |d| from the border decides; a rotated key is in doubt when it
 // lies within its error of a border.
 template <bool ROT>
-__device__ __forceinline__ bool ap_quick(const float y[4], const float low[4], const float err[4], uint16_t *scale,
-                                         uint32_t *codes) {
+__device__ __forceinline__ bool ap_quick(const float y[4], const float low[4], const float err[4], bool turned,
+                                         uint16_t *scale, uint32_t *codes) {
     float hi = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), lo = fminf(fminf(y[0], y[1]), fminf(y[2], y[3]));
     const float none = (y[0] + y[1]) * 0.f + (y[2] + y[3]) * 0.f;  // NaN if one is not finite
 #pragma unroll
@@ -463,6 +463,7 @@ __device__ __forceinline__ bool ap_quick(const float y[4], const float low[4], c
     }
     const uint32_t flip = (uint32_t)(db & 0x8000u) << 16;
     const float inv = __fdividef(1.f, d), half = 0.5f * d, clear = half - 0x1p-23f * d;
+    float room = 1.f;  // of the key that is nearest to a border
     uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -474,10 +475,11 @@ __device__ __forceinline__ bool ap_quick(const float y[4], const float low[4], c
         n -= below ? 1.f : 0.f;
         if (ROT) {
             gap += below ? d : 0.f;
-            sure &= (err[j] == 0.f) | (fabsf(gap - half) < clear - err[j]);
+            room = fminf(room, (clear - err[j]) - fabsf(gap - half));
         }
         c[j] = __float_as_uint(fminf(n, 0x1p23f + 15.f));
     }
+    if (ROT) sure &= (room > 0.f) | !turned;
     *scale = db;
     *codes = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     return sure;
@@ -498,21 +500,32 @@ __device__ __forceinline__ void ap_head(const ApArgs &A, int t, int head, int la
     const int d0 = 4 * lane;
     const bool is_v = head >= A.Hq + A.Hkv;
     float xb[4] = {0.f, 0.f, 0.f, 0.f}, y[4], low[4] = {0.f, 0.f, 0.f, 0.f}, err[4] = {0.f, 0.f, 0.f, 0.f};
+    // (branches around the loops, selects inside them)
     if (!is_v) {
+        if (turn.mate < 0) {
+            xb[0] = x[1]; xb[1] = x[0]; xb[2] = x[3]; xb[3] = x[2];
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) xb[j] = turn.mate < 0 ? x[j ^ 1] : __shfl_sync(~0u, x[j], turn.mate);
+            for (int j = 0; j < 4; ++j) xb[j] = __shfl_sync(~0u, x[j], turn.mate);
+        }
+    }
+    if (head < A.Hq) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float r = __fadd_rn(__fmul_rn(x[j], turn.c[j]), __fmul_rn(xb[j], turn.s[j]));
+            y[j] = turn.on ? r : x[j];
+        }
+    } else if (!is_v) {  // a key: with what the products and the sum dropped, and cos' and sin's low parts
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float p = __fmul_rn(x[j], turn.c[j]), q = __fmul_rn(xb[j], turn.s[j]), r = __fadd_rn(p, q);
-            y[j] = turn.on ? r : x[j];
-            if (head >= A.Hq && turn.on) {  // a key: what the products and the sum dropped, and cos' and sin's low parts
-                const float b = __fsub_rn(r, p), lost = __fadd_rn(__fsub_rn(p, __fsub_rn(r, b)), __fsub_rn(q, b));
-                const float rest = fmaf(x[j], turn.c[j], -p) + fmaf(xb[j], turn.s[j], -q) + lost +
-                                   fmaf(x[j], turn.cl[j], xb[j] * turn.sl[j]);
-                y[j] = __fadd_rn(r, rest);
-                low[j] = __fsub_rn(rest, __fsub_rn(y[j], r));
-                err[j] = (fabsf(x[j]) + fabsf(xb[j])) * 0x1p-27f;
-            }
+            const float b = __fsub_rn(r, p), lost = __fadd_rn(__fsub_rn(p, __fsub_rn(r, b)), __fsub_rn(q, b));
+            const float rest = fmaf(x[j], turn.c[j], -p) + fmaf(xb[j], turn.s[j], -q) + lost +
+                               fmaf(x[j], turn.cl[j], xb[j] * turn.sl[j]);
+            const float v = __fadd_rn(r, rest);
+            y[j] = turn.on ? v : x[j];
+            low[j] = turn.on ? __fsub_rn(rest, __fsub_rn(v, r)) : 0.f;
+            err[j] = turn.on ? (fabsf(x[j]) + fabsf(xb[j])) * 0x1p-27f : 0.f;
         }
     } else {
 #pragma unroll
@@ -530,7 +543,8 @@ __device__ __forceinline__ void ap_head(const ApArgs &A, int t, int head, int la
     // The common case; whatever it cannot settle goes the general way.
     uint16_t db;
     uint32_t codes;
-    const bool sure = is_v ? ap_quick<false>(y, low, err, &db, &codes) : ap_quick<true>(y, low, err, &db, &codes);
+    const bool sure = is_v ? ap_quick<false>(y, low, err, false, &db, &codes)
+                           : ap_quick<true>(y, low, err, turn.on, &db, &codes);
     if (!__all_sync(~0u, sure)) {
         // Rotated blocks in doubt need the angle again; others only their values.
         const bool turned = !is_v && 4 * (lane & 24) < 2 * A.rope.pairs;
