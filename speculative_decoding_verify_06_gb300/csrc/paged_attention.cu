@@ -15,18 +15,37 @@
 // second kernel joins them.
 //
 // One tile.  Bulk copies bring up to eight units into a ring stage.  Four warps turn K into fp16 in
-// tensor memory (lane = position) and four others V (lane = dimension, two positions per column):
-// every d (c - 8) is exact in fp16.  S^T = K Q^T (M = 128 positions, N = query rows) and
-// O^T += V^T P^T (M = 128 dimensions) run on tcgen05 with A in tensor memory and fp32 accumulators;
-// the K warps turn S into P, with the next tile's K written before that, so the next S runs
-// meanwhile.  A lane holds one position of S for all rows, so the softmax needs no lane exchange:
-// the reference of a row changes only when a score exceeds it by 15 (p <= 2^15 in between), checked
-// by one vote of the four warps, and starts 7 below the first tile's maximum.  p keeps fp16's eleven
-// bits from 2^22 down below the maximum and loses them gradually to 2^31 below.  For fp32 outputs P
-// is split into two fp16 parts (relative 2^-22) and V^T P^T runs over both.
+// tensor memory (lane = position) and four others V (lane = dimension, two positions per column): codes
+// to fp16 by a mask and an exponent, then d (c - 8), exact because d has eight significant bits (K as
+// d / 8 (c - 8), whose blocks with d < 2^-14 round to multiples of 2^-24).  S^T = K Q^T (M = 128
+// positions, N = query rows) and O^T += V^T P^T (M = 128 dimensions) run on tcgen05 with A in tensor
+// memory and fp32 accumulators, issued by a warp each; K is refilled by halves, so that its next tile
+// starts while S still reads the second half.  The softmax warps turn S into P in shared memory.  A lane
+// holds one position of S for all rows, so the softmax needs no lane exchange: the reference of a row
+// changes only when a score exceeds it by 15 (p <= 2^15 in between), checked by one vote of the four
+// warps, and starts 7 below the first tile's maximum.  p keeps fp16's eleven bits down to 2^-22 of the
+// largest and loses them gradually to 2^-32.  For fp32 outputs P is split into two fp16 parts
+// (relative 2^-22) that stand side by side as columns of one product, and O is added up in registers
+// tile by tile, because the tensor core truncates what it adds to its accumulators: 256 additions
+// were 2.5e-6 off, so are 6e-7.
 //
 // Rows a mask leaves empty get zeros.  Positions past the length, or on a page outside the pool,
 // are cut out of S, and their V scales are replaced by 0, whatever their bytes.
+//
+// What bounds it.  Every cache byte is read once, 144 per position and kv head, but each takes work that
+// no pipe does at HBM's pace: of about 4500 warp instructions per tile at 20 rows (K 1000, V 1400, softmax
+// 1000, the rest copies, waits and MMA issue) the SM issues 72 % of what it could, with instruction
+// fetch and the chain copy - K - S - P - O behind the rest.  262144 positions of 8 kv heads, 20 rows: 91.5 us,
+// 3.3 TB/s of cache; 64 ragged requests of up to 16K: 214 us, 3.35 TB/s; 200 requests of 2K, one
+// token, fp32: 102 us, 2.5 TB/s; 32768 positions: 23.5 us, of which 12 are the launch, the first tile's
+// latency and the join; two chunks of 512 tokens behind 8K: 261 us, 547 TFLOP/s.
+//
+// What was measured on the way (262K / chunk of 512): K and softmax in the same four warps, 105 / 640 us;
+// four roles with one MMA warp, 107 / 450; two MMA warps and halves, 103 / 422; queries fetched
+// ahead and a join by eight warps, 93 / 356; row tiles of 128 instead of 64 rows for long windows, 261.  Not
+// kept: two K and two V groups (355 with 64 rows), softmax groups of 16 rows (372), MMAs under
+// elect.sync with uniform operands (359, 93.3), V's loop unrolled four or eight times (200 short requests:
+// 117 and 125 us against 109), waits that poll without suspending, that sleep, or with a hint (no gain).
 #include "paged.cuh"
 
 namespace svd {
