@@ -19,8 +19,9 @@ namespace svd {
 // One launch: every CTA computes the sums over all requests for itself (up to 4096 of them, 16
 // bytes each, from L2), keeps them in shared memory, and then fills its share of the outputs, each
 // element a function of the sums and the inputs alone (no CTA waits for another).  What bounds it is
-// latency, a launch and three block-wide sums one after the other: 4.1 us for 8 requests (95 KB moved), 6.3
-// us for 256 with 131 K table entries, 6.9 us for 48 prompts with 49 K new tokens.
+// latency, a launch and three block-wide sums one after the other: 3.8 us for 8 requests (95 KB moved), 5.9
+// us for 256 with 131 K table entries, 6.4 us for 48 prompts with 49 K new tokens.  (With 64-bit divisions in
+// the sums 4.1, 6.3 and 6.9.)
 constexpr int kTbThreads = 512;
 constexpr int kTbWarps = kTbThreads / 32;
 constexpr int kTbChunk = 1024;  // outputs per work item
@@ -78,33 +79,35 @@ __global__ void __launch_bounds__(kTbThreads) paged_tables_kernel(const TbArgs A
     unsigned long long tok_sum = 0, page_sum = 0, total;
     for (int base = 0; base < R; base += kTbThreads) {
         const int r = base + tid;
-        long long keep = 0, add = 0, p0 = 0, p1 = 0;
-        uint32_t st = 0;
+        long long keep = 0;
+        uint32_t st = 0, ask = 0, p0 = 0, p1 = 0;
         if (r < R) {
             const long long held = A.held[r], n = A.n_new[r];
             const long long win = A.window ? A.window[r] : 0, emi = A.window ? A.emitted[r] : 0;
+            const long long room = (long long)A.width * A.page;  // < 2^31
             keep = held - win + emi;
-            p0 = (held + A.page - 1) / A.page;
-            p1 = (keep + n + A.page - 1) / A.page;
-            add = n;
-            if (win < 0 || emi < 0 || emi > win || win > held || n < 0 || p0 > A.width || p1 > A.width)
+            if (win < 0 || emi < 0 || emi > win || win > held || n < 0 || held > room || keep + n > room) {
                 st = SVD_ST_BAD_REQUEST;
+            } else {
+                p0 = ((uint32_t)held + A.page - 1) / (uint32_t)A.page;
+                p1 = ((uint32_t)(keep + n) + A.page - 1) / (uint32_t)A.page;
+                ask = (uint32_t)n;
+            }
         }
-        const unsigned long long ask = st ? 0ull : (unsigned long long)add;
         const unsigned long long upto = tok_sum + tb_scan(ask, &total, s_w);
         tok_sum += total;
         if (!st && ask > 0 && upto > (unsigned long long)A.tokens) st = SVD_ST_NO_TOKENS;
         if (st) p1 = p0;
-        const unsigned long long take = p1 > p0 ? p1 - p0 : 0, give = p0 > p1 ? p0 - p1 : 0;
-        const unsigned long long pg = (give << 32) | take;
+        const uint32_t take = p1 > p0 ? p1 - p0 : 0, give = p0 > p1 ? p0 - p1 : 0;
+        const unsigned long long pg = ((unsigned long long)give << 32) | take;
         const unsigned long long sum = page_sum + tb_scan(pg, &total, s_w);
         page_sum += total;
         if (r < R) {
             s_keep[r] = (int)keep;
-            s_p0[r] = st == SVD_ST_BAD_REQUEST ? 0 : (int)p0;
-            s_q1[r] = st == SVD_ST_BAD_REQUEST ? 0 : (int)p1;
-            s_take[r] = (int)((uint32_t)sum - (uint32_t)take);
-            s_give[r] = (int)((uint32_t)(sum >> 32) - (uint32_t)give);
+            s_p0[r] = (int)p0;
+            s_q1[r] = (int)p1;
+            s_take[r] = (int)((uint32_t)sum - take);
+            s_give[r] = (int)((uint32_t)(sum >> 32) - give);
             s_st[r] = (uint8_t)st;
         }
     }
@@ -161,12 +164,11 @@ __global__ void __launch_bounds__(kTbThreads) paged_tables_kernel(const TbArgs A
             *A.n_free_out = left;
         }
     }
-    const int row_items = (A.width + kTbChunk - 1) / kTbChunk;
-    const int64_t t_items = (int64_t)R * row_items;
-    const int f_items = (A.n_pages + kTbChunk - 1) / kTbChunk, s_items = (A.tokens + kTbChunk - 1) / kTbChunk;
-    for (int64_t it = blockIdx.x; it < t_items + f_items + s_items; it += gridDim.x) {
+    const uint32_t row_items = (A.width + kTbChunk - 1) / kTbChunk, t_items = (uint32_t)R * row_items;  // < 2^31
+    const uint32_t f_items = (A.n_pages + kTbChunk - 1) / kTbChunk, s_items = (A.tokens + kTbChunk - 1) / kTbChunk;
+    for (uint32_t it = blockIdx.x; it < t_items + f_items + s_items; it += gridDim.x) {
         if (it < t_items) {
-            const int r = (int)(it / row_items), c0 = (int)(it % row_items) * kTbChunk;
+            const int r = (int)(it / row_items), c0 = (int)(it - r * row_items) * kTbChunk;
             const int c1 = min(c0 + kTbChunk, A.width);
             for (int c = c0 + tid; c < c1; c += kTbThreads) A.table_out[(int64_t)r * A.width + c] = entry(r, c);
         } else if (it < t_items + f_items) {
@@ -180,7 +182,8 @@ __global__ void __launch_bounds__(kTbThreads) paged_tables_kernel(const TbArgs A
                 if (i < n_tok) {
                     const int r = tb_last_le(s_tok, R, i);
                     pos = s_keep[r] + i - s_tok[r];
-                    slot = (int64_t)entry(r, pos / A.page) * A.page + pos % A.page;
+                    const uint32_t col = (uint32_t)pos / (uint32_t)A.page;
+                    slot = (int64_t)entry(r, (int)col) * A.page + (pos - (int)col * A.page);
                 }
                 A.slots[i] = slot;
                 A.positions[i] = pos;
@@ -229,18 +232,19 @@ int paged_tables(const int32_t *held, const int32_t *window, const int32_t *emit
 // Codes.  A key next to the border of two codes must get the code that exact arithmetic gives, or
 // the cache would depend on how the angle was rounded.  Keys are therefore carried as sums of two
 // floats with an error bound of 2^-27 (|x_a| + |x_b|) (none for values and for unrotated dimensions);
-// where a block's scale or one of its codes could still change within it, about once in 10^4 key heads,
-// the warp redoes the head in fp64 from the same integer angle.  (With plain fp32 keys it was once
-// in 10^3, and a batch of 256 tokens waited 6 to 9 us for the one or two warps concerned.)  Borders are
+// where a block's scale or one of its codes could still change within it (by the bound, about once in 10^4
+// key heads; ten times as often with plain fp32 keys, for which a batch of 256 tokens took 16.5 us instead
+// of 11.5 with the read-back), the warp redoes the head in fp64 from the same integer angle.  Borders are
 // (n - 8.5) d, exact in fp32 because d has eight significant bits, so a code is settled by comparing
 // against them and no division is rounded.
 //
 // Split.  A CTA of four warps takes a token, its warps every fourth head, four heads fetched ahead;
 // calls of few tokens spread a token's heads over several CTAs.  4099 tokens of 32 + 2 x 8 heads in
-// bf16 take 41 us (88 MB, 2.1 TB/s), 256 tokens of 40 + 2 x 8 in fp32 8 us: what bounds them is issue (73 %
-// at 200 instructions a head: a query head takes 24 beside the loop's 25, a value head 240, a key head 440).
-// Eight warps to a CTA: 51.4 us with the read-back against 50.4; six or seven CTAs to an SM 55 and 53; a warp a
-// head and no loop 89.
+// bf16 take 41 us (88 MB, 2.2 TB/s), 256 tokens of 40 + 2 x 8 in fp32 8.7 us: what bounds the first is issue
+// (74 % at 173 warp instructions a head on average; before branches left the loops over dimensions, copies
+// with a part taken out counted 24 for a query head, 248 for a value head and 529 for a key head).
+// With the read-back 50.4 us; eight warps to a CTA 51.4, two 52.0; six or seven CTAs to an SM 54.9 and 52.5
+// (and 10.2 and 10.4 for the 256 tokens, against 11.0); a warp a head and no loop 89.
 constexpr int kApWarps = 4;
 
 struct RopeArgs {
@@ -705,7 +709,7 @@ int paged_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv,
 
 // ---- read-back -----------------------------------------------------------------------------
 // One warp per token and kv head; a lane's four dimensions of K and of V.  Bounded by its fp32 writes and
-// by latency: 4099 tokens of 8 heads (38 MB) in 9.6 us, 3.9 TB/s.
+// by latency: 4099 tokens of 8 heads (38 MB) in 10.3 us, 3.7 TB/s.
 __global__ void __launch_bounds__(256) paged_read_kernel(const int64_t *__restrict__ slots, int T, int Hkv,
                                                          const uint8_t *__restrict__ pages, int page,
                                                          int64_t n_slots, float *__restrict__ k,
