@@ -26,7 +26,7 @@ def test_wrappers_convert_sizes_and_addresses(size):
              lambda: svd.svd_paged_append(a, size(768), n, n, n, a, a, size(17), n, a, dtype=size(0), stream=0),
              lambda: svd.svd_paged_tables(a, None, None, a, n, size(17), a, n, a, a, n, a, a, a, a, a, a, a, n, a, stream=0),
              lambda: svd.svd_paged_attention(a, n, a, a, n, n, a, n, a, size(17), n, n, n, size(1), a, size(0), a, n, stream=0),
-             lambda: svd.svd_kv_unpack(a, size(17), n, size(0), n, a, a, a, a, n, stream=0)]
+             lambda: svd.svd_kv_unpack(a, size(-1), n, size(0), n, a, a, a, a, n, stream=0)]
     for call in calls:
         with pytest.raises(svd.SvdError, match="INVALID_ARG"):
             call()
