@@ -493,10 +493,10 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             }
             ++n_seg;
         }
-        // After a give-up: the copies in flight land before the CTA ends.
-        if (pa_stopped(&s_ctl))
-            for (int j = max(0, k - A.stages); j < k; ++j)
-                mbar_wait_ok(b_full + 8 * (j % A.stages), (uint32_t)(j / A.stages) & 1u);
+        // Whatever the other warps do (one may still give up a wait once this one has no more to copy), the
+        // copies in flight land before the CTA ends.
+        for (int j = max(0, k - A.stages); j < k; ++j)
+            mbar_wait_ok(b_full + 8 * (j % A.stages), (uint32_t)(j / A.stages) & 1u);
         __syncwarp();
     } else if (warp == kSWarp) {
         // ---- S = K Q^T ---------------------------------------------------------------------

@@ -1,0 +1,68 @@
+"""The paged calls on the GPU in cases that once went wrong, against the fp64 reference: waits that give up
+with the copies of a short range in flight."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as ref
+from speculative_decoding_verify_06_gb300 import svd
+from tests.gpu_helpers import DEV, lib, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    lib()
+
+
+def random_pool(g, n_pages, Hkv, page):
+    """Pages of normal keys and values."""
+    pool = np.zeros((n_pages, Hkv, page // 16, ref.UNIT), np.uint8)
+    n = n_pages * page
+    return ref.put(pool, np.arange(n), g.normal(size=(n, Hkv, 128)), g.normal(size=(n, Hkv, 128)), page)
+
+
+class Attend:
+    """One attention call: lens and new tokens of each request, its pages in order unless a table is given."""
+
+    def __init__(self, lens, new, Hq, Hkv, page, out_dtype=svd.SVD_BF16, seed=0, pool=None, table=None, q=None):
+        g = np.random.default_rng(seed)
+        have = [-(-x // page) for x in lens]
+        if table is None:
+            table = np.full((len(lens), max(have)), -1, np.int32)
+            for r, n in enumerate(have):
+                table[r, :n] = sum(have[:r]) + np.arange(n)
+        self.lens, self.page, self.Hq, self.Hkv, self.out_dtype, self.table = lens, page, Hq, Hkv, out_dtype, table
+        self.pool = random_pool(g, sum(have), Hkv, page) if pool is None else pool
+        self.q_start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        self.T, self.most, self.scale = int(self.q_start[-1]), max(new), 128 ** -0.5
+        self.q = torch.from_numpy(g.normal(size=(self.T, Hq, 128)) if q is None else q).to(torch.bfloat16)
+        self.dev = [self.q.to(DEV), to_dev(np.array(lens, np.int32)), to_dev(self.q_start), to_dev(table), to_dev(self.pool.reshape(-1))]
+        self.ws = torch.zeros(svd.svd_paged_attention_workspace_bytes(Hq, Hkv, len(lens), self.most), dtype=torch.uint8, device=DEV)
+        self.out = torch.full((self.T, Hq, 128), -7.0, dtype=torch.bfloat16 if out_dtype == svd.SVD_BF16 else torch.float32,
+                              device=DEV)
+
+    def run(self):
+        q, lens, starts, table, pool = self.dev
+        svd.svd_paged_attention(q, self.T, lens, starts, len(self.lens), self.most, table, table.shape[1], pool, self.page,
+                                self.pool.shape[0], self.Hq, self.Hkv, self.scale, self.out, self.out_dtype, self.ws)
+        torch.cuda.synchronize()
+        return self.out.double().cpu().numpy()
+
+    def reference(self):
+        return ref.attention(self.q.double().numpy(), self.pool, self.page, self.table, self.lens, self.q_start, self.scale)
+
+
+@pytest.mark.parametrize("polls", [1, 2, 5])
+@pytest.mark.parametrize("lens,new,Hq", [([130, 260], [1, 4], 10), ([100] * 40, [3] * 40, 10), ([700, 900], [40, 70], 8), ([40], [1], 2)])
+def test_waits_that_give_up_after_the_last_copy_is_issued(lens, new, Hq, polls):
+    """Ranges of no more tiles than the ring has stages: the copying warp never waits.  It must still let
+    its copies land, and the next calls (over the same shared memory) give what they gave before."""
+    c = Attend(lens, new, Hq, 2, 32)
+    want = c.run()
+    for _ in range(3):
+        c.ws[:8].view(torch.int32)[1] = polls
+        c.run()
+        c.ws[:8] = 0
+        assert np.array_equal(c.run(), want) and not c.ws[:4].any()
