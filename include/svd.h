@@ -452,7 +452,8 @@ int svd_kv_attention(const uint16_t *q, const void *cache, int capacity, int n_q
  *   heads of 128 (fp32 or bf16; 16-byte aligned, ld a multiple of 4).  Queries and keys are rotated:
  *   pair i of dimensions, (i, i + n_pairs) or, interleaved, (2i, 2i + 1), turns by
  *   positions[axis[i] * positions_ld + t] * inv_freq[i] radians (axes: time, height and width of
- *   an image token, or one); dimensions past 2 n_pairs stay; rope NULL rotates nothing.  Queries go
+ *   an image token, or one; positions_ld 0: one row of positions for all axes, as text tokens have);
+ *   dimensions past 2 n_pairs stay; rope NULL rotates nothing.  Queries go
  *   to q, bf16 [T][Hq][128]; keys and values are stored at slots[t] (negative: not stored).  Per
  *   block of 32: m = the value of largest magnitude (the lowest dimension on ties), d = m / -8
  *   rounded to eight significant bits, then to fp16, c = floor(x / d + 8.5) limited to 0..15 (8 when

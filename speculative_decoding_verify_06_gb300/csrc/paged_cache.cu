@@ -684,7 +684,7 @@ int paged_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv,
     if (rope) {
         const svd_rope &r = *rope;
         if (!positions || r.n_pairs < 4 || r.n_pairs > SVD_ROPE_MAX_PAIRS || r.n_pairs % 4 || r.n_axes < 1 ||
-            r.n_axes > SVD_ROPE_MAX_AXES || (r.n_axes > 1 && positions_ld < T))
+            r.n_axes > SVD_ROPE_MAX_AXES || (r.n_axes > 1 && positions_ld != 0 && positions_ld < T))
             return SVD_ERR_INVALID_ARG;
         A.rope.pairs = r.n_pairs;
         A.rope.interleaved = r.interleaved != 0;

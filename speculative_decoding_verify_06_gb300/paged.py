@@ -71,15 +71,33 @@ class PagedBatch:
         torch.sub(self.q_start[1:], self.q_start[:-1], out=self.window)
         self.now = b
 
+    def _positions(self, positions, T: int):
+        """The positions of layer() and the distance of their axes (0: one row for all of them)."""
+        if positions is None:
+            return self.positions, 0
+        axes = 1 if self.rope is None else self.rope.n_axes
+        if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] < T:
+            raise ValueError(f"positions: int32 [{axes}][{T}] or [{T}]")
+        if positions.dim() == 1:
+            row, ld = positions, 0
+        else:
+            if positions.shape[0] < axes:
+                raise ValueError(f"positions: {positions.shape[0]} axes, the rotary positions have {axes}")
+            row, ld = positions[0], positions.stride(0) if axes > 1 else 0
+        if row.shape[0] > 1 and row.stride(0) != 1:
+            raise ValueError("positions: an axis lies in one piece")
+        return positions, ld
+
     def layer(self, l: int, qkv, out, n_tokens: int | None = None, positions=None, stream=None):
         """Layer l's step: rotates and stores qkv [n_tokens][(Hq + 2 Hkv) * 128] (fp32, as
         svd_verify_linear writes it, or bf16) and writes its attention to out [n_tokens][Hq][128].
-        positions [axes][n_tokens] replaces the requests' own positions (images: time, height, width)."""
+        positions, int32 [axes][n_tokens] (images: time, height, width) or [n_tokens] for all axes alike,
+        replaces the requests' own positions, which are the same on every axis."""
         T = self.max_tokens if n_tokens is None else n_tokens
-        pos = self.positions if positions is None else positions
+        pos, pos_ld = self._positions(positions, T)
         pool = self.pools[l]
         svd.svd_paged_append(qkv, qkv.stride(0), T, self.Hq, self.Hkv, self.slots, pool, self.page, self.n_pages, self.q,
-                             rope=self.rope, positions=pos, positions_ld=pos.shape[-1],
+                             rope=self.rope, positions=pos, positions_ld=pos_ld,
                              dtype=svd.SVD_F32 if qkv.dtype == torch.float32 else svd.SVD_BF16, status=self.bad,
                              stream=stream)
         svd.svd_paged_attention(self.q, T, self.kv_len, self.q_start, self.R, self.max_window, self.table[self.now], self.width,

@@ -131,6 +131,10 @@ class Rope:
         self._s.n_pairs, self._s.n_axes, self._s.interleaved = len(inv), int(n_axes), int(bool(interleaved))
         self._p = ctypes.addressof(self._s)
 
+    @property
+    def n_axes(self) -> int:
+        return self._s.n_axes
+
 
 class Sampler:
     def __init__(self, temperature=0.6, top_p=0.95, min_p=0.05, greedy=False):

@@ -1,11 +1,11 @@
 """The paged calls on the GPU in cases that once went wrong, against the fp64 reference: waits that give up
-with the copies of a short range in flight."""
+with the copies of a short range in flight; one row of positions for several axes."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import paged as ref
-from speculative_decoding_verify_06_gb300 import svd
+from speculative_decoding_verify_06_gb300 import paged, svd
 from tests.gpu_helpers import DEV, lib, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +66,26 @@ def test_waits_that_give_up_after_the_last_copy_is_issued(lens, new, Hq, polls):
         c.run()
         c.ws[:8] = 0
         assert np.array_equal(c.run(), want) and not c.ws[:4].any()
+
+
+@pytest.mark.parametrize("given", [None, "row", "axes"])
+def test_a_step_with_several_axes(given):
+    """Text tokens turn by the same position on every axis, image tokens by each axis' own."""
+    g = np.random.default_rng(2)
+    T, Hq, Hkv, page, n = 9, 3, 1, 16, 64
+    inv, axis = 100.0 ** (-np.arange(n) / n), np.arange(n) % 3
+    b = paged.PagedBatch(2, 1, n_pages=8, page_size=page, max_len=64, max_window=5, n_q_heads=Hq, n_kv_heads=Hkv,
+                         rope=svd.Rope(inv, axis, 3))
+    b.begin(torch.tensor([4, 5], dtype=torch.int32, device=DEV))
+    text = np.array([0, 1, 2, 3, 0, 1, 2, 3, 4])
+    pos = {None: np.stack([text] * 3), "row": np.stack([text + 7] * 3), "axes": g.integers(0, 5000, (3, T))}[given]
+    x = g.normal(size=(T, 5, 128)).astype(np.float32)
+    arg = None if given is None else to_dev(pos[0].astype(np.int32) if given == "row" else pos.astype(np.int32))
+    out = torch.zeros((T, Hq, 128), dtype=torch.bfloat16, device=DEV)
+    b.layer(0, to_dev(x.reshape(T, -1)), out, n_tokens=T, positions=arg)
+    y = ref.rotate(x.astype(np.float64), pos, inv, axis, False)
+    q = b.q[:T].double().cpu().numpy()
+    # bf16's rounding, and the rotation before it
+    assert np.all(np.abs(q - y[:, :Hq]) <= 2.0 ** -8 * np.abs(y[:, :Hq]) + 2.0 ** -17)
+    want = ref.put(np.zeros((8, Hkv, 1, ref.UNIT), np.uint8), b.slots[:T].cpu().numpy(), y[:, Hq:Hq + 1], x[:, Hq + 1:].astype(float), page)
+    assert np.array_equal(b.pools[0].cpu().numpy().reshape(want.shape), want) and not b.bad.any()

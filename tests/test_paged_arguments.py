@@ -1,10 +1,12 @@
 """What the binding and PagedBatch hand to the library, without a GPU."""
 import enum
+import inspect
 
 import numpy as np
 import pytest
+import torch
 
-from speculative_decoding_verify_06_gb300 import build, svd
+from speculative_decoding_verify_06_gb300 import build, paged, svd
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -30,3 +32,60 @@ def test_wrappers_convert_sizes_and_addresses(size):
     for call in calls:
         with pytest.raises(svd.SvdError, match="INVALID_ARG"):
             call()
+
+
+# ---- PagedBatch: what its calls are given -----------------------------------------------------------
+@pytest.fixture
+def calls(monkeypatch):
+    """Every call of the paged entry points, recorded instead of made."""
+    made = []
+
+    def record(name):
+        f = inspect.signature(getattr(svd, name))
+
+        def call(*a, **k):
+            b = f.bind(*a, **k)
+            b.apply_defaults()
+            made.append((name, b.arguments))
+        monkeypatch.setattr(svd, name, call)
+    for name in ("svd_paged_tables", "svd_paged_append", "svd_paged_attention"):
+        record(name)
+    return made
+
+
+def batch(**kw):
+    a = dict(requests=3, layers=1, n_pages=12, page_size=16, max_len=64, max_window=4, n_q_heads=4, n_kv_heads=2, device="cpu")
+    return paged.PagedBatch(**{**a, **kw})
+
+
+def rows(T, heads=8, dtype=torch.float32):
+    return torch.zeros((T, heads * 128), dtype=dtype), torch.zeros((T, 4, 128), dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("axes", [1, 2, 3, 4])
+@pytest.mark.parametrize("given", [None, "row", "axes", "wide", "expanded"])
+def test_every_axis_has_its_positions(calls, axes, given):
+    b = batch(rope=svd.Rope([0.1] * 8, [i % axes for i in range(8)], axes))
+    T = 9
+    pos = {None: None, "row": torch.zeros(T, dtype=torch.int32), "axes": torch.zeros((axes, T), dtype=torch.int32),
+           "wide": torch.zeros((axes + 1, T + 5), dtype=torch.int32), "expanded": torch.zeros(T, dtype=torch.int32).expand(axes, T)}[given]
+    qkv, out = rows(T)
+    b.layer(0, qkv, out, n_tokens=T, positions=pos)
+    a = dict(calls)["svd_paged_append"]
+    held, ld = a["positions"], a["positions_ld"]
+    end = held.untyped_storage().nbytes() // 4
+    # the last position that the call reads lies in the tensor, and axes do not lie inside each other
+    assert held.storage_offset() + (axes - 1) * ld + a["n_tokens"] <= end and (ld == 0 or ld >= T)
+    if given in ("axes", "wide") and axes > 1:
+        assert ld == pos.stride(0)
+
+
+@pytest.mark.parametrize("pos", [torch.zeros(9), torch.zeros((2, 9), dtype=torch.int32), torch.zeros(8, dtype=torch.int32),
+                                 torch.zeros((3, 9), dtype=torch.int64), torch.zeros((3, 18), dtype=torch.int32)[:, ::2],
+                                 torch.zeros((1, 3, 9), dtype=torch.int32)])
+def test_positions_of_another_form_are_refused(calls, pos):
+    b = batch(rope=svd.Rope([0.1] * 9, [0, 1, 2] * 3, 3))
+    qkv, out = rows(9)
+    with pytest.raises(ValueError, match="positions"):
+        b.layer(0, qkv, out, n_tokens=9, positions=pos)
+    assert not calls
