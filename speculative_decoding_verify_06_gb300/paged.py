@@ -92,8 +92,16 @@ class PagedBatch:
         """Layer l's step: rotates and stores qkv [n_tokens][(Hq + 2 Hkv) * 128] (fp32, as
         svd_verify_linear writes it, or bf16) and writes its attention to out [n_tokens][Hq][128].
         positions, int32 [axes][n_tokens] (images: time, height, width) or [n_tokens] for all axes alike,
-        replaces the requests' own positions, which are the same on every axis."""
-        T = self.max_tokens if n_tokens is None else n_tokens
+        replaces the requests' own positions, which are the same on every axis.  n_tokens: the rows of qkv
+        that count (None: all of them, up to max_tokens); it covers the step's tokens, q_start's last entry."""
+        T = min(qkv.shape[0], self.max_tokens) if n_tokens is None else int(n_tokens)
+        width = (self.Hq + 2 * self.Hkv) * 128
+        if not 0 <= T <= self.max_tokens:
+            raise ValueError(f"{T} tokens, the batch was made for {self.max_tokens}")
+        if qkv.dim() != 2 or qkv.shape[0] < T or qkv.shape[1] < width or qkv.stride(1) != 1:
+            raise ValueError(f"qkv: {T} rows of {width}, got {tuple(qkv.shape)} with strides {qkv.stride()}")
+        if out.numel() < T * self.Hq * 128 or not out.is_contiguous():
+            raise ValueError(f"out: [{T}][{self.Hq}][128] in one piece, got {tuple(out.shape)}")
         pos, pos_ld = self._positions(positions, T)
         pool = self.pools[l]
         svd.svd_paged_append(qkv, qkv.stride(0), T, self.Hq, self.Hkv, self.slots, pool, self.page, self.n_pages, self.q,

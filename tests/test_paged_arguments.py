@@ -89,3 +89,30 @@ def test_positions_of_another_form_are_refused(calls, pos):
     with pytest.raises(ValueError, match="positions"):
         b.layer(0, qkv, out, n_tokens=9, positions=pos)
     assert not calls
+
+
+@pytest.mark.parametrize("given,tokens", [(5, None), (12, None), (20, None), (9, 7), (0, None), (4, 0)])
+def test_as_many_tokens_as_there_are_rows(calls, given, tokens):
+    b = batch()  # 12 tokens at most
+    qkv, out = rows(given)
+    b.layer(0, qkv, out, n_tokens=tokens)
+    for name, a in calls:
+        assert a["n_tokens"] == (min(given, 12) if tokens is None else tokens), name
+
+
+@pytest.mark.parametrize("change", [
+    dict(n_tokens=13), dict(n_tokens=-1), dict(n_tokens=8, rows=7), dict(n_tokens=8, out=7), dict(out=11), dict(heads=7),
+    dict(strided=True), dict(loose=True), dict(flat=True)])
+def test_rows_that_do_not_suffice_are_refused(calls, change):
+    b = batch()
+    qkv, _ = rows(change.get("rows", 20), change.get("heads", 8))
+    out = torch.zeros((change.get("out", 20), 4, 128), dtype=torch.bfloat16)
+    if "strided" in change:
+        qkv = torch.zeros((1024, 20)).t()
+    if "loose" in change:
+        out = torch.zeros((20, 8, 128), dtype=torch.bfloat16)[:, :4]
+    if "flat" in change:
+        qkv = qkv.reshape(-1)
+    with pytest.raises(ValueError, match="tokens|qkv|out"):
+        b.layer(0, qkv, out, n_tokens=change.get("n_tokens"))
+    assert not calls
