@@ -63,6 +63,9 @@ class PagedBatch:
         """Opens a step of n_new [R] new tokens for each request, after `emitted` [R] of the last
         step's tokens were kept (None: all of them).  Requests that cannot be served have a status
         and no tokens; they keep what they hold."""
+        self._counts("n_new", n_new)
+        if emitted is not None:
+            self._counts("emitted", emitted)
         a, b = self.now, 1 - self.now
         svd.svd_paged_tables(self.held[a], None if emitted is None else self.window, emitted, n_new, self.R,
                              self.page, self.table[a], self.width, self.free[a], self.n_free[a], self.n_pages,
@@ -71,13 +74,24 @@ class PagedBatch:
         torch.sub(self.q_start[1:], self.q_start[:-1], out=self.window)
         self.now = b
 
+    def _here(self, name: str, t, *dtypes):
+        """The library takes addresses: a tensor of another type or place would be read as it lies."""
+        if t.dtype not in dtypes or t.device != self.q_start.device:
+            raise ValueError(f"{name}: {' or '.join(str(d) for d in dtypes)} on {self.q_start.device}, got {t.dtype} on {t.device}")
+
+    def _counts(self, name: str, t):
+        self._here(name, t, torch.int32)
+        if t.shape != (self.R,) or not t.is_contiguous():
+            raise ValueError(f"{name}: [{self.R}] in one piece, got {tuple(t.shape)}")
+
     def _positions(self, positions, T: int):
         """The positions of layer() and the distance of their axes (0: one row for all of them)."""
         if positions is None:
             return self.positions, 0
         axes = 1 if self.rope is None else self.rope.n_axes
-        if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] < T:
-            raise ValueError(f"positions: int32 [{axes}][{T}] or [{T}]")
+        self._here("positions", positions, torch.int32)
+        if positions.dim() not in (1, 2) or positions.shape[-1] < T:
+            raise ValueError(f"positions: [{axes}][{T}] or [{T}], got {tuple(positions.shape)}")
         if positions.dim() == 1:
             row, ld = positions, 0
         else:
@@ -98,6 +112,8 @@ class PagedBatch:
         width = (self.Hq + 2 * self.Hkv) * 128
         if not 0 <= T <= self.max_tokens:
             raise ValueError(f"{T} tokens, the batch was made for {self.max_tokens}")
+        self._here("qkv", qkv, torch.float32, torch.bfloat16)
+        self._here("out", out, torch.float32 if self.out_dtype == svd.SVD_F32 else torch.bfloat16)
         if qkv.dim() != 2 or qkv.shape[0] < T or qkv.shape[1] < width or qkv.stride(1) != 1:
             raise ValueError(f"qkv: {T} rows of {width}, got {tuple(qkv.shape)} with strides {qkv.stride()}")
         if out.numel() < T * self.Hq * 128 or not out.is_contiguous():

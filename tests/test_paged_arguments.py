@@ -116,3 +116,30 @@ def test_rows_that_do_not_suffice_are_refused(calls, change):
     with pytest.raises(ValueError, match="tokens|qkv|out"):
         b.layer(0, qkv, out, n_tokens=change.get("n_tokens"))
     assert not calls
+
+
+@pytest.mark.parametrize("kind", [torch.float16, torch.float64, torch.int32])
+def test_activations_of_another_type_are_refused(calls, kind):
+    qkv, out = rows(4, dtype=kind)
+    with pytest.raises(ValueError, match="qkv"):
+        batch().layer(0, qkv, out)
+    assert not calls
+
+
+@pytest.mark.parametrize("made,given", [(svd.SVD_F32, torch.bfloat16), (svd.SVD_BF16, torch.float32), (svd.SVD_BF16, torch.float16)])
+def test_outputs_have_the_type_the_batch_was_made_for(calls, made, given):
+    qkv, out = rows(4)
+    with pytest.raises(ValueError, match="out"):
+        batch(out_dtype=made).layer(0, qkv, out.to(given))
+    assert not calls
+
+
+@pytest.mark.parametrize("n_new", [torch.ones(3, dtype=torch.int64), torch.ones(2, dtype=torch.int32), torch.ones(3),
+                                   torch.ones(6, dtype=torch.int32)[::2], torch.ones((3, 1), dtype=torch.int32),
+                                   torch.ones(3, dtype=torch.int32, device="meta")])
+def test_counts_of_another_form_are_refused(calls, n_new):
+    good = torch.ones(3, dtype=torch.int32)
+    for a in ((n_new, None), (good, n_new)):
+        with pytest.raises(ValueError, match="n_new|emitted"):
+            batch().begin(*a)
+    assert not calls
