@@ -71,7 +71,9 @@ class PagedBatch:
                              self.page, self.table[a], self.width, self.free[a], self.n_free[a], self.n_pages,
                              self.table[b], self.free[b], self.n_free[b], self.held[b], self.q_start, self.slots,
                              self.positions, self.max_tokens, self.status, stream=stream)
-        torch.sub(self.q_start[1:], self.q_start[:-1], out=self.window)
+        on = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        with torch.cuda.stream(on):  # (None: the current one)
+            torch.sub(self.q_start[1:], self.q_start[:-1], out=self.window)
         self.now = b
 
     def _here(self, name: str, t, *dtypes):
