@@ -448,6 +448,14 @@ int svd_kv_attention(const uint16_t *q, const void *cache, int capacity, int n_q
  *   the row as held).  After a request with status, pass its old held again.
  *   Outputs must not be the inputs.  R <= SVD_PAGED_MAX_REQUESTS; max_pages * page_size and
  *   R * max_pages < 2^31; n_pages, max_tokens <= 2^30.
+ * svd_paged_advance: svd_paged_tables for a program that carries the state from call to call on the GPU
+ *   without looking at it: held and window [R] are what the last call wrote to held_out and window_out
+ *   (zeros before the first).  window > 0: the tokens added by the last call, of which emitted [R] stay
+ *   (NULL: all); window <= 0: -window positions go and emitted says nothing (a request that had
+ *   no tokens has no count; window = -held, n_new = 0 ends a request).  A request with status keeps its pages:
+ *   held_out = held; window_out is minus what is rejected, so that its count is not asked for again, or
+ *   window itself if the count was out of order.  kv_len is keep + the tokens granted (held - window where the
+ *   count was out of order).
  * svd_paged_append: for every token t the row qkv[t * ld ..] holds Hq query, Hkv key and Hkv value
  *   heads of 128 (fp32 or bf16; 16-byte aligned, ld a multiple of 4).  Queries and keys are rotated:
  *   pair i of dimensions, (i, i + n_pairs) or, interleaved, (2i, 2i + 1), turns by
@@ -498,6 +506,12 @@ int svd_paged_tables(const int32_t *held, const int32_t *window, const int32_t *
                      int32_t *table_out, int32_t *free_out, int32_t *n_free_out, int32_t *kv_len,
                      int32_t *q_start, int64_t *slots, int32_t *positions, int64_t max_tokens,
                      int32_t *status, svd_stream_t stream);
+int svd_paged_advance(const int32_t *held, const int32_t *window, const int32_t *emitted,
+                      const int32_t *n_new, int n_requests, int page_size, const int32_t *table,
+                      int max_pages, const int32_t *free_ids, const int32_t *n_free, int64_t n_pages,
+                      int32_t *held_out, int32_t *window_out, int32_t *table_out, int32_t *free_out,
+                      int32_t *n_free_out, int32_t *kv_len, int32_t *q_start, int64_t *slots,
+                      int32_t *positions, int64_t max_tokens, int32_t *status, svd_stream_t stream);
 int svd_paged_append(const void *qkv, int dtype, int64_t ld, int n_tokens, int n_q_heads,
                      int n_kv_heads, const svd_rope *rope, const int32_t *positions,
                      int64_t positions_ld, const int64_t *slots, void *pages, int page_size,

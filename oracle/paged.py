@@ -68,6 +68,28 @@ def tables(held, window, emitted, n_new, page, table, free, n_free, max_tokens):
                 status=np.array(status, np.int32))
 
 
+def advance(held, window, emitted, n_new, page, table, free, n_free, max_tokens):
+    """tables() with the state carried: also held and window of the next call."""
+    R = len(held)
+    win, kept, odd = [], [], []
+    for r in range(R):
+        w, h = int(window[r]), int(held[r])
+        e = (w if emitted is None else int(emitted[r])) if w > 0 else 0
+        win.append(abs(w))
+        kept.append(e)
+        odd.append(not 0 <= e <= abs(w) <= h)
+    o = tables(held, win, kept, n_new, page, table, free, n_free, max_tokens)
+    o["held"], o["window"] = np.zeros(R, np.int32), np.zeros(R, np.int32)
+    for r in range(R):
+        keep = int(held[r]) - win[r] + (0 if odd[r] else kept[r])
+        if o["status"][r] == 0:
+            o["held"][r], o["window"][r] = keep + int(n_new[r]), int(n_new[r])
+        else:
+            o["held"][r], o["window"][r] = held[r], window[r] if odd[r] else kept[r] - win[r]
+            o["kv_len"][r] = max(keep, 0)
+    return o
+
+
 def rotate(x, positions, inv_freq, axis, interleaved):
     """x [T, heads, 128] fp64; positions [axes, T]."""
     y = x.copy()

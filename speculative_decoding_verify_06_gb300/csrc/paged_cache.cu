@@ -31,7 +31,29 @@ struct TbArgs {
     int32_t *table_out, *free_out, *n_free_out, *kv_len, *q_start, *positions, *status;
     int64_t *slots;
     int R, page, width, n_pages, tokens;
+    int32_t *held_out, *window_out;  // the state carried to the next call, or null: see tb_ask
 };
+
+// What request r asks for: the positions held, the tokens of the last window and how many of them
+// stay.  Where the state is carried, a window of -d says that d positions go (its count is settled),
+// and a request without a window has no count.
+struct TbAsk {
+    long long held, win, emi;
+    __device__ bool in_order() const { return win >= 0 && emi >= 0 && emi <= win && win <= held; }
+};
+__device__ __forceinline__ TbAsk tb_ask(const TbArgs &A, int r) {
+    TbAsk a = {A.held[r], 0, 0};
+    if (!A.window) return a;
+    a.win = A.window[r];
+    if (!A.held_out) {
+        a.emi = A.emitted[r];
+    } else if (a.win > 0) {
+        a.emi = A.emitted ? A.emitted[r] : a.win;
+    } else {
+        a.win = -a.win;
+    }
+    return a;
+}
 
 // Inclusive sum over the block of one 64-bit value per thread; *total gets the block's sum.
 __device__ __forceinline__ unsigned long long tb_scan(unsigned long long v, unsigned long long *total,
@@ -82,14 +104,14 @@ __global__ void __launch_bounds__(kTbThreads) paged_tables_kernel(const TbArgs A
         long long keep = 0;
         uint32_t st = 0, ask = 0, p0 = 0, p1 = 0;
         if (r < R) {
-            const long long held = A.held[r], n = A.n_new[r];
-            const long long win = A.window ? A.window[r] : 0, emi = A.window ? A.emitted[r] : 0;
+            const TbAsk a = tb_ask(A, r);
+            const long long n = A.n_new[r];
             const long long room = (long long)A.width * A.page;  // < 2^31
-            keep = held - win + emi;
-            if (win < 0 || emi < 0 || emi > win || win > held || n < 0 || held > room || keep + n > room) {
+            keep = a.held - a.win + a.emi;
+            if (!a.in_order() || n < 0 || a.held > room || keep + n > room) {
                 st = SVD_ST_BAD_REQUEST;
             } else {
-                p0 = ((uint32_t)held + A.page - 1) / (uint32_t)A.page;
+                p0 = ((uint32_t)a.held + A.page - 1) / (uint32_t)A.page;
                 p1 = ((uint32_t)(keep + n) + A.page - 1) / (uint32_t)A.page;
                 ask = (uint32_t)n;
             }
@@ -155,9 +177,20 @@ __global__ void __launch_bounds__(kTbThreads) paged_tables_kernel(const TbArgs A
     if (blockIdx.x == 0) {
         for (int r = tid; r < R; r += kTbThreads) {
             const uint32_t st = s_st[r];
-            A.kv_len[r] = st == SVD_ST_BAD_REQUEST ? 0 : st ? s_keep[r] : s_keep[r] + A.n_new[r];
+            const int n = st ? 0 : A.n_new[r];
             A.q_start[r] = s_tok[r];
             A.status[r] = (int)st;
+            if (!A.held_out) {
+                A.kv_len[r] = st == SVD_ST_BAD_REQUEST ? 0 : s_keep[r] + n;
+            } else {
+                // A refused request holds what it held; its count is settled if it was in order, and
+                // else asked for again (what stays for certain is counted).
+                const TbAsk a = tb_ask(A, r);
+                const bool good = a.in_order();
+                A.kv_len[r] = good ? s_keep[r] + n : (int)max(a.held - a.win, 0ll);
+                A.held_out[r] = st ? (int)a.held : s_keep[r] + n;
+                A.window_out[r] = !st ? n : good ? (int)(a.emi - a.win) : A.window[r];
+            }
         }
         if (tid == 0) {
             A.q_start[R] = n_tok;
@@ -192,31 +225,50 @@ __global__ void __launch_bounds__(kTbThreads) paged_tables_kernel(const TbArgs A
     }
 }
 
+static int tb_launch(TbArgs A, int64_t n_pages, int64_t tokens, cudaStream_t stream) {
+    if (!A.held || !A.n_new || !A.table || !A.free_ids || !A.n_free || !A.table_out || !A.free_out || !A.n_free_out ||
+        !A.kv_len || !A.q_start || !A.slots || !A.positions || !A.status)
+        return SVD_ERR_INVALID_ARG;
+    if (A.R < 1 || A.R > SVD_PAGED_MAX_REQUESTS || !pg_page_size_ok(A.page) || A.width < 1 ||
+        (int64_t)A.width * A.page > INT32_MAX || (int64_t)A.width * A.R > INT32_MAX || n_pages < 1 ||
+        n_pages > (int64_t)1 << 30 || tokens < 1 || tokens > (int64_t)1 << 30)
+        return SVD_ERR_INVALID_ARG;
+    if (A.table_out == A.table || A.free_out == A.free_ids || A.n_free_out == A.n_free) return SVD_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms < 1) return SVD_ERR_CUDA;
+    A.n_pages = (int)n_pages;
+    A.tokens = (int)tokens;
+    const size_t smem = (size_t)A.R * 25 + 8;
+    if (smem > 48 * 1024)
+        SVD_CUDA_TRY(allow_smem<paged_tables_kernel>((size_t)SVD_PAGED_MAX_REQUESTS * 25 + 8));
+    auto items = [](int64_t n) { return (n + kTbChunk - 1) / kTbChunk; };
+    const int64_t work = (int64_t)A.R * items(A.width) + items(n_pages) + items(tokens);
+    const int grid = (int)(work < 2 * sms ? work : 2 * sms);
+    SVD_CUDA_TRY(launch(paged_tables_kernel, dim3(grid), dim3(kTbThreads), smem, stream, true, A));
+    return SVD_OK;
+}
+
 int paged_tables(const int32_t *held, const int32_t *window, const int32_t *emitted, const int32_t *n_new,
                  int R, int page, const int32_t *table, int width, const int32_t *free_ids,
                  const int32_t *n_free, int64_t n_pages, int32_t *table_out, int32_t *free_out,
                  int32_t *n_free_out, int32_t *kv_len, int32_t *q_start, int64_t *slots,
                  int32_t *positions, int64_t tokens, int32_t *status, cudaStream_t stream) {
-    if (!held || !n_new || !table || !free_ids || !n_free || !table_out || !free_out || !n_free_out ||
-        !kv_len || !q_start || !slots || !positions || !status || (!window) != (!emitted))
-        return SVD_ERR_INVALID_ARG;
-    if (R < 1 || R > SVD_PAGED_MAX_REQUESTS || !pg_page_size_ok(page) || width < 1 ||
-        (int64_t)width * page > INT32_MAX || (int64_t)width * R > INT32_MAX || n_pages < 1 ||
-        n_pages > (int64_t)1 << 30 || tokens < 1 || tokens > (int64_t)1 << 30)
-        return SVD_ERR_INVALID_ARG;
-    if (table_out == table || free_out == free_ids || n_free_out == n_free) return SVD_ERR_INVALID_ARG;
-    const int sms = sm_count();
-    if (sms < 1) return SVD_ERR_CUDA;
-    const TbArgs A = {held, window, emitted, n_new, table, free_ids, n_free, table_out, free_out, n_free_out,
-                      kv_len, q_start, positions, status, slots, R, page, width, (int)n_pages, (int)tokens};
-    const size_t smem = (size_t)R * 25 + 8;
-    if (smem > 48 * 1024)
-        SVD_CUDA_TRY(allow_smem<paged_tables_kernel>((size_t)SVD_PAGED_MAX_REQUESTS * 25 + 8));
-    auto items = [](int64_t n) { return (n + kTbChunk - 1) / kTbChunk; };
-    const int64_t work = (int64_t)R * items(width) + items(n_pages) + items(tokens);
-    const int grid = (int)(work < 2 * sms ? work : 2 * sms);
-    SVD_CUDA_TRY(launch(paged_tables_kernel, dim3(grid), dim3(kTbThreads), smem, stream, true, A));
-    return SVD_OK;
+    if ((!window) != (!emitted)) return SVD_ERR_INVALID_ARG;
+    return tb_launch({held, window, emitted, n_new, table, free_ids, n_free, table_out, free_out, n_free_out, kv_len,
+                      q_start, positions, status, slots, R, page, width, 0, 0, nullptr, nullptr},
+                     n_pages, tokens, stream);
+}
+
+int paged_advance(const int32_t *held, const int32_t *window, const int32_t *emitted, const int32_t *n_new,
+                  int R, int page, const int32_t *table, int width, const int32_t *free_ids,
+                  const int32_t *n_free, int64_t n_pages, int32_t *held_out, int32_t *window_out,
+                  int32_t *table_out, int32_t *free_out, int32_t *n_free_out, int32_t *kv_len,
+                  int32_t *q_start, int64_t *slots, int32_t *positions, int64_t tokens, int32_t *status,
+                  cudaStream_t stream) {
+    if (!window || !held_out || !window_out || held_out == held || window_out == window) return SVD_ERR_INVALID_ARG;
+    return tb_launch({held, window, emitted, n_new, table, free_ids, n_free, table_out, free_out, n_free_out, kv_len,
+                      q_start, positions, status, slots, R, page, width, 0, 0, held_out, window_out},
+                     n_pages, tokens, stream);
 }
 
 // ---- rotary positions and the append -------------------------------------------------------

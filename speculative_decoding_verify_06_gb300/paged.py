@@ -2,7 +2,7 @@
 
 A step is what "100 tokens per second ..." ("How speculative decoding gets past a per-token wall")
 describes for one sequence, for a batch of them ("Why a hiring company is writing this"): the tables
-follow the tokens that the last acceptance kept (svd_paged_tables), every layer's queries and keys are
+follow the tokens that the last acceptance kept (svd_paged_advance), every layer's queries and keys are
 rotated and its keys and values appended (svd_paged_append), and the window's tokens attend to
 their requests' caches (svd_paged_attention).  Nothing of a step waits for the host: acceptance
 counts, lengths, page ids and free pages stay in device memory, so a step can be recorded.
@@ -22,7 +22,8 @@ class PagedBatch:
     """The caches of `requests` requests in `layers` pools of n_pages pages, one table for all layers.
 
     begin() opens a step, layer() runs one layer's append and attention.  Between two begin() calls
-    the device tensors q_start, kv_len, slots, positions and status describe the step's tokens."""
+    the device tensors q_start, kv_len, slots, positions and status describe the step's tokens; held and
+    window are the state that the next begin() goes on from."""
 
     def __init__(self, requests: int, layers: int, n_pages: int, page_size: int = 64, max_len: int = 32768,
                  max_window: int = 8, n_q_heads: int = 40, n_kv_heads: int = 8, rope: svd.Rope | None = None,
@@ -42,13 +43,14 @@ class PagedBatch:
         self.table = [torch.full((requests, self.width), -1, **i32) for _ in range(2)]
         self.free = [torch.arange(n_pages - 1, -1, -1, **i32) for _ in range(2)]  # page 0 on top
         self.n_free = [torch.full((1,), n_pages, **i32) for _ in range(2)]
-        self.held = [torch.zeros(requests, **i32) for _ in range(2)]
+        self.held = [torch.zeros(requests, **i32) for _ in range(2)]  # positions that the pages hold
+        self._window = [torch.zeros(requests, **i32) for _ in range(2)]
         self.now = 0
         self.q_start = torch.zeros(requests + 1, **i32)
         self.slots = torch.full((self.max_tokens,), -1, dtype=torch.int64, device=dev)
         self.positions = torch.full((self.max_tokens,), -1, **i32)
         self.status = torch.zeros(requests, **i32)
-        self.window = torch.zeros(requests, **i32)  # tokens of the step before
+        self.kv_len = torch.zeros(requests, **i32)
         self.ws = torch.zeros(svd.svd_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, requests, max_window),
                               dtype=torch.uint8, device=dev)
         self.q = torch.empty((self.max_tokens, n_q_heads, 128), dtype=torch.bfloat16, device=dev)
@@ -56,24 +58,24 @@ class PagedBatch:
         self.scale = 128 ** -0.5
 
     @property
-    def kv_len(self):
-        return self.held[self.now]
+    def window(self):
+        """Tokens of the step whose count of kept ones the next begin() takes; -d once d positions are
+        known to go."""
+        return self._window[self.now]
 
     def begin(self, n_new, emitted=None, stream=None):
         """Opens a step of n_new [R] new tokens for each request, after `emitted` [R] of the last
-        step's tokens were kept (None: all of them).  Requests that cannot be served have a status
-        and no tokens; they keep what they hold."""
+        step's tokens were kept (None: all of them; a request that had no tokens has no count).  Requests
+        that cannot be served have a status and no tokens; they keep what they hold, and the count of their
+        last window holds as given, unless it was out of order."""
         self._counts("n_new", n_new)
         if emitted is not None:
             self._counts("emitted", emitted)
         a, b = self.now, 1 - self.now
-        svd.svd_paged_tables(self.held[a], None if emitted is None else self.window, emitted, n_new, self.R,
-                             self.page, self.table[a], self.width, self.free[a], self.n_free[a], self.n_pages,
-                             self.table[b], self.free[b], self.n_free[b], self.held[b], self.q_start, self.slots,
-                             self.positions, self.max_tokens, self.status, stream=stream)
-        on = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-        with torch.cuda.stream(on):  # (None: the current one)
-            torch.sub(self.q_start[1:], self.q_start[:-1], out=self.window)
+        svd.svd_paged_advance(self.held[a], self._window[a], emitted, n_new, self.R, self.page, self.table[a], self.width,
+                              self.free[a], self.n_free[a], self.n_pages, self.held[b], self._window[b], self.table[b],
+                              self.free[b], self.n_free[b], self.kv_len, self.q_start, self.slots, self.positions,
+                              self.max_tokens, self.status, stream=stream)
         self.now = b
 
     def _here(self, name: str, t, *dtypes):

@@ -1,4 +1,5 @@
-"""The state that PagedBatch carries from step to step: every page in one place, on any stream."""
+"""The state that PagedBatch carries from step to step: refused requests lose nothing, every page is in one
+place, on any stream."""
 import numpy as np
 import pytest
 import torch
@@ -31,6 +32,134 @@ def whole(b):
     ids = np.concatenate([table[r, :n] for r, n in enumerate(have)] + [b.free[b.now].cpu().numpy()[:int(b.n_free[b.now])]])
     assert np.array_equal(np.sort(ids), np.arange(b.n_pages))
     assert all((table[r, n:] == -1).all() for r, n in enumerate(have))
+
+
+def test_carried_state_against_the_definitions():
+    """Whole outputs of the call, over random states and counts in and out of order."""
+    g = np.random.default_rng(7)
+    for R, page, width, spare, tokens in ((1, 16, 3, 2, 40), (37, 32, 6, 9, 150), (700, 16, 4, 200, 3000)):
+        held = g.integers(0, width * page + 1, R)
+        have = -(-held // page)
+        ids = g.permutation(int(have.sum()) + spare).astype(np.int32)
+        table = np.full((R, width), -1, np.int32)
+        table[np.arange(width) < have[:, None]] = ids[:have.sum()]
+        free = np.full(len(ids), -1, np.int32)
+        free[:spare] = ids[have.sum():]
+        window = np.minimum(held, g.integers(0, 12, R)) * g.choice([1, 1, -1], R)
+        window[g.random(R) < 0.1] += 1000
+        emitted = np.maximum(window, 0) - g.integers(-1, 4, R)
+        n_new = g.integers(-1, 20, R)
+        for kept in (emitted, None):
+            want = ref.advance(held, window, kept, n_new, page, table, free, spare, tokens)
+            d = {k: torch.full(np.shape(v) or (1,), -77, dtype=torch.int64 if k == "slots" else torch.int32, device=DEV)
+                 for k, v in want.items()}
+            ins = [None if a is None else i32(*a.reshape(-1).tolist()) for a in (held, window, kept, n_new, table, free)]
+            svd.svd_paged_advance(*ins[:4], R, page, ins[4], width, ins[5], i32(spare), len(ids), d["held"], d["window"],
+                                  d["table"], d["free"], d["n_free"], d["kv_len"], d["q_start"], d["slots"], d["positions"],
+                                  tokens, d["status"])
+            for k in want:
+                assert np.array_equal(d[k].cpu().numpy().reshape(np.shape(want[k])), want[k]), k
+
+
+def test_a_request_that_reaches_its_longest_keeps_its_cache():
+    b = batch(2)
+    b.begin(i32(60, 3))
+    row = b.table[b.now][0].tolist()
+    b.begin(i32(8, 2), i32(60, 3))  # 68 positions do not fit
+    assert b.status.tolist() == [svd.SVD_ST_BAD_REQUEST, 0] and b.q_start.tolist() == [0, 0, 2]
+    whole(b)
+    assert b.table[b.now][0].tolist() == row
+    for kept in (i32(0, 1), i32(5, 1)):  # counts of a request that had no tokens say nothing
+        b.begin(i32(8, 2), kept)
+        assert b.status.tolist() == [svd.SVD_ST_BAD_REQUEST, 0]
+        whole(b)
+    b.begin(i32(4, 0))
+    assert b.status.tolist() == [0, 0] and b.kv_len.tolist()[0] == 64 and b.positions[:4].tolist() == [60, 61, 62, 63]
+    assert b.table[b.now][0].tolist() == row
+    whole(b)
+
+
+def test_a_request_refused_for_pages_after_rejected_drafts():
+    b = batch(2, n_pages=4)
+    b.begin(i32(30, 10))
+    b.begin(i32(10, 0), i32(30, 10))  # request 0 holds 40: three pages; none is left
+    assert b.kv_len.tolist() == [40, 10] and int(b.n_free[b.now]) == 0
+    b.begin(i32(33, 0), i32(1, 0))    # of ten drafts one stays: 31, and 64 do not fit
+    assert b.status.tolist() == [svd.SVD_ST_NO_PAGES, 0] and b.kv_len.tolist() == [31, 10]
+    whole(b)
+    b.begin(i32(33, 0), i32(9, 3))    # refused again; the count was settled with the first refusal
+    assert b.status.tolist() == [svd.SVD_ST_NO_PAGES, 0] and b.kv_len.tolist() == [31, 10]
+    whole(b)
+    b.begin(i32(1, 0))                # 32 need two pages: the third goes back
+    assert b.status.tolist() == [0, 0] and b.kv_len.tolist() == [32, 10] and b.positions[0].item() == 31
+    assert int(b.n_free[b.now]) == 1
+    whole(b)
+
+
+def test_a_request_refused_for_tokens_after_rejected_drafts():
+    b = batch(2, max_tokens=20)
+    b.begin(i32(16, 4))
+    b.begin(i32(4, 16), i32(14, 4))
+    assert b.kv_len.tolist() == [18, 20]
+    b.begin(i32(10, 11), i32(1, 2))
+    assert b.status.tolist() == [0, svd.SVD_ST_NO_TOKENS] and b.kv_len.tolist() == [25, 6]
+    whole(b)
+    b.begin(i32(0, 1))
+    assert b.status.tolist() == [0, 0] and b.kv_len.tolist() == [25, 7] and b.positions[0].item() == 6
+    whole(b)
+
+
+def test_counts_out_of_order_are_asked_for_again():
+    b = batch(1)
+    b.begin(i32(20))
+    for bad in (i32(21), i32(-1)):
+        b.begin(i32(2), bad)
+        assert b.status.tolist() == [svd.SVD_ST_BAD_REQUEST]
+        whole(b)
+    b.begin(i32(2), i32(17))
+    assert b.status.tolist() == [0] and b.kv_len.tolist() == [19] and b.positions[:2].tolist() == [17, 18]
+    whole(b)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_many_steps_against_the_definitions(seed):
+    """Refusals of every kind, again and again, beside a list of the positions each request should hold."""
+    g = np.random.default_rng(seed)
+    R, page, n_pages, longest, tokens = 6, 16, 14, 80, 60
+    b = batch(R, n_pages=n_pages, max_len=longest, max_tokens=tokens, max_window=longest)
+    kept, last, seen = [0] * R, [0] * R, set()  # positions kept before the last window; the last window
+    for step in range(80):
+        emitted = [int(g.integers(0, w + 1)) if w else int(g.integers(0, 5)) for w in last]
+        wrong = g.random(R) < 0.05
+        given = [w + 1 if x and w else e for e, w, x in zip(emitted, last, wrong)]
+        n = [int(g.choice([0, 1, 4, 9, 30])) if g.random() < 0.97 else -1 for _ in range(R)]
+        b.begin(i32(*n), i32(*given))
+        status = b.status.tolist()
+        seen |= set(status)
+        for r in range(R):
+            if wrong[r] and last[r]:
+                assert status[r] == svd.SVD_ST_BAD_REQUEST
+                continue  # the window waits for its count
+            kept[r] += emitted[r] if last[r] else 0
+            last[r] = n[r] if status[r] == 0 else 0
+            assert (status[r] == svd.SVD_ST_BAD_REQUEST) == (n[r] < 0 or kept[r] + n[r] > longest)
+            assert b.kv_len.tolist()[r] == kept[r] + last[r]
+        granted = [n[r] if status[r] == 0 else 0 for r in range(R)]
+        assert b.q_start.tolist() == np.concatenate([[0], np.cumsum(granted)]).tolist()
+        table, pos, slots = b.table[b.now].cpu().numpy(), b.positions.tolist(), b.slots.tolist()
+        t = 0
+        for r in range(R):
+            for i in range(granted[r]):
+                assert pos[t] == kept[r] + i and slots[t] == table[r, pos[t] // page] * page + pos[t] % page
+                t += 1
+        whole(b)
+        if step % 16 == 15:  # start some anew: what is held and not kept goes back
+            b.begin(i32(*[0] * R), i32(*[0] * R))
+            for r in range(R):
+                if b.status.tolist()[r] == 0:
+                    last[r] = 0
+            whole(b)
+    assert {0, svd.SVD_ST_BAD_REQUEST, svd.SVD_ST_NO_PAGES, svd.SVD_ST_NO_TOKENS} <= seen
 
 
 def test_a_step_on_a_stream_that_is_not_the_current_one():
