@@ -455,7 +455,8 @@ int svd_kv_attention(const uint16_t *q, const void *cache, int capacity, int n_q
  *   no tokens has no count; window = -held, n_new = 0 ends a request).  A request with status keeps its pages:
  *   held_out = held; window_out is minus what is rejected, so that its count is not asked for again, or
  *   window itself if the count was out of order.  kv_len is keep + the tokens granted (held - window where the
- *   count was out of order).
+ *   count was out of order).  More than max_new tokens for one request, which svd_paged_attention with that
+ *   bound would leave without outputs, are refused with SVD_ST_NO_TOKENS (and not among the tokens asked for).
  * svd_paged_append: for every token t the row qkv[t * ld ..] holds Hq query, Hkv key and Hkv value
  *   heads of 128 (fp32 or bf16; 16-byte aligned, ld a multiple of 4).  Queries and keys are rotated:
  *   pair i of dimensions, (i, i + n_pairs) or, interleaved, (2i, 2i + 1), turns by
@@ -507,9 +508,10 @@ int svd_paged_tables(const int32_t *held, const int32_t *window, const int32_t *
                      int32_t *q_start, int64_t *slots, int32_t *positions, int64_t max_tokens,
                      int32_t *status, svd_stream_t stream);
 int svd_paged_advance(const int32_t *held, const int32_t *window, const int32_t *emitted,
-                      const int32_t *n_new, int n_requests, int page_size, const int32_t *table,
-                      int max_pages, const int32_t *free_ids, const int32_t *n_free, int64_t n_pages,
-                      int32_t *held_out, int32_t *window_out, int32_t *table_out, int32_t *free_out,
+                      const int32_t *n_new, int n_requests, int max_new, int page_size,
+                      const int32_t *table, int max_pages, const int32_t *free_ids,
+                      const int32_t *n_free, int64_t n_pages, int32_t *held_out,
+                      int32_t *window_out, int32_t *table_out, int32_t *free_out,
                       int32_t *n_free_out, int32_t *kv_len, int32_t *q_start, int64_t *slots,
                       int32_t *positions, int64_t max_tokens, int32_t *status, svd_stream_t stream);
 int svd_paged_append(const void *qkv, int dtype, int64_t ld, int n_tokens, int n_q_heads,

@@ -68,17 +68,23 @@ def tables(held, window, emitted, n_new, page, table, free, n_free, max_tokens):
                 status=np.array(status, np.int32))
 
 
-def advance(held, window, emitted, n_new, page, table, free, n_free, max_tokens):
-    """tables() with the state carried: also held and window of the next call."""
+def advance(held, window, emitted, n_new, max_new, page, table, free, n_free, max_tokens):
+    """tables() with the state carried: also held and window of the next call.  A request for more than
+    max_new tokens asks for nothing and gives nothing back."""
     R = len(held)
-    win, kept, odd = [], [], []
+    room = table.shape[1] * page
+    win, kept, odd, over = [], [], [], []
     for r in range(R):
         w, h = int(window[r]), int(held[r])
         e = (w if emitted is None else int(emitted[r])) if w > 0 else 0
         win.append(abs(w))
         kept.append(e)
         odd.append(not 0 <= e <= abs(w) <= h)
-    o = tables(held, win, kept, n_new, page, table, free, n_free, max_tokens)
+        over.append(not odd[r] and max(h, h - win[r] + e + int(n_new[r])) <= room and int(n_new[r]) > max_new)
+    still = np.array(over)
+    o = tables(held, np.where(still, 0, win), np.where(still, 0, kept), np.where(still, 0, n_new), page, table, free,
+               n_free, max_tokens)
+    o["status"][still] = NO_TOKENS
     o["held"], o["window"] = np.zeros(R, np.int32), np.zeros(R, np.int32)
     for r in range(R):
         keep = int(held[r]) - win[r] + (0 if odd[r] else kept[r])

@@ -38,7 +38,7 @@ int paged_tables(const int32_t *held, const int32_t *window, const int32_t *emit
                  int32_t *n_free_out, int32_t *kv_len, int32_t *q_start, int64_t *slots,
                  int32_t *positions, int64_t tokens, int32_t *status, cudaStream_t stream);
 int paged_advance(const int32_t *held, const int32_t *window, const int32_t *emitted, const int32_t *n_new,
-                  int R, int page, const int32_t *table, int width, const int32_t *free_ids,
+                  int R, int max_new, int page, const int32_t *table, int width, const int32_t *free_ids,
                   const int32_t *n_free, int64_t n_pages, int32_t *held_out, int32_t *window_out,
                   int32_t *table_out, int32_t *free_out, int32_t *n_free_out, int32_t *kv_len,
                   int32_t *q_start, int64_t *slots, int32_t *positions, int64_t tokens, int32_t *status,
@@ -214,13 +214,13 @@ int svd_paged_tables(const int32_t *held, const int32_t *window, const int32_t *
 }
 
 int svd_paged_advance(const int32_t *held, const int32_t *window, const int32_t *emitted,
-                      const int32_t *n_new, int R, int page, const int32_t *table, int width,
+                      const int32_t *n_new, int R, int max_new, int page, const int32_t *table, int width,
                       const int32_t *free_ids, const int32_t *n_free, int64_t n_pages, int32_t *held_out,
                       int32_t *window_out, int32_t *table_out, int32_t *free_out, int32_t *n_free_out,
                       int32_t *kv_len, int32_t *q_start, int64_t *slots, int32_t *positions, int64_t tokens,
                       int32_t *status, svd_stream_t stream) {
-    return svd::paged_advance(held, window, emitted, n_new, R, page, table, width, free_ids, n_free, n_pages,
-                              held_out, window_out, table_out, free_out, n_free_out, kv_len, q_start, slots,
+    return svd::paged_advance(held, window, emitted, n_new, R, max_new, page, table, width, free_ids, n_free,
+                              n_pages, held_out, window_out, table_out, free_out, n_free_out, kv_len, q_start, slots,
                               positions, tokens, status, (cudaStream_t)stream);
 }
 

@@ -32,6 +32,7 @@ struct TbArgs {
     int64_t *slots;
     int R, page, width, n_pages, tokens;
     int32_t *held_out, *window_out;  // the state carried to the next call, or null: see tb_ask
+    int max_new;                     // tokens of one request
 };
 
 // What request r asks for: the positions held, the tokens of the last window and how many of them
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kTbThreads) paged_tables_kernel(const TbArgs A
             } else {
                 p0 = ((uint32_t)a.held + A.page - 1) / (uint32_t)A.page;
                 p1 = ((uint32_t)(keep + n) + A.page - 1) / (uint32_t)A.page;
-                ask = (uint32_t)n;
+                if (n > A.max_new) st = SVD_ST_NO_TOKENS;
+                else ask = (uint32_t)n;
             }
         }
         const unsigned long long upto = tok_sum + tb_scan(ask, &total, s_w);
@@ -255,19 +257,20 @@ int paged_tables(const int32_t *held, const int32_t *window, const int32_t *emit
                  int32_t *positions, int64_t tokens, int32_t *status, cudaStream_t stream) {
     if ((!window) != (!emitted)) return SVD_ERR_INVALID_ARG;
     return tb_launch({held, window, emitted, n_new, table, free_ids, n_free, table_out, free_out, n_free_out, kv_len,
-                      q_start, positions, status, slots, R, page, width, 0, 0, nullptr, nullptr},
+                      q_start, positions, status, slots, R, page, width, 0, 0, nullptr, nullptr, INT32_MAX},
                      n_pages, tokens, stream);
 }
 
 int paged_advance(const int32_t *held, const int32_t *window, const int32_t *emitted, const int32_t *n_new,
-                  int R, int page, const int32_t *table, int width, const int32_t *free_ids,
+                  int R, int max_new, int page, const int32_t *table, int width, const int32_t *free_ids,
                   const int32_t *n_free, int64_t n_pages, int32_t *held_out, int32_t *window_out,
                   int32_t *table_out, int32_t *free_out, int32_t *n_free_out, int32_t *kv_len,
                   int32_t *q_start, int64_t *slots, int32_t *positions, int64_t tokens, int32_t *status,
                   cudaStream_t stream) {
-    if (!window || !held_out || !window_out || held_out == held || window_out == window) return SVD_ERR_INVALID_ARG;
+    if (!window || !held_out || !window_out || held_out == held || window_out == window || max_new < 1)
+        return SVD_ERR_INVALID_ARG;
     return tb_launch({held, window, emitted, n_new, table, free_ids, n_free, table_out, free_out, n_free_out, kv_len,
-                      q_start, positions, status, slots, R, page, width, 0, 0, held_out, window_out},
+                      q_start, positions, status, slots, R, page, width, 0, 0, held_out, window_out, max_new},
                      n_pages, tokens, stream);
 }
 

@@ -21,6 +21,9 @@ from . import svd
 class PagedBatch:
     """The caches of `requests` requests in `layers` pools of n_pages pages, one table for all layers.
 
+    A request has up to max_window tokens in a step (lowered where windows stay shorter: the attention then
+    takes smaller tiles), all requests together max_tokens.
+
     begin() opens a step, layer() runs one layer's append and attention.  Between two begin() calls
     the device tensors q_start, kv_len, slots, positions and status describe the step's tokens; held and
     window are the state that the next begin() goes on from."""
@@ -32,7 +35,7 @@ class PagedBatch:
         self.device, self.R, self.page, self.n_pages = dev, requests, page_size, n_pages
         self.Hq, self.Hkv, self.rope, self.out_dtype = n_q_heads, n_kv_heads, rope, out_dtype
         self.width = -(-max_len // page_size)
-        self.max_window = max_window
+        self.max_window = self._step_window = max_window
         self.max_tokens = max_tokens or requests * max_window
         nbytes = svd.svd_paged_cache_bytes(n_kv_heads, page_size, n_pages)
         if nbytes == 0:
@@ -72,8 +75,9 @@ class PagedBatch:
         if emitted is not None:
             self._counts("emitted", emitted)
         a, b = self.now, 1 - self.now
-        svd.svd_paged_advance(self.held[a], self._window[a], emitted, n_new, self.R, self.page, self.table[a], self.width,
-                              self.free[a], self.n_free[a], self.n_pages, self.held[b], self._window[b], self.table[b],
+        self._step_window = self.max_window
+        svd.svd_paged_advance(self.held[a], self._window[a], emitted, n_new, self.R, self.max_window, self.page, self.table[a],
+                              self.width, self.free[a], self.n_free[a], self.n_pages, self.held[b], self._window[b], self.table[b],
                               self.free[b], self.n_free[b], self.kv_len, self.q_start, self.slots, self.positions,
                               self.max_tokens, self.status, stream=stream)
         self.now = b
@@ -128,7 +132,7 @@ class PagedBatch:
                              rope=self.rope, positions=pos, positions_ld=pos_ld,
                              dtype=svd.SVD_F32 if qkv.dtype == torch.float32 else svd.SVD_BF16, status=self.bad,
                              stream=stream)
-        svd.svd_paged_attention(self.q, T, self.kv_len, self.q_start, self.R, self.max_window, self.table[self.now], self.width,
+        svd.svd_paged_attention(self.q, T, self.kv_len, self.q_start, self.R, self._step_window, self.table[self.now], self.width,
                                 pool, self.page, self.n_pages, self.Hq, self.Hkv, self.scale, out, self.out_dtype, self.ws,
                                 stream=stream)
         return out

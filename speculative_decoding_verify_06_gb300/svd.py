@@ -211,7 +211,7 @@ def load(path: str = LIB_PATH):
             "svd_paged_cache_bytes": (sz, [i32, i32, i64]),
             "svd_paged_tables": (i32, [P, P, P, P, i32, i32, P, i32, P, P, i64, P, P, P, P, P, P, P,
                                        i64, P, P]),
-            "svd_paged_advance": (i32, [P, P, P, P, i32, i32, P, i32, P, P, i64, P, P, P, P, P, P, P, P, P,
+            "svd_paged_advance": (i32, [P, P, P, P, i32, i32, i32, P, i32, P, P, i64, P, P, P, P, P, P, P, P, P,
                                         i64, P, P]),
             "svd_paged_append": (i32, [P, i32, i64, i32, i32, i32, P, P, i64, P, P, i32, i64, P, P,
                                        P]),
@@ -592,15 +592,15 @@ def svd_paged_tables(held, window, emitted, n_new, n_requests: int, page_size: i
         _ptr(status), _stream(stream)))
 
 
-def svd_paged_advance(held, window, emitted, n_new, n_requests: int, page_size: int, table,
-                      max_pages: int, free_ids, n_free, n_pages: int, held_out, window_out, table_out,
-                      free_out, n_free_out, kv_len, q_start, slots, positions, max_tokens: int, status,
-                      stream=None):
+def svd_paged_advance(held, window, emitted, n_new, n_requests: int, max_new: int, page_size: int,
+                      table, max_pages: int, free_ids, n_free, n_pages: int, held_out, window_out,
+                      table_out, free_out, n_free_out, kv_len, q_start, slots, positions,
+                      max_tokens: int, status, stream=None):
     _check("svd_paged_advance", load().svd_paged_advance(
-        _ptr(held), _ptr(window), _ptr(emitted), _ptr(n_new), int(n_requests), int(page_size), _ptr(table),
-        int(max_pages), _ptr(free_ids), _ptr(n_free), int(n_pages), _ptr(held_out), _ptr(window_out),
-        _ptr(table_out), _ptr(free_out), _ptr(n_free_out), _ptr(kv_len), _ptr(q_start), _ptr(slots),
-        _ptr(positions), int(max_tokens), _ptr(status), _stream(stream)))
+        _ptr(held), _ptr(window), _ptr(emitted), _ptr(n_new), int(n_requests), int(max_new),
+        int(page_size), _ptr(table), int(max_pages), _ptr(free_ids), _ptr(n_free), int(n_pages),
+        _ptr(held_out), _ptr(window_out), _ptr(table_out), _ptr(free_out), _ptr(n_free_out), _ptr(kv_len),
+        _ptr(q_start), _ptr(slots), _ptr(positions), int(max_tokens), _ptr(status), _stream(stream)))
 
 
 def svd_paged_append(qkv, ld: int, n_tokens: int, n_q_heads: int, n_kv_heads: int, slots, pages,

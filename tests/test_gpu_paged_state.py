@@ -49,12 +49,12 @@ def test_carried_state_against_the_definitions():
         window[g.random(R) < 0.1] += 1000
         emitted = np.maximum(window, 0) - g.integers(-1, 4, R)
         n_new = g.integers(-1, 20, R)
-        for kept in (emitted, None):
-            want = ref.advance(held, window, kept, n_new, page, table, free, spare, tokens)
+        for kept, most in ((emitted, 15), (None, 1 << 20), (emitted, 2)):
+            want = ref.advance(held, window, kept, n_new, most, page, table, free, spare, tokens)
             d = {k: torch.full(np.shape(v) or (1,), -77, dtype=torch.int64 if k == "slots" else torch.int32, device=DEV)
                  for k, v in want.items()}
             ins = [None if a is None else i32(*a.reshape(-1).tolist()) for a in (held, window, kept, n_new, table, free)]
-            svd.svd_paged_advance(*ins[:4], R, page, ins[4], width, ins[5], i32(spare), len(ids), d["held"], d["window"],
+            svd.svd_paged_advance(*ins[:4], R, most, page, ins[4], width, ins[5], i32(spare), len(ids), d["held"], d["window"],
                                   d["table"], d["free"], d["n_free"], d["kv_len"], d["q_start"], d["slots"], d["positions"],
                                   tokens, d["status"])
             for k in want:
@@ -177,3 +177,21 @@ def test_a_step_on_a_stream_that_is_not_the_current_one():
         assert b.status.tolist() == [0, 0] and b.kv_len.tolist() == [7, 25] and b.window.tolist() == [2, 2]
     torch.cuda.synchronize()
     whole(b)
+
+
+def test_more_tokens_than_a_window_holds_are_refused():
+    """What the attention would leave without outputs gets no slots either; the rest is served."""
+    b = batch(3, max_window=5, max_tokens=12)
+    b.begin(i32(5, 6, 4))
+    assert b.status.tolist() == [0, svd.SVD_ST_NO_TOKENS, 0]
+    assert b.q_start.tolist() == [0, 5, 5, 9] and b.kv_len.tolist() == [5, 0, 4]
+    b.max_window = 4
+    b.begin(i32(5, 4, 4), i32(2, 3, 4))
+    assert b.status.tolist() == [svd.SVD_ST_NO_TOKENS, 0, 0] and b.kv_len.tolist() == [2, 4, 8]
+    whole(b)
+    b.max_window = 1  # (for the next step)
+    # every token with a slot has its output
+    x = torch.randn((12, 4 * 128), device=DEV)
+    out = torch.full((12, 2, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    b.layer(0, x, out)
+    assert torch.isfinite(out[:8]).all() and torch.isnan(out[8:]).all() and (b.slots[:8] >= 0).all() and (b.slots[8:] < 0).all()

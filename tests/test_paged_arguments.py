@@ -145,7 +145,7 @@ def test_counts_of_another_form_are_refused(calls, n_new):
     assert not calls
 
 
-ADVANCE = dict(held=16, window=16, emitted=16, n_new=16, R=2, page=16, table=32, width=4, free_ids=48, n_free=64, n_pages=8,
+ADVANCE = dict(held=16, window=16, emitted=16, n_new=16, R=2, max_new=4, page=16, table=32, width=4, free_ids=48, n_free=64, n_pages=8,
                held_out=208, window_out=224, table_out=80, free_out=96, n_free_out=112, kv_len=128, q_start=144, slots=160,
                positions=176, tokens=8, status=192, stream=None)
 
@@ -153,6 +153,6 @@ ADVANCE = dict(held=16, window=16, emitted=16, n_new=16, R=2, page=16, table=32,
 @pytest.mark.parametrize("change", [
     dict(held=None), dict(window=None), dict(n_new=None), dict(table=None), dict(held_out=None), dict(window_out=None),
     dict(held_out=16), dict(window_out=16), dict(table_out=32), dict(free_out=48), dict(n_free_out=64), dict(R=0), dict(R=4097),
-    dict(page=24), dict(width=0), dict(n_pages=0), dict(tokens=0), dict(kv_len=None), dict(status=None)])
+    dict(page=24), dict(width=0), dict(n_pages=0), dict(tokens=0), dict(kv_len=None), dict(status=None), dict(max_new=0)])
 def test_advance_refusals(lib, change):
     assert lib.svd_paged_advance(*{**ADVANCE, **change}.values()) == svd.SVD_ERR_INVALID_ARG
