@@ -5,13 +5,16 @@ describes for one sequence, for a batch of them ("Why a hiring company is writin
 follow the tokens that the last acceptance kept (svd_paged_advance), every layer's queries and keys are
 rotated and its keys and values appended (svd_paged_append), and the window's tokens attend to
 their requests' caches (svd_paged_attention).  Nothing of a step waits for the host: acceptance
-counts, lengths, page ids and free pages stay in device memory, so a step can be recorded.
+counts, lengths, page ids and free pages stay in device memory, at the same addresses in every step, so a step can
+be recorded and replayed.
 
     python -m speculative_decoding_verify_06_gb300.paged [requests] [window] [steps]
 
 runs a two-layer stand-in for a model on synthetic weights, accepting drafts and growing the caches.
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -42,13 +45,16 @@ class PagedBatch:
             raise ValueError("no such pool: see svd_paged_cache_bytes")
         self.pools = [torch.zeros(nbytes, dtype=torch.uint8, device=dev) for _ in range(layers)]
         i32 = dict(dtype=torch.int32, device=dev)
-        # the tables are read from one copy and written to the other, in turn
-        self.table = [torch.full((requests, self.width), -1, **i32) for _ in range(2)]
-        self.free = [torch.arange(n_pages - 1, -1, -1, **i32) for _ in range(2)]  # page 0 on top
-        self.n_free = [torch.full((1,), n_pages, **i32) for _ in range(2)]
-        self.held = [torch.zeros(requests, **i32) for _ in range(2)]  # positions that the pages hold
-        self._window = [torch.zeros(requests, **i32) for _ in range(2)]
-        self.now = 0
+        # The state lies in one piece, so that the copy that a step writes takes one transfer to become the
+        # copy that the next one reads; both stay where they are, so that a recorded step can be replayed.
+        sizes = [requests * self.width, n_pages, 1, requests, requests]
+        self._state = [torch.zeros(sum(sizes), **i32) for _ in range(2)]
+        table, self.free, self.n_free, self.held, self._window = zip(*(c.split(sizes) for c in self._state))
+        self.table = [t.view(requests, self.width) for t in table]
+        self.now = 0  # the copy that holds the state between steps
+        self.table[0].fill_(-1)
+        self.free[0].copy_(torch.arange(n_pages - 1, -1, -1, **i32))  # page 0 on top
+        self.n_free[0].fill_(n_pages)
         self.q_start = torch.zeros(requests + 1, **i32)
         self.slots = torch.full((self.max_tokens,), -1, dtype=torch.int64, device=dev)
         self.positions = torch.full((self.max_tokens,), -1, **i32)
@@ -80,7 +86,14 @@ class PagedBatch:
                               self.width, self.free[a], self.n_free[a], self.n_pages, self.held[b], self._window[b], self.table[b],
                               self.free[b], self.n_free[b], self.kv_len, self.q_start, self.slots, self.positions,
                               self.max_tokens, self.status, stream=stream)
-        self.now = b
+        with self._on(stream):
+            self._state[a].copy_(self._state[b])
+
+    @staticmethod
+    def _on(stream):
+        if stream is None:
+            return contextlib.nullcontext()
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
     def _here(self, name: str, t, *dtypes):
         """The library takes addresses: a tensor of another type or place would be read as it lies."""

@@ -1,5 +1,5 @@
 """The state that PagedBatch carries from step to step: refused requests lose nothing, every page is in one
-place, on any stream."""
+place, on any stream and in a graph."""
 import numpy as np
 import pytest
 import torch
@@ -195,3 +195,55 @@ def test_more_tokens_than_a_window_holds_are_refused():
     out = torch.full((12, 2, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
     b.layer(0, x, out)
     assert torch.isfinite(out[:8]).all() and torch.isnan(out[8:]).all() and (b.slots[:8] >= 0).all() and (b.slots[8:] < 0).all()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_one_step_recorded_and_replayed(raw):
+    """A graph of a single step goes on from where the last replay, or the last step outside it, ended."""
+    R, n = 3, 2
+
+    def make():
+        b = paged.PagedBatch(R, 1, n_pages=40, page_size=16, max_len=256, max_window=n, n_q_heads=4, n_kv_heads=2,
+                             rope=svd.Rope(np.full(64, 0.3)))
+        g = torch.Generator(device=DEV)
+        g.manual_seed(3)
+        return (b, torch.randn((R * n, 8 * 128), generator=g, device=DEV),
+                torch.zeros((R * n, 4, 128), dtype=torch.bfloat16, device=DEV), i32(1, 2, 1))
+
+    new = i32(*[n] * R)
+    b, x, out, kept = make()
+    b.begin(new)
+    want = []
+    for step in range(7):
+        b.begin(new, kept)
+        b.layer(0, x, out)
+        want.append((out.clone(), b.kv_len.tolist(), b.slots.tolist()))
+    b, x, out, kept = make()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        b.begin(new)
+    s.synchronize()
+
+    def step(stream=None):
+        b.begin(new, kept, stream=stream)
+        b.layer(0, x, out, stream=stream)
+    if raw:
+        svd.svd_graph_begin(s)
+        step(s.cuda_stream)
+        graph = svd.svd_graph_end(s)
+        play = lambda: graph.launch(s)  # noqa: E731
+    else:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step()
+        play = graph.replay
+    with torch.cuda.stream(s):
+        for i, (o, lens, slots) in enumerate(want):
+            if i == 3:
+                step()  # one outside the graph
+            else:
+                play()
+            assert torch.equal(out, o) and b.kv_len.tolist() == lens and b.slots.tolist() == slots, i
+    torch.cuda.synchronize()
+    whole(b)
