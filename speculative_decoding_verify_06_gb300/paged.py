@@ -89,6 +89,15 @@ class PagedBatch:
         with self._on(stream):
             self._state[a].copy_(self._state[b])
 
+    def end(self, who, stream=None):
+        """Requests (bool [R]) that are over: the next begin() gives all their pages back, and counts what it adds
+        for them from position 0.  Comes after the last layer() of a step, in place of their kept counts."""
+        self._here("who", who, torch.bool)
+        if who.shape != (self.R,):
+            raise ValueError(f"who: [{self.R}], got {tuple(who.shape)}")
+        with self._on(stream):
+            torch.where(who, -self.held[self.now], self.window, out=self.window)
+
     @staticmethod
     def _on(stream):
         if stream is None:

@@ -247,3 +247,31 @@ def test_one_step_recorded_and_replayed(raw):
             assert torch.equal(out, o) and b.kv_len.tolist() == lens and b.slots.tolist() == slots, i
     torch.cuda.synchronize()
     whole(b)
+
+
+def test_a_request_that_ends_gives_its_pages_back():
+    b = batch(3)
+    b.begin(i32(40, 20, 33))
+    b.end(torch.tensor([False, True, True], device=DEV))
+    b.begin(i32(2, 0, 50), i32(39, 7, 5))  # request 2's place goes to another one at once
+    assert b.status.tolist() == [0, 0, 0] and b.kv_len.tolist() == [41, 0, 50]
+    assert b.positions[:52].tolist() == [39, 40] + list(range(50)) and int(b.n_free[b.now]) == 8 - 3 - 4
+    whole(b)
+    b.end(torch.tensor([True, False, False], device=DEV))
+    b.begin(i32(4, 33, 64), i32(2, 0, 50))  # a refusal beside the end: request 2's length
+    assert b.status.tolist() == [0, 0, svd.SVD_ST_BAD_REQUEST] and b.kv_len.tolist() == [4, 33, 50]
+    b.end(torch.tensor([True, True, True], device=DEV))
+    b.begin(i32(0, 65, 0))                  # an end holds through a refusal
+    assert b.status.tolist() == [0, svd.SVD_ST_BAD_REQUEST, 0] and b.kv_len.tolist() == [0, 0, 0]
+    whole(b)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    b.begin(i32(0, 0, 0), i32(9, 9, 9), stream=s)
+    s.synchronize()
+    assert int(b.n_free[b.now]) == 8
+    b.begin(i32(20, 20, 20), stream=s)
+    b.end(torch.ones(3, dtype=torch.bool, device=DEV), stream=s)
+    b.begin(i32(0, 0, 1), stream=s)
+    s.synchronize()
+    assert b.kv_len.tolist() == [0, 0, 1] and int(b.n_free[b.now]) == 7
+    whole(b)

@@ -156,3 +156,9 @@ ADVANCE = dict(held=16, window=16, emitted=16, n_new=16, R=2, max_new=4, page=16
     dict(page=24), dict(width=0), dict(n_pages=0), dict(tokens=0), dict(kv_len=None), dict(status=None), dict(max_new=0)])
 def test_advance_refusals(lib, change):
     assert lib.svd_paged_advance(*{**ADVANCE, **change}.values()) == svd.SVD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("who", [torch.ones(3, dtype=torch.int32), torch.ones(2, dtype=torch.bool), torch.ones((3, 1), dtype=torch.bool)])
+def test_ends_of_another_form_are_refused(who):
+    with pytest.raises(ValueError, match="who"):
+        batch().end(who)
