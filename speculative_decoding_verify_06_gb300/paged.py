@@ -72,6 +72,12 @@ class PagedBatch:
         known to go."""
         return self._window[self.now]
 
+    @property
+    def gave_up(self):
+        """int32 [1], not 0 once a bounded wait of an attention kernel gave up: outputs since then are undefined.
+        Stays until it is zeroed."""
+        return self.ws[:4].view(torch.int32)
+
     def begin(self, n_new, emitted=None, stream=None):
         """Opens a step of n_new [R] new tokens for each request, after `emitted` [R] of the last
         step's tokens were kept (None: all of them; a request that had no tokens has no count).  Requests
