@@ -471,14 +471,12 @@ __device__ __noinline__ ApOut ap_keys_f64(const ApArgs &A, int t, float4 xa, flo
 }
 
 // Values as they came, with anything in them: not finite, too large, all zero, ties, scales among
-// fp16's subnormals.  What is not finite is noted and stored as 0 or the largest magnitude: a cache
-// byte never stands for a NaN that a masked position could spread.
-__device__ __noinline__ ApOut ap_general(int32_t *status, float4 y4, int lane) {
+// fp16's subnormals.  What came not finite (odd: in this lane) is noted and stored as 0 or the largest
+// magnitude: a cache byte never stands for a NaN that a masked position could spread.
+__device__ __noinline__ ApOut ap_general(int32_t *status, float4 y4, bool odd, int lane) {
     float y[4] = {y4.x, y4.y, y4.z, y4.w};
-    bool odd = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        odd |= !(fabsf(y[j]) <= 3.4028235e38f);
         if (y[j] != y[j]) y[j] = 0.f;
         y[j] = fminf(fmaxf(y[j], -(float)kPgMaxAbs), (float)kPgMaxAbs);
     }
@@ -614,16 +612,34 @@ __device__ __forceinline__ void ap_head(const ApArgs &A, int t, int head, int la
     const bool sure = is_v ? ap_quick<false>(y, low, err, false, &db, &codes)
                            : ap_quick<true>(y, low, err, turn.on, &db, &codes);
     if (!__all_sync(~0u, sure)) {
-        // Rotated blocks in doubt need the angle again; others only their values.
+        // Rotated blocks in doubt need the angle again; others, and those with a value that is not finite,
+        // only their values (for the latter as the formula gives them: the parts that the products dropped
+        // are not numbers there).
         const bool turned = !is_v && 4 * (lane & 24) < 2 * A.rope.pairs;
-        const bool finite = (y[0] + y[1]) * 0.f + (y[2] + y[3]) * 0.f == 0.f;
-        const bool angle = __any_sync(~0u, !sure && turned) && __all_sync(~0u, finite);
-        const ApOut o =
-            angle ? ap_keys_f64(A, t, make_float4(x[0], x[1], x[2], x[3]), make_float4(xb[0], xb[1], xb[2], xb[3]), lane)
-                  : ap_general(A.status ? A.status + t : nullptr, make_float4(y[0], y[1], y[2], y[3]), lane);
-        if (angle || !turned || !sure) {
-            codes = o.codes;
-            db = (uint16_t)o.scale;
+        bool odd = false, clean = true;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            odd |= !(fabsf(x[j]) <= 3.4028235e38f);
+            clean &= fabsf(x[j]) <= 3.4028235e38f && (is_v || fabsf(xb[j]) <= 3.4028235e38f);
+            if (!is_v && turn.on && !(fabsf(y[j]) <= 3.4028235e38f))
+                y[j] = __fadd_rn(__fmul_rn(x[j], turn.c[j]), __fmul_rn(xb[j], turn.s[j]));
+        }
+        const uint32_t all_clean = __ballot_sync(~0u, clean);  // (a vote of all lanes: before anything that divides them)
+        const bool again = turned && ((all_clean >> (lane & 24)) & 0xFFu) == 0xFFu;  // of the block
+        if (__any_sync(~0u, !sure && again)) {
+            const ApOut o =
+                ap_keys_f64(A, t, make_float4(x[0], x[1], x[2], x[3]), make_float4(xb[0], xb[1], xb[2], xb[3]), lane);
+            if (again) {
+                codes = o.codes;
+                db = (uint16_t)o.scale;
+            }
+        }
+        if (__any_sync(~0u, !sure && !again)) {
+            const ApOut o = ap_general(A.status ? A.status + t : nullptr, make_float4(y[0], y[1], y[2], y[3]), odd, lane);
+            if (!again) {
+                codes = o.codes;
+                db = (uint16_t)o.scale;
+            }
         }
     }
 

@@ -1,5 +1,6 @@
 """The paged calls on the GPU in cases that once went wrong, against the fp64 reference: waits that give up
-with the copies of a short range in flight; one row of positions for several axes."""
+with the copies of a short range in flight; one row of positions for several axes; rotated keys that are not finite or too
+large for fp32."""
 import numpy as np
 import pytest
 import torch
@@ -89,3 +90,32 @@ def test_a_step_with_several_axes(given):
     assert np.all(np.abs(q - y[:, :Hq]) <= 2.0 ** -8 * np.abs(y[:, :Hq]) + 2.0 ** -17)
     want = ref.put(np.zeros((8, Hkv, 1, ref.UNIT), np.uint8), b.slots[:T].cpu().numpy(), y[:, Hq:Hq + 1], x[:, Hq + 1:].astype(float), page)
     assert np.array_equal(b.pools[0].cpu().numpy().reshape(want.shape), want) and not b.bad.any()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("pairs", [64, 20])
+def test_rotated_keys_that_are_not_finite(pairs, interleaved):
+    """An infinite key is infinite after the rotation (the largest magnitude), not a NaN (0); finite ones that
+    leave fp32's range are not reported; blocks beside them get the codes of exact arithmetic."""
+    g = np.random.default_rng(pairs + interleaved)
+    T, page = 600, 64
+    x = g.normal(size=(T, 2, 128)).astype(np.float32)
+    odd = g.random(T) < 0.5
+    for t in range(T):
+        big = [np.inf, -np.inf, np.nan, 3.3e38, -3e38, 7e4]
+        for d in g.integers(0, 128, g.integers(0, 4)):
+            x[t, 0, d] = big[g.integers(0, 6)] if odd[t] else big[g.integers(3, 6)]
+        # a block of values near the borders of its codes, wherever it is
+        x[t, 0, 96:] = ((np.arange(32) % 16) - 7.5).astype(np.float32) if pairs == 20 else x[t, 0, 96:]
+    pos = g.integers(1, 4000, (1, T))
+    inv = g.uniform(0.05, 1.0, pairs)
+    pool = torch.zeros(10 * 4 * ref.UNIT, dtype=torch.uint8, device=DEV)
+    status = torch.zeros(T, dtype=torch.int32, device=DEV)
+    svd.svd_paged_append(to_dev(x.reshape(T, -1)), 256, T, 0, 1, torch.arange(T, device=DEV), pool, page, 10, None,
+                         rope=svd.Rope(inv, interleaved=interleaved), positions=to_dev(pos.astype(np.int32)), positions_ld=T,
+                         status=status)
+    with np.errstate(invalid="ignore", over="ignore"):
+        y = ref.rotate(x.astype(np.float64), pos, inv, [0] * pairs, interleaved)
+    want = ref.put(np.zeros((10, 1, 4, ref.UNIT), np.uint8), np.arange(T), y[:, :1], x[:, 1:].astype(float), page)
+    assert np.array_equal(pool.cpu().numpy().reshape(want.shape), want)
+    assert np.array_equal(status.cpu().numpy() != 0, ~np.isfinite(x).all((1, 2)))
