@@ -747,8 +747,10 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
             if (ti.mask != 0xFFu || (ti.tile + 1) * kPaTile > whole_to) {
                 const int pos = ti.tile * kPaTile + gt;
                 const bool here = ((ti.mask >> (gt >> 4)) & 1u) && pos < len;
-                // row j is token tok + (off + j) / G: it sees the position once j reaches this
-                const int from = here ? (pos - pos0) * A.G - off0 : RG;
+                // row j is token tok + (off + j) / G: it sees the position once j reaches this (a
+                // position before the first token is seen by all rows, one RP + 1 past it by none; the
+                // distance times G may pass 32 bits)
+                const int from = here ? min(max(pos - pos0, 0), RP + 1) * A.G - off0 : RG;
 #pragma unroll
                 for (int j = 0; j < RG / 2; ++j) {
                     float2 v = pa_un2(s[j]);

@@ -1,6 +1,6 @@
 """The paged calls on the GPU in cases that once went wrong, against the fp64 reference: waits that give up
 with the copies of a short range in flight; one row of positions for several axes; rotated keys that are not finite or too
-large for fp32."""
+large for fp32; masks of many heads far behind the window."""
 import numpy as np
 import pytest
 import torch
@@ -119,3 +119,28 @@ def test_rotated_keys_that_are_not_finite(pairs, interleaved):
     want = ref.put(np.zeros((10, 1, 4, ref.UNIT), np.uint8), np.arange(T), y[:, :1], x[:, 1:].astype(float), page)
     assert np.array_equal(pool.cpu().numpy().reshape(want.shape), want)
     assert np.array_equal(status.cpu().numpy() != 0, ~np.isfinite(x).all((1, 2)))
+
+
+@pytest.mark.parametrize("out_dtype", [svd.SVD_BF16, svd.SVD_F32])
+def test_a_missing_page_far_behind_a_window_of_many_heads(out_dtype):
+    """8.5 million positions before the window, 256 heads to a kv head: the product of both passes 32 bits.
+    The first page is missing; the second, which shares its tile, holds about half of the weight."""
+    page, G, cols = 64, 256, 132800
+    g = np.random.default_rng(4)
+    k, v = np.zeros((2 * page, 1, 128)), g.normal(size=(2 * page, 1, 128))
+    k[:page] = 1.0
+    pool = ref.put(np.zeros((2, 1, 4, ref.UNIT), np.uint8), np.arange(2 * page), k, v, page)
+    table = np.ones((1, cols), np.int32)
+    table[0, :2] = -1, 0
+    q = np.full((1, G, 128), 11.8 / 128 * 128 ** 0.5)
+    q += g.normal(0, 0.05, q.shape)
+    c = Attend([cols * page], [1], G, 1, page, out_dtype, pool=pool, table=table, q=q)
+    got = c.run()[0]
+    kk, vv = ref.get(pool, np.arange(2 * page), page)
+    times = np.repeat([1.0, cols - 2.0], page)
+    s = c.q[0].double().numpy() @ kk[:, 0].T * c.scale
+    p = np.exp(s - s.max(1, keepdims=True)) * times
+    p /= p.sum(1, keepdims=True)
+    assert np.all((p[:, :page].sum(1) > 0.2) & (p[:, :page].sum(1) < 0.8))
+    # the output's 2^-8, P's 2^-11, scores of 12 good to 2^-16 (twice), 2^14 truncated additions: below 2^-7 together
+    assert np.all(np.abs(got - p @ vv[:, 0]) <= 2.0 ** -7 * (p @ np.abs(vv[:, 0])))
