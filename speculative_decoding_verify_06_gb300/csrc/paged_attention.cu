@@ -23,9 +23,10 @@
 // starts while S still reads the second half.  The softmax warps turn S into P in shared memory.  A lane
 // holds one position of S for all rows, so the softmax needs no lane exchange: the reference of a row
 // changes only when a score exceeds it by 15 (p <= 2^15 in between), checked by one vote of the four
-// warps, and starts 7 below the first tile's maximum.  p keeps fp16's eleven bits down to 2^-22 of the
-// largest and loses them gradually to 2^-32.  For fp32 outputs P is split into two fp16 parts
-// (relative 2^-22) that stand side by side as columns of one product, and O is added up in registers
+// warps, and starts 7 below the first tile's maximum.  p keeps fp16's eleven bits down to 2^-21 of the
+// largest and loses them gradually to 2^-32.  For fp32 outputs P is split into two fp16 parts that
+// stand side by side as columns of one product, the second times 2^11 so that it does not fall among fp16's
+// subnormals (p to a relative 2^-22 and 2^-43 of the largest), and O is added up in registers
 // tile by tile, because the tensor core truncates what it adds to its accumulators: 256 additions
 // were 2.5e-6 off, so are 6e-7.
 //
@@ -698,6 +699,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         int pos0 = 0, off0 = 0, whole_to = 0, len = 0;  // of the segment
         f2 l[RG / 2], acc[F32 ? RG / 2 : 1];
         const f2 c2 = pa_f2(c, c);
+        const f2 lo_step = pa_f2(0x1p-11f, 0x1p-11f), lo_up = pa_f2(2048.f, 2048.f), lo_neg = pa_f2(-2048.f, -2048.f);
         if (lane == 0)  // the first SB tiles find their S columns free
             for (int i = 0; i < SB; ++i) pa_arrive(b_s0 + 8 * i);
         for (uint32_t t = 0; t < count; ++t) {
@@ -845,7 +847,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
                     pa_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[j / 2 + i] = pa_add2(acc[j / 2 + i], pa_add2(pa_f2(o[2 * i], o[2 * i + 1]), pa_f2(lo[2 * i], lo[2 * i + 1])));
+                        acc[j / 2 + i] = pa_add2(acc[j / 2 + i], pa_fma2(pa_f2(lo[2 * i], lo[2 * i + 1]), lo_step, pa_f2(o[2 * i], o[2 * i + 1])));
                 }
                 pa_fence_before();
                 if (any) {
@@ -872,7 +874,8 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 f = __half22float2(reinterpret_cast<const __half2 &>(h[i]));
-                        lo2[i] = pa_pack(p[2 * i] - f.x, p[2 * i + 1] - f.y);
+                        const float2 r = pa_un2(pa_fma2(pa_f2(f.x, f.y), lo_neg, pa_mul2(pa_f2(p[2 * i], p[2 * i + 1]), lo_up)));
+                        lo2[i] = pa_pack(r.x, r.y);  // 2^11 (p - f), exact before the rounding
                     }
                     *reinterpret_cast<uint4 *>(prow + (RP >> 3) * 2048 + (j >> 3) * 2048) = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
                 }
@@ -934,7 +937,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float2 x = pa_un2(acc[(j + i) / 2]);
-                            o[j + i] = (o[j + i] + lo[i]) + (i & 1 ? x.y : x.x);
+                            o[j + i] = fmaf(lo[i], 0x1p-11f, o[j + i]) + (i & 1 ? x.y : x.x);
                         }
                     }
                 }

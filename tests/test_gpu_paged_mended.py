@@ -1,6 +1,7 @@
 """The paged calls on the GPU in cases that once went wrong, against the fp64 reference: waits that give up
 with the copies of a short range in flight; one row of positions for several axes; rotated keys that are not finite or too
-large for fp32; masks of many heads far behind the window."""
+large for fp32; masks of many heads far behind the window; small
+probabilities in fp32 outputs."""
 import numpy as np
 import pytest
 import torch
@@ -144,3 +145,30 @@ def test_a_missing_page_far_behind_a_window_of_many_heads(out_dtype):
     assert np.all((p[:, :page].sum(1) > 0.2) & (p[:, :page].sum(1) < 0.8))
     # the output's 2^-8, P's 2^-11, scores of 12 good to 2^-16 (twice), 2^14 truncated additions: below 2^-7 together
     assert np.all(np.abs(got - p @ vv[:, 0]) <= 2.0 ** -7 * (p @ np.abs(vv[:, 0])))
+
+
+def test_a_long_tail_behind_one_large_probability():
+    """fp32 outputs: one position takes nearly all, 4096 others 2^-21.6 of it each, between two steps of fp16's
+    subnormals.  Its value is 0 and theirs are 1, so the output is the tail's share of the sum.  Requests
+    enough that a CTA holds the first position and a long tail."""
+    page, n, R, scale = 64, 4096, 256, 128 ** -0.5
+    for key in range(128, 256):  # an eight-bit key for which the tail lies about half way between two steps
+        m = 5.5 * key / 128 * 16 * scale / np.log(2.0)
+        steps = 2.0 ** (31 - m)
+        if 300 < steps < 900 and 0.45 < steps % 1 < 0.55:
+            break
+    assert 300 < steps < 900 and 0.45 < steps % 1 < 0.55
+    k, v = np.zeros((2 * page, 1, 128)), np.ones((2 * page, 1, 128))
+    k[page, :, :16], v[page] = key / 128, 0.0
+    pool = ref.put(np.zeros((2, 1, 4, ref.UNIT), np.uint8), np.arange(2 * page), k, v, page)
+    kk, vv = ref.get(pool, np.arange(2 * page), page)
+    assert np.array_equal(kk, k) and np.array_equal(vv, v)
+    table = np.zeros((R, n // page + 1), np.int32)
+    table[:, 0] = 1
+    c = Attend([n + 1] * R, [1] * R, 4, 1, page, svd.SVD_F32, pool=pool, table=table, q=np.full((R, 4, 128), 5.5))
+    got = c.run()
+    tail = n * 2.0 ** -m
+    # fp32 additions of equal numbers: n / 128 within a lane and 16 across them and the segments, for the sum and
+    # for the output; p: its exponent's 2^-20, the exponential's and the split's 2^-22
+    bound = 2 * (n / 128 + 16) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -21
+    assert np.all(np.abs(got / (tail / (1 + tail)) - 1) <= bound)
