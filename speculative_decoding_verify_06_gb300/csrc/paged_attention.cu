@@ -699,7 +699,7 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         int pos0 = 0, off0 = 0, whole_to = 0, len = 0;  // of the segment
         f2 l[RG / 2], acc[F32 ? RG / 2 : 1];
         const f2 c2 = pa_f2(c, c);
-        const f2 lo_step = pa_f2(0x1p-11f, 0x1p-11f), lo_up = pa_f2(2048.f, 2048.f), lo_neg = pa_f2(-2048.f, -2048.f);
+        const f2 lo_step = pa_f2(0x1p-11f, 0x1p-11f);
         if (lane == 0)  // the first SB tiles find their S columns free
             for (int i = 0; i < SB; ++i) pa_arrive(b_s0 + 8 * i);
         for (uint32_t t = 0; t < count; ++t) {
@@ -874,8 +874,8 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 f = __half22float2(reinterpret_cast<const __half2 &>(h[i]));
-                        const float2 r = pa_un2(pa_fma2(pa_f2(f.x, f.y), lo_neg, pa_mul2(pa_f2(p[2 * i], p[2 * i + 1]), lo_up)));
-                        lo2[i] = pa_pack(r.x, r.y);  // 2^11 (p - f), exact before the rounding
+                        // 2^11 (p - f), exact before the rounding
+                        lo2[i] = pa_pack(fmaf(f.x, -2048.f, p[2 * i] * 2048.f), fmaf(f.y, -2048.f, p[2 * i + 1] * 2048.f));
                     }
                     *reinterpret_cast<uint4 *>(prow + (RP >> 3) * 2048 + (j >> 3) * 2048) = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
                 }
