@@ -1,7 +1,7 @@
 """The paged calls on the GPU in cases that once went wrong, against the fp64 reference: waits that give up
 with the copies of a short range in flight; one row of positions for several axes; rotated keys that are not finite or too
 large for fp32; masks of many heads far behind the window; small
-probabilities in fp32 outputs."""
+probabilities in fp32 outputs; keys of very small and very large scales."""
 import numpy as np
 import pytest
 import torch
@@ -172,3 +172,38 @@ def test_a_long_tail_behind_one_large_probability():
     # for the output; p: its exponent's 2^-20, the exponential's and the split's 2^-22
     bound = 2 * (n / 128 + 16) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -21
     assert np.all(np.abs(got / (tail / (1 + tail)) - 1) <= bound)
+
+
+def check(c, got, small_keys):
+    """Bounds counted from the roundings: scores 2^-16 of sum |q k| (fp32 additions in the tensor core), small
+    keys eight steps of half of 2^-22, P's 2^-11 (fp32 outputs: its two parts' 2^-21), a position's 2^-32, the sums,
+    the output."""
+    o, a, e = c.reference()
+    n = max(c.lens)
+    score = 2.0 ** -16 * e[..., None]
+    if small_keys:
+        score = score + 2.0 ** -20 * c.scale * np.abs(c.q.double().numpy()).sum(-1, keepdims=True)
+    if c.out_dtype == svd.SVD_BF16:
+        bound = 2.0 ** -8 * np.abs(o) + a * (2.0 ** -11 + 2 * score + n * 2.0 ** -23 + 2.0 ** -19) + n * 2.0 ** -32 * 8
+    else:
+        bound = a * (2.0 ** -21 + 2 * score + (256 + n / 128) * 2.0 ** -23 + 2.0 ** -19) + n * 2.0 ** -43 * 8
+    err = np.abs(got - o)
+    assert np.all(err <= bound + 1e-30), float(np.max(err / (bound + 1e-30)))
+
+
+@pytest.mark.parametrize("out_dtype", [svd.SVD_BF16, svd.SVD_F32])
+@pytest.mark.parametrize("new,Hq", [(4, 5), (40, 5)])
+@pytest.mark.parametrize("size", [2.0 ** -23, 2.0 ** -19, 2.0 ** -15, 2.0 ** -13, 2.0 ** 9, 2.0 ** 11])
+def test_keys_of_any_scale(out_dtype, new, Hq, size):
+    """Keys around 8 d for d from fp16's subnormals to its largest; queries that make their scores a few units.
+    Scales from 2^-15 on are exact, smaller ones rounded to multiples of 2^-22."""
+    page, n = 32, 400
+    g = np.random.default_rng(6)
+    k = g.normal(size=(416, 1, 128))
+    k *= np.minimum(2.5 * size, 60000 / np.abs(k).max())
+    pool = ref.put(np.zeros((13, 1, 2, ref.UNIT), np.uint8), np.arange(416), k, g.normal(size=k.shape), page)
+    d = pool.view(np.float16)[..., 1024:1088].astype(float)
+    assert np.median(np.abs(d)) < 2 * size and (size < 2.0 ** 11 or np.abs(d).max() > 2720)
+    q = g.normal(size=(new, Hq, 128)) * min(0.6 / size, 12000.0)
+    c = Attend([n], [new], Hq, 1, page, out_dtype, pool=pool, q=q)
+    check(c, c.run(), (np.abs(d) < 2.0 ** -15).any())
