@@ -478,14 +478,15 @@ int svd_kv_attention(const uint16_t *q, const void *cache, int capacity, int n_q
  *   written.  max_new bounds the tokens of a request (later ones are not written).  Positions whose
  *   page id lies outside the pool take no part; bytes of positions from kv_len on are never read
  *   into the result.  Queries are used as fp16: exact for bf16 of magnitude in [2^-14, 65504] and 0,
- *   rounded outside.  Scales of keys are exact from 2^-15 on, and below rounded to multiples of 2^-22 (each
+ *   rounded to multiples of 2^-24 below; above, the row is NaN and the workspace reports it.  Scales of keys are exact from 2^-15 on, and below rounded to multiples of 2^-22 (each
  *   head's keys of magnitude below 2^-12, by up to 2^-20).  The scales of positions before kv_len must be finite (svd_paged_append
  *   writes no others).
  * Errors: SVD_ERR_INVALID_ARG for null or misaligned (16 bytes) pointers, sizes out of range, Hq %
  * Hkv != 0; SVD_ERR_WORKSPACE for a short workspace.  The workspace is zero-filled before its first
  * use and serves any number of calls in stream order, with the same heads and no more requests or
  * max_new than it was asked for; its first word gets bit 0 set if a bounded wait
- * of the kernel gave up (the output is then undefined); its second word, when non-zero, is one more
+ * of the kernel gave up (the output is then undefined) and bit 1 if a query was finite but above 65504
+ * in magnitude; its second word, when non-zero, is one more
  * than the number of polls after which a wait gives up (a test hook, as for svd_kv_attention).
  * SVD_ERR_UNSUPPORTED when n_requests * max_new * max_pages allow 2^31 tiles of 128 positions. */
 #define SVD_PAGED_UNIT_BYTES 2304

@@ -73,9 +73,9 @@ class PagedBatch:
         return self._window[self.now]
 
     @property
-    def gave_up(self):
-        """int32 [1], not 0 once a bounded wait of an attention kernel gave up: outputs since then are undefined.
-        Stays until it is zeroed."""
+    def attention_status(self):
+        """int32 [1], 0 while all is well; bit 0: a bounded wait of an attention kernel gave up, outputs since then
+        are undefined; bit 1: a finite query was above 65504 in magnitude, its row is NaN.  Stays until zeroed."""
         return self.ws[:4].view(torch.int32)
 
     def begin(self, n_new, emitted=None, stream=None):

@@ -1,7 +1,8 @@
 """The paged calls on the GPU in cases that once went wrong, against the fp64 reference: waits that give up
 with the copies of a short range in flight; one row of positions for several axes; rotated keys that are not finite or too
 large for fp32; masks of many heads far behind the window; small
-probabilities in fp32 outputs; keys of very small and very large scales."""
+probabilities in fp32 outputs; keys of very small and very large scales; queries
+beyond fp16."""
 import numpy as np
 import pytest
 import torch
@@ -207,3 +208,21 @@ def test_keys_of_any_scale(out_dtype, new, Hq, size):
     q = g.normal(size=(new, Hq, 128)) * min(0.6 / size, 12000.0)
     c = Attend([n], [new], Hq, 1, page, out_dtype, pool=pool, q=q)
     check(c, c.run(), (np.abs(d) < 2.0 ** -15).any())
+
+
+@pytest.mark.parametrize("lens,new", [([70, 3000], [1, 2]), ([900, 40], [300, 30])])
+@pytest.mark.parametrize("value,told", [(65280.0, 0), (65536.0, 2), (-3e38, 2), (np.inf, 0), (np.nan, 0)])
+def test_queries_beyond_fp16_are_reported(lens, new, value, told):
+    """One such value makes its row NaN and no other; what is not finite to begin with is not reported."""
+    g = np.random.default_rng(9)
+    q = g.normal(size=(sum(new), 10, 128))
+    c = Attend(lens, new, 10, 2, 32, q=q)
+    want = c.run()
+    assert c.ws[:4].view(torch.int32).item() == 0
+    q[-1, 6, 77] = value
+    c.dev[0].copy_(torch.from_numpy(q).to(torch.bfloat16))
+    got = c.run()
+    assert c.ws[:4].view(torch.int32).item() == told
+    assert np.isfinite(got[-1, 6]).all() if abs(value) < 65504 else np.isnan(got[-1, 6]).all()
+    got[-1, 6] = want[-1, 6]
+    assert np.array_equal(got, want)

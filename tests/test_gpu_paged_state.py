@@ -282,13 +282,13 @@ def test_a_wait_that_gave_up_is_seen():
     b.begin(i32(40))
     x, out = torch.randn((40, 4 * 128), device=DEV), torch.zeros((40, 2, 128), dtype=torch.bfloat16, device=DEV)
     b.layer(0, x, out)
-    assert b.gave_up.tolist() == [0]
+    assert b.attention_status.tolist() == [0]
     want = out.clone()
     b.ws[4:8].view(torch.int32).fill_(1)  # every wait that is not satisfied at once gives up
     b.layer(0, x, out)
-    assert b.gave_up.tolist() == [1]
+    assert b.attention_status.tolist() == [1]
     b.ws[4:8] = 0
     b.layer(0, x, out)
-    assert b.gave_up.tolist() == [1] and torch.equal(out, want)
-    b.gave_up.zero_()
-    assert b.gave_up.tolist() == [0]
+    assert b.attention_status.tolist() == [1] and torch.equal(out, want)
+    b.attention_status.zero_()
+    assert b.attention_status.tolist() == [0]
