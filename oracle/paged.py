@@ -146,6 +146,7 @@ def put(pages, slots, k, v, page):
     return pages
 
 
+@np.errstate(invalid="ignore")  # (bytes of positions that nobody asked for may be signalling NaNs)
 def get(pages, slots, page):
     """The fp64 keys and values that pages hold at slots: [T, Hkv, 128] each; 0 outside the pool."""
     T, H = len(slots), pages.shape[1]
