@@ -104,11 +104,13 @@ class PagedBatch:
         with self._on(stream):
             torch.where(who, -self.held[self.now], self.window, out=self.window)
 
-    @staticmethod
-    def _on(stream):
+    def _on(self, stream):
         if stream is None:
             return contextlib.nullcontext()
-        return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        if isinstance(stream, int):  # (an ExternalStream of 0 would be a new stream)
+            dev = self.q_start.device
+            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+        return torch.cuda.stream(stream)
 
     def _here(self, name: str, t, *dtypes):
         """The library takes addresses: a tensor of another type or place would be read as it lies."""
@@ -142,7 +144,8 @@ class PagedBatch:
         """Layer l's step: rotates and stores qkv [n_tokens][(Hq + 2 Hkv) * 128] (fp32, as
         svd_verify_linear writes it, or bf16) and writes its attention to out [n_tokens][Hq][128].
         positions, int32 [axes][n_tokens] (images: time, height, width) or [n_tokens] for all axes alike,
-        replaces the requests' own positions, which are the same on every axis.  n_tokens: the rows of qkv
+        replaces the requests' own positions, which are the same on every axis; the request of every token, for
+        offsets of its own, is torch.searchsorted(q_start, arange, right=True) - 1.  n_tokens: the rows of qkv
         that count (None: all of them, up to max_tokens); it covers the step's tokens, q_start's last entry."""
         T = min(qkv.shape[0], self.max_tokens) if n_tokens is None else int(n_tokens)
         width = (self.Hq + 2 * self.Hkv) * 128

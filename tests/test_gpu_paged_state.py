@@ -292,3 +292,30 @@ def test_a_wait_that_gave_up_is_seen():
     assert b.attention_status.tolist() == [1] and torch.equal(out, want)
     b.attention_status.zero_()
     assert b.attention_status.tolist() == [0]
+
+
+@pytest.mark.parametrize("handle", ["stream", "address", "default"])
+def test_streams_in_every_form(handle):
+    busy = torch.cuda.Stream()
+    s = torch.cuda.default_stream() if handle == "default" else torch.cuda.Stream()
+    given = s if handle == "stream" else s.cuda_stream
+    assert given == 0 or handle != "default"
+    b, warm = batch(2), batch(2)
+    new, who = i32(10, 20), torch.tensor([False, True], device=DEV)
+    warm.begin(new, stream=given)
+    warm.end(who, stream=given)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(40_000_000)  # what runs anywhere else comes too early
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(800_000_000)
+        b.begin(new, stream=given)
+        b.end(who, stream=given)
+        b.begin(new, stream=given)
+        s.synchronize()
+        assert not busy.query()
+        with torch.cuda.stream(s):
+            assert b.kv_len.tolist() == [20, 20] and b.held[b.now].tolist() == [20, 20]
+        assert not busy.query()
+    torch.cuda.synchronize()
+    whole(b)
