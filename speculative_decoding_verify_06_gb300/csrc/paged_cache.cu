@@ -43,15 +43,10 @@ struct TbAsk {
     __device__ bool in_order() const { return win >= 0 && emi >= 0 && emi <= win && win <= held; }
 };
 __device__ __forceinline__ TbAsk tb_ask(const TbArgs &A, int r) {
-    TbAsk a = {A.held[r], 0, 0};
-    if (!A.window) return a;
-    a.win = A.window[r];
-    if (!A.held_out) {
-        a.emi = A.emitted[r];
-    } else if (a.win > 0) {
-        a.emi = A.emitted ? A.emitted[r] : a.win;
-    } else {
-        a.win = -a.win;
+    TbAsk a = {A.held[r], A.window ? A.window[r] : 0, A.emitted ? A.emitted[r] : 0};
+    if (A.held_out) {
+        a.emi = a.win <= 0 ? 0 : A.emitted ? a.emi : a.win;
+        a.win = a.win < 0 ? -a.win : a.win;
     }
     return a;
 }
