@@ -582,13 +582,15 @@ def svd_paged_cache_bytes(n_kv_heads: int, page_size: int, n_pages: int) -> int:
     return int(load().svd_paged_cache_bytes(int(n_kv_heads), int(page_size), int(n_pages)))
 
 
+# (The paged calls leave the conversion of sizes to ctypes, which takes any integer type: int() on every size
+# costs 0.4 us of a call that takes 2.3 before its launch.)
 def svd_paged_tables(held, window, emitted, n_new, n_requests: int, page_size: int, table,
                      max_pages: int, free_ids, n_free, n_pages: int, table_out, free_out, n_free_out,
                      kv_len, q_start, slots, positions, max_tokens: int, status, stream=None):
     _check("svd_paged_tables", load().svd_paged_tables(
-        _ptr(held), _ptr(window), _ptr(emitted), _ptr(n_new), int(n_requests), int(page_size), _ptr(table),
-        int(max_pages), _ptr(free_ids), _ptr(n_free), int(n_pages), _ptr(table_out), _ptr(free_out),
-        _ptr(n_free_out), _ptr(kv_len), _ptr(q_start), _ptr(slots), _ptr(positions), int(max_tokens),
+        _ptr(held), _ptr(window), _ptr(emitted), _ptr(n_new), n_requests, page_size, _ptr(table),
+        max_pages, _ptr(free_ids), _ptr(n_free), n_pages, _ptr(table_out), _ptr(free_out),
+        _ptr(n_free_out), _ptr(kv_len), _ptr(q_start), _ptr(slots), _ptr(positions), max_tokens,
         _ptr(status), _stream(stream)))
 
 
@@ -597,25 +599,25 @@ def svd_paged_advance(held, window, emitted, n_new, n_requests: int, max_new: in
                       table_out, free_out, n_free_out, kv_len, q_start, slots, positions,
                       max_tokens: int, status, stream=None):
     _check("svd_paged_advance", load().svd_paged_advance(
-        _ptr(held), _ptr(window), _ptr(emitted), _ptr(n_new), int(n_requests), int(max_new),
-        int(page_size), _ptr(table), int(max_pages), _ptr(free_ids), _ptr(n_free), int(n_pages),
+        _ptr(held), _ptr(window), _ptr(emitted), _ptr(n_new), n_requests, max_new,
+        page_size, _ptr(table), max_pages, _ptr(free_ids), _ptr(n_free), n_pages,
         _ptr(held_out), _ptr(window_out), _ptr(table_out), _ptr(free_out), _ptr(n_free_out), _ptr(kv_len),
-        _ptr(q_start), _ptr(slots), _ptr(positions), int(max_tokens), _ptr(status), _stream(stream)))
+        _ptr(q_start), _ptr(slots), _ptr(positions), max_tokens, _ptr(status), _stream(stream)))
 
 
 def svd_paged_append(qkv, ld: int, n_tokens: int, n_q_heads: int, n_kv_heads: int, slots, pages,
                      page_size: int, n_pages: int, q, rope: Rope | None = None, positions=None,
                      positions_ld: int = 0, dtype: int = SVD_F32, status=None, stream=None):
     _check("svd_paged_append", load().svd_paged_append(
-        _ptr(qkv), int(dtype), int(ld), int(n_tokens), int(n_q_heads), int(n_kv_heads),
-        None if rope is None else rope._p, _ptr(positions), int(positions_ld), _ptr(slots), _ptr(pages),
-        int(page_size), int(n_pages), _ptr(q), _ptr(status), _stream(stream)))
+        _ptr(qkv), dtype, ld, n_tokens, n_q_heads, n_kv_heads,
+        None if rope is None else rope._p, _ptr(positions), positions_ld, _ptr(slots), _ptr(pages),
+        page_size, n_pages, _ptr(q), _ptr(status), _stream(stream)))
 
 
 def svd_paged_read(slots, n_tokens: int, n_kv_heads: int, pages, page_size: int, n_pages: int, k, v,
                    stream=None):
     _check("svd_paged_read", load().svd_paged_read(
-        _ptr(slots), int(n_tokens), int(n_kv_heads), _ptr(pages), int(page_size), int(n_pages), _ptr(k),
+        _ptr(slots), n_tokens, n_kv_heads, _ptr(pages), page_size, n_pages, _ptr(k),
         _ptr(v), _stream(stream)))
 
 
@@ -632,6 +634,6 @@ def svd_paged_attention(q, n_tokens: int, kv_len, q_start, n_requests: int, max_
     if not workspace_bytes and workspace is not None and not isinstance(workspace, int):
         workspace_bytes = workspace.numel() * workspace.element_size()
     _check("svd_paged_attention", load().svd_paged_attention(
-        _ptr(q), int(n_tokens), _ptr(kv_len), _ptr(q_start), int(n_requests), int(max_new), _ptr(table),
-        int(max_pages), _ptr(pages), int(page_size), int(n_pages), int(n_q_heads), int(n_kv_heads),
-        float(scale), _ptr(out), int(out_dtype), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+        _ptr(q), n_tokens, _ptr(kv_len), _ptr(q_start), n_requests, max_new, _ptr(table),
+        max_pages, _ptr(pages), page_size, n_pages, n_q_heads, n_kv_heads,
+        scale, _ptr(out), out_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))

@@ -19,9 +19,9 @@ class Address(enum.IntEnum):
     A = 16
 
 
-@pytest.mark.parametrize("size", [int, np.int32, np.int64, float])
-def test_wrappers_convert_sizes_and_addresses(size):
-    """Sizes of any numeric type and addresses of any integer type reach the library, whose own
+@pytest.mark.parametrize("size", [int, np.int32, np.int64, torch.tensor])
+def test_wrappers_take_sizes_and_addresses_of_any_integer_type(size):
+    """Sizes and addresses of any integer type reach the library, whose own
     refusal (a page of 17 positions) is what comes back."""
     a, n = Address.A, size(2)
     calls = [lambda: svd.svd_paged_read(a, n, n, a, size(17), n, a, a, stream=0),
