@@ -29,7 +29,8 @@ class PagedBatch:
 
     begin() opens a step, layer() runs one layer's append and attention.  Between two begin() calls
     the device tensors q_start, kv_len, slots, positions and status describe the step's tokens; held and
-    window are the state that the next begin() goes on from."""
+    window are the state that the next begin() goes on from.  stream: a torch stream or its address, None for
+    the current one; a tensor handed to a call stays alive until that stream has used it."""
 
     def __init__(self, requests: int, layers: int, n_pages: int, page_size: int = 64, max_len: int = 32768,
                  max_window: int = 8, n_q_heads: int = 40, n_kv_heads: int = 8, rope: svd.Rope | None = None,
@@ -158,8 +159,10 @@ class PagedBatch:
         if out.numel() < T * self.Hq * 128 or not out.is_contiguous():
             raise ValueError(f"out: [{T}][{self.Hq}][128] in one piece, got {tuple(out.shape)}")
         pos, pos_ld = self._positions(positions, T)
+        if T == 0:
+            return out
         pool = self.pools[l]
-        svd.svd_paged_append(qkv, qkv.stride(0), T, self.Hq, self.Hkv, self.slots, pool, self.page, self.n_pages, self.q,
+        svd.svd_paged_append(qkv, qkv.stride(0) if T > 1 else width, T, self.Hq, self.Hkv, self.slots, pool, self.page, self.n_pages, self.q,
                              rope=self.rope, positions=pos, positions_ld=pos_ld,
                              dtype=svd.SVD_F32 if qkv.dtype == torch.float32 else svd.SVD_BF16, status=self.bad,
                              stream=stream)

@@ -162,3 +162,18 @@ def test_advance_refusals(lib, change):
 def test_ends_of_another_form_are_refused(who):
     with pytest.raises(ValueError, match="who"):
         batch().end(who)
+
+
+def test_a_step_without_tokens():
+    """Every request idle: no rows, for which torch has no address either."""
+    qkv, out = rows(0)
+    assert batch().layer(0, qkv, out) is out
+    assert batch().layer(0, *rows(3), n_tokens=0).shape == (3, 4, 128)
+
+
+def test_one_row_of_any_stride(calls):
+    b = batch()
+    qkv = torch.zeros((8 * 128, 1)).t()  # [1][1024], whose rows torch says lie one element apart
+    b.layer(0, qkv, rows(1)[1])
+    a = dict(calls)["svd_paged_append"]
+    assert a["n_tokens"] == 1 and a["ld"] >= 8 * 128 and a["ld"] % 4 == 0
