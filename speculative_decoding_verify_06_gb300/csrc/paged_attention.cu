@@ -36,12 +36,12 @@
 // are cut out of S, and their V scales are replaced by 0, whatever their bytes.
 //
 // What bounds it.  Every cache byte is read once, 144 per position and kv head, but each takes work that
-// no pipe does at HBM's pace: a tile takes 4535 warp instructions at 20 rows, of
-// which the SM issues 72 % of what it could, with instruction
-// fetch and the chain copy - K - S - P - O behind the rest.  262144 positions of 8 kv heads, 20 rows: 91.5 us,
-// 3.3 TB/s of cache; 64 ragged requests of up to 16K: 214 us, 3.35 TB/s; 200 requests of 2K, one
-// token, fp32: 102 us, 2.5 TB/s; 32768 positions: 23.5 us, of which 11 to 14 do not depend on the
-// length (lines through 8K and 16K, and through 32K and 262K); two chunks of 512 tokens behind 8K: 261 us, 547 TFLOP/s.
+// no pipe does at HBM's pace: a tile takes 4538 warp instructions at 20 rows, of
+// which the SM issues 73 % of what it could, with instruction
+// fetch and the chain copy - K - S - P - O behind the rest.  262144 positions of 8 kv heads, 20 rows: 91.4 us,
+// 3.3 TB/s of cache; 64 ragged requests of up to 16K: 213 us, 3.35 TB/s; 200 requests of 2K, one
+// token, fp32: 103 us, 2.5 TB/s; 32768 positions: 23.4 us, of which 11 to 14 do not depend on the
+// length (lines through 8K and 16K, and through 32K and 262K); two chunks of 512 tokens behind 8K: 260 us, 550 TFLOP/s.
 //
 // What was measured on the way (262K / chunk of 512): K and softmax in the same four warps, 105 / 640 us;
 // four roles with one MMA warp, 107 / 450; two MMA warps and halves, 103 / 422; queries fetched

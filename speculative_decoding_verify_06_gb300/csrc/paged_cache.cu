@@ -20,7 +20,7 @@ namespace svd {
 // bytes each, from L2), keeps them in shared memory, and then fills its share of the outputs, each
 // element a function of the sums and the inputs alone (no CTA waits for another).  What bounds it is
 // latency, a launch and three block-wide sums one after the other: 3.8 us for 8 requests (95 KB moved), 5.9
-// us for 256 with 131 K table entries, 6.4 us for 48 prompts with 49 K new tokens.  (With 64-bit divisions in
+// us for 256 with 131 K table entries, 6.5 us for 48 prompts with 49 K new tokens.  (With 64-bit divisions in
 // the sums 4.1, 6.3 and 6.9.)
 constexpr int kTbThreads = 512;
 constexpr int kTbWarps = kTbThreads / 32;
@@ -290,11 +290,13 @@ int paged_advance(const int32_t *held, const int32_t *window, const int32_t *emi
 //
 // Split.  A CTA of four warps takes a token, its warps every fourth head, four heads fetched ahead;
 // calls of few tokens spread a token's heads over several CTAs.  4099 tokens of 32 + 2 x 8 heads in
-// bf16 take 41 us (88 MB, 2.2 TB/s), 256 tokens of 40 + 2 x 8 in fp32 8.7 us: what bounds the first is issue
-// (74 % at 173 warp instructions a head on average; before branches left the loops over dimensions, copies
+// bf16 take 42 us (88 MB, 2.1 TB/s), 256 tokens of 40 + 2 x 8 in fp32 8.8 us: what bounds the first is issue
+// (72 % at 173 warp instructions a head on average; before branches left the loops over dimensions, copies
 // with a part taken out counted 24 for a query head, 248 for a value head and 529 for a key head).
-// With the read-back 50.4 us; eight warps to a CTA 51.4, two 52.0; six or seven CTAs to an SM 54.9 and 52.5
-// (and 10.2 and 10.4 for the 256 tokens, against 11.0); a warp a head and no loop 89.
+// With the read-back 51.6 us.  Compared when that was 50.4 (before finite and other blocks of a head were
+// told apart): eight warps to a CTA 51.4, two 52.0; six or seven CTAs to an SM 54.9 and 52.5 (and 10.2 and
+// 10.4 for the 256 tokens, against 11.0); a warp a head and no loop 89.  The rare paths behind one call that
+// makes both: 57.8, in a loop over them: 59.5.
 constexpr int kApWarps = 4;
 
 struct RopeArgs {
