@@ -478,8 +478,8 @@ int svd_kv_attention(const uint16_t *q, const void *cache, int capacity, int n_q
  *   written.  max_new bounds the tokens of a request (later ones are not written).  Positions whose
  *   page id lies outside the pool take no part; bytes of positions from kv_len on are never read
  *   into the result.  Queries are used as fp16: exact for bf16 of magnitude in [2^-14, 65504] and 0,
- *   rounded to multiples of 2^-24 below; above, the row is NaN and the workspace reports it.  Scales of keys are exact from 2^-15 on, and below rounded to multiples of 2^-22 (each
- *   head's keys of magnitude below 2^-12, by up to 2^-20).  The scales of positions before kv_len must be finite (svd_paged_append
+ *   rounded to multiples of 2^-24 below; above, the row is NaN and the workspace reports it.  Scales of keys are exact from 2^-15 on, and below rounded to multiples of 2^-22
+ *   (blocks whose keys stay below 2^-12 in magnitude: up to 2^-20 a key).  The scales of positions before kv_len must be finite (svd_paged_append
  *   writes no others).
  * Errors: SVD_ERR_INVALID_ARG for null or misaligned (16 bytes) pointers, sizes out of range, Hq %
  * Hkv != 0; SVD_ERR_WORKSPACE for a short workspace.  The workspace is zero-filled before its first

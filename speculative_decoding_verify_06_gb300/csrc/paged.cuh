@@ -10,7 +10,8 @@
 //   bytes 2176..2303  V scales fp16 [4 blocks][16 positions]
 // Every byte belongs to one position, so appends of different positions never meet in a byte.
 // The value of code c is d (c - 8).  d has eight significant bits: d (c - 8) then needs at most
-// eleven, so it is exact in fp16 and the attention kernel's operands carry no rounding at all.
+// eleven, so it is exact in fp16 and the attention kernel's operands carry no rounding (but for blocks
+// of keys below 2^-12, whose d it holds to a multiple of 2^-22).
 #pragma once
 
 #include "svd_common.cuh"
