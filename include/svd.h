@@ -530,6 +530,84 @@ int svd_paged_attention(const uint16_t *q, int n_tokens, const int32_t *kv_len,
                         int n_q_heads, int n_kv_heads, float scale, void *out, int out_dtype,
                         void *workspace, size_t workspace_bytes, svd_stream_t stream);
 
+/* ---- paged cache held in 8 bits -------------------------------------------------------------- */
+/* The same pool of pages, block tables and ragged windows with 8 bits a value, for models whose answers do
+ * not stand 4.5 ("100 tokens per second ...", "The wall": the page keeps its keys at 8 bits).
+ *
+ * A page holds page_size positions (a multiple of 16 up to SVD_PAGED_PAGE_MAX) of every kv head, [page][kv head]
+ * [page_size / 16] units of 16 positions and SVD_PAGED8_UNIT_BYTES: K codes [16 positions][128 bytes], the 16 bytes of
+ * dimensions 16c .. 16c + 15 at place c ^ (position % 8); V codes [128 dimensions][16 positions]; the scales of the unit's
+ * keys and of its values, fp32; 8 unused bytes.  A code is a float of 1 sign, 4 exponent and 3 fraction bits (e4m3: largest 448,
+ * smallest 2^-9); it stands for code * scale.  A scale is a power of two from 2^-64 to 2^7.  svd_paged_tables and
+ * svd_paged_advance serve both kinds of pool.
+ *
+ * svd_paged8_append: request r has the tokens q_start[r] .. q_start[r + 1] - 1, the last of them at position
+ *   kv_len[r] - 1 of the request, which lies in page table[r][position / page_size].  Rows of qkv, rotation and q as for
+ *   svd_paged_append, but a token from q_start[n_requests] on is left alone, its row of q too.  Per unit, kv head, and K and V
+ *   apart: e = the smallest exponent (-64..7) with 448 * 2^e >= every magnitude that the call brings to the unit; where
+ *   the unit has positions before the call's first one in it, at least the exponent it has, and if it grows, their codes are
+ *   rounded again to code * scale / 2^e.  New codes are value / 2^e to nearest (ties to even); scale and codes are decided as in
+ *   exact arithmetic.  NaN counts as 0 and magnitudes end at 57344; status (NULL, or int32 [n_tokens] that the call ORs
+ *   into) has SVD_ST_NONFINITE, and SVD_ST_BAD_SLOT for a token whose position has no page in the pool: it is not
+ *   stored.  Bytes of other positions stay.  A page belongs to one request.
+ * svd_paged8_read: the values that the pool holds at slots[t] (page * page_size + offset), fp32 [T][Hkv][128] each (0
+ *   for a slot outside the pool).
+ * svd_paged8_attention: as svd_paged_attention, tokens, masks, outputs, workspace and errors alike.  A query row is used
+ *   as a power of two times the sum of two e4m3 parts: exact for bf16 down to 2^-14 of the row's largest, and to 2^-22 of
+ *   it below; there is no bound on its magnitude.  A row with a query that is not finite is NaN.  The softmax's weights are
+ *   used as fp16 (as two fp16 parts for fp32 outputs), and the sums are fp32.  Codes of positions before kv_len must be
+ *   finite (svd_paged8_append writes no others); bytes of later ones may be anything, but for the scales of the units that hold
+ *   positions.  The workspace's first word gets bit 0 only.
+ *
+ * ---- moving pages (of either kind of pool)
+ * svd_paged_fork: requests become copies of others, for several answers to one prompt or a search.  parent[r] < 0
+ *   or parent[r] = r: r stays as it is.  Else r becomes what request parent[r] keeps: held - window + emitted positions, with the
+ *   state as svd_paged_advance carries it (window, emitted NULL: 0, all).  r's own pages are used first; surplus ones go
+ *   onto the stack of free pages, then missing ones are taken from its top; both in request order, then page
+ *   order.  held_out, window_out (0 for a child: emitted says nothing of it), table_out, free_out, n_free_out: the new
+ *   state.  copy_from, copy_to [n_pages]: the pages to copy, in request and page order, *n_copies of them, -1 behind.  A
+ *   child that cannot be served stays as it is: SVD_ST_BAD_REQUEST for a parent that does not exist, is a child
+ *   itself or has a count out of order, or held beyond the row; SVD_ST_NO_PAGES.  Outputs must not be the inputs.
+ * svd_paged_compact: the pages in use, U of them (all ids in the first ceil(held / page_size) entries of the rows; ids outside
+ *   the pool stay and do not count), move to ids 0 .. U - 1: the used ids from U on, ascending, to the unused ones below
+ *   U, ascending.  table_out (-1 past a row's pages), the stack of free pages anew (every page that no row holds, U on
+ *   top) and the copies as for svd_paged_fork.  n_pages <= SVD_PAGED_COMPACT_MAX_PAGES, else SVD_ERR_UNSUPPORTED.
+ * svd_paged_copy: copies page copy_from[i] to page copy_to[i], i < min(*n_copies, max_copies), in each of n_pools pools (a
+ *   host array of device pointers, 16-byte aligned) of n_pages pages of page_bytes (a multiple of 16).  Pairs with an
+ *   id outside the pool are passed over.  No page may be written twice, or be both read and written. */
+#define SVD_PAGED8_UNIT_BYTES 4112
+#define SVD_PAGED_MAX_POOLS 128 /* of one launch; svd_paged_copy makes more launches for more */
+#define SVD_PAGED_COMPACT_MAX_PAGES 1048576
+size_t svd_paged8_cache_bytes(int n_kv_heads, int page_size, int64_t n_pages);
+int svd_paged8_append(const void *qkv, int dtype, int64_t ld, int n_tokens, int n_q_heads,
+                      int n_kv_heads, const svd_rope *rope, const int32_t *positions,
+                      int64_t positions_ld, const int32_t *kv_len, const int32_t *q_start,
+                      int n_requests, const int32_t *table, int max_pages, void *pages,
+                      int page_size, int64_t n_pages, uint16_t *q, int32_t *status,
+                      svd_stream_t stream);
+int svd_paged8_read(const int64_t *slots, int n_tokens, int n_kv_heads, const void *pages,
+                    int page_size, int64_t n_pages, float *k, float *v, svd_stream_t stream);
+size_t svd_paged8_attention_workspace_bytes(int n_q_heads, int n_kv_heads, int n_requests,
+                                            int max_new);
+int svd_paged8_attention(const uint16_t *q, int n_tokens, const int32_t *kv_len,
+                         const int32_t *q_start, int n_requests, int max_new, const int32_t *table,
+                         int max_pages, const void *pages, int page_size, int64_t n_pages,
+                         int n_q_heads, int n_kv_heads, float scale, void *out, int out_dtype,
+                         void *workspace, size_t workspace_bytes, svd_stream_t stream);
+int svd_paged_fork(const int32_t *held, const int32_t *window, const int32_t *emitted,
+                   const int32_t *parent, int n_requests, int page_size, const int32_t *table,
+                   int max_pages, const int32_t *free_ids, const int32_t *n_free, int64_t n_pages,
+                   int32_t *held_out, int32_t *window_out, int32_t *table_out, int32_t *free_out,
+                   int32_t *n_free_out, int32_t *copy_from, int32_t *copy_to, int32_t *n_copies,
+                   int32_t *status, svd_stream_t stream);
+int svd_paged_compact(const int32_t *held, int n_requests, int page_size, const int32_t *table,
+                      int max_pages, int64_t n_pages, int32_t *table_out, int32_t *free_out,
+                      int32_t *n_free_out, int32_t *copy_from, int32_t *copy_to, int32_t *n_copies,
+                      svd_stream_t stream);
+int svd_paged_copy(void *const *pools, int n_pools, int64_t page_bytes, int64_t n_pages,
+                   const int32_t *copy_from, const int32_t *copy_to, const int32_t *n_copies,
+                   int64_t max_copies, svd_stream_t stream);
+
 /* ---- host-side companions: depth policy and n-gram drafter ----------------------------- */
 /* No GPU work; safe to call from any host thread (a handle is not shared between threads
  * without the caller's locking).

@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsvd.so")
 SOURCES = ["verify_linear.cu", "kquant.cu", "kv_attention.cu", "paged_cache.cu",
-           "paged_attention.cu", "accept.cu", "sampler.cu", "api.cu", "host_policy.cpp"]
+           "paged_attention.cu", "paged8_cache.cu", "paged8_attention.cu", "paged_moves.cu", "accept.cu", "sampler.cu", "api.cu", "host_policy.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 

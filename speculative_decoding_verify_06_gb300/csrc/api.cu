@@ -54,6 +54,27 @@ int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32
                     int64_t n_pages, int Hq, int Hkv, float scale, void *out, int out_dtype, void *ws,
                     size_t ws_bytes, cudaStream_t stream);
 
+int paged8_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv, const svd_rope *rope,
+                  const int32_t *positions, int64_t positions_ld, const int32_t *kv_len, const int32_t *q_start, int R,
+                  const int32_t *table, int width, void *pages, int page, int64_t n_pages, void *q, int32_t *status,
+                  cudaStream_t stream);
+int paged8_read(const int64_t *slots, int T, int Hkv, const void *pages, int page, int64_t n_pages, float *k, float *v,
+                cudaStream_t stream);
+int paged8_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,
+                     int max_new, const int32_t *table, int width, const void *pages, int page,
+                     int64_t n_pages, int Hq, int Hkv, float scale, void *out, int out_dtype, void *ws,
+                     size_t ws_bytes, cudaStream_t stream);
+int paged_fork(const int32_t *held, const int32_t *window, const int32_t *emitted, const int32_t *parent, int R,
+               int page, const int32_t *table, int width, const int32_t *free_ids, const int32_t *n_free,
+               int64_t n_pages, int32_t *held_out, int32_t *window_out, int32_t *table_out, int32_t *free_out,
+               int32_t *n_free_out, int32_t *copy_from, int32_t *copy_to, int32_t *n_copies, int32_t *status,
+               cudaStream_t stream);
+int paged_compact(const int32_t *held, int R, int page, const int32_t *table, int width, int64_t n_pages,
+                  int32_t *table_out, int32_t *free_out, int32_t *n_free_out, int32_t *copy_from, int32_t *copy_to,
+                  int32_t *n_copies, cudaStream_t stream);
+int paged_copy(void *const *pools, int n_pools, int64_t page_bytes, int64_t n_pages, const int32_t *from,
+               const int32_t *to, const int32_t *n_copies, int64_t most, cudaStream_t stream);
+
 static thread_local int g_last_cuda_error = 0;
 void set_cuda_error(cudaError_t e) { g_last_cuda_error = (int)e; }
 
@@ -246,6 +267,57 @@ int svd_paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const i
                         size_t ws_bytes, svd_stream_t stream) {
     return svd::paged_attention(q, T, kv_len, q_start, R, max_new, table, width, pages, page, n_pages, Hq,
                                 Hkv, scale, out, out_dtype, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+size_t svd_paged8_cache_bytes(int n_kv_heads, int page_size, int64_t n_pages) {
+    return svd_paged_cache_bytes(n_kv_heads, page_size, n_pages) / SVD_PAGED_UNIT_BYTES * SVD_PAGED8_UNIT_BYTES;
+}
+
+int svd_paged8_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv, const svd_rope *rope,
+                      const int32_t *positions, int64_t positions_ld, const int32_t *kv_len,
+                      const int32_t *q_start, int R, const int32_t *table, int width, void *pages, int page,
+                      int64_t n_pages, uint16_t *q, int32_t *status, svd_stream_t stream) {
+    return svd::paged8_append(qkv, dtype, ld, T, Hq, Hkv, rope, positions, positions_ld, kv_len, q_start, R, table,
+                              width, pages, page, n_pages, q, status, (cudaStream_t)stream);
+}
+int svd_paged8_read(const int64_t *slots, int T, int Hkv, const void *pages, int page, int64_t n_pages,
+                    float *k, float *v, svd_stream_t stream) {
+    return svd::paged8_read(slots, T, Hkv, pages, page, n_pages, k, v, (cudaStream_t)stream);
+}
+
+size_t svd_paged8_attention_workspace_bytes(int Hq, int Hkv, int R, int max_new) {
+    return svd::paged_attention_ws_bytes(Hq, Hkv, R, max_new);
+}
+
+int svd_paged8_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,
+                         int max_new, const int32_t *table, int width, const void *pages, int page,
+                         int64_t n_pages, int Hq, int Hkv, float scale, void *out, int out_dtype, void *ws,
+                         size_t ws_bytes, svd_stream_t stream) {
+    return svd::paged8_attention(q, T, kv_len, q_start, R, max_new, table, width, pages, page, n_pages, Hq,
+                                 Hkv, scale, out, out_dtype, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+int svd_paged_fork(const int32_t *held, const int32_t *window, const int32_t *emitted, const int32_t *parent,
+                   int R, int page, const int32_t *table, int width, const int32_t *free_ids,
+                   const int32_t *n_free, int64_t n_pages, int32_t *held_out, int32_t *window_out,
+                   int32_t *table_out, int32_t *free_out, int32_t *n_free_out, int32_t *copy_from,
+                   int32_t *copy_to, int32_t *n_copies, int32_t *status, svd_stream_t stream) {
+    return svd::paged_fork(held, window, emitted, parent, R, page, table, width, free_ids, n_free, n_pages, held_out,
+                           window_out, table_out, free_out, n_free_out, copy_from, copy_to, n_copies, status,
+                           (cudaStream_t)stream);
+}
+
+int svd_paged_compact(const int32_t *held, int R, int page, const int32_t *table, int width, int64_t n_pages,
+                      int32_t *table_out, int32_t *free_out, int32_t *n_free_out, int32_t *copy_from,
+                      int32_t *copy_to, int32_t *n_copies, svd_stream_t stream) {
+    return svd::paged_compact(held, R, page, table, width, n_pages, table_out, free_out, n_free_out, copy_from, copy_to,
+                              n_copies, (cudaStream_t)stream);
+}
+
+int svd_paged_copy(void *const *pools, int n_pools, int64_t page_bytes, int64_t n_pages, const int32_t *copy_from,
+                   const int32_t *copy_to, const int32_t *n_copies, int64_t max_copies, svd_stream_t stream) {
+    return svd::paged_copy(pools, n_pools, page_bytes, n_pages, copy_from, copy_to, n_copies, max_copies,
+                           (cudaStream_t)stream);
 }
 
 int svd_graph_begin(svd_stream_t stream) {

@@ -49,6 +49,43 @@ inline cudaError_t allow_smem(size_t bytes) {
     return e;
 }
 
+// ---- sums over requests (block tables, forks, compaction) ------------------------------------
+constexpr int kTbThreads = 512;
+constexpr int kTbWarps = kTbThreads / 32;
+
+// Inclusive sum over the block of one 64-bit value per thread; *total gets the block's sum.
+__device__ __forceinline__ unsigned long long tb_scan(unsigned long long v, unsigned long long *total,
+                                                      unsigned long long *s_w) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long u = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += u;
+    }
+    __syncthreads();  // s_w may still be read from the scan before
+    if (lane == 31) s_w[warp] = v;
+    __syncthreads();
+    unsigned long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kTbWarps; ++w) {
+        const unsigned long long x = s_w[w];
+        if (w < warp) before += x;
+        all += x;
+    }
+    *total = all;
+    return v + before;
+}
+
+// The last index r in [0, n) with a[r] <= x (a ascending, a[0] <= x).
+__device__ __forceinline__ int tb_last_le(const int *a, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
 inline bool pg_page_size_ok(int ps) { return ps >= 16 && ps <= SVD_PAGED_PAGE_MAX && ps % 16 == 0; }
 inline bool pg_pool_ok(int n_kv_heads, int page_size, int64_t n_pages) {
     return n_kv_heads >= 1 && n_kv_heads <= 1024 && pg_page_size_ok(page_size) && n_pages >= 1 &&

@@ -52,6 +52,9 @@ SVD_PAGED_PAGE_MAX = 256
 SVD_PAGED_MAX_REQUESTS = 4096
 SVD_ROPE_MAX_PAIRS = 64
 SVD_ROPE_MAX_AXES = 4
+SVD_PAGED8_UNIT_BYTES = 4112
+SVD_PAGED_MAX_POOLS = 128
+SVD_PAGED_COMPACT_MAX_PAGES = 1048576
 
 # Every symbol include/svd.h declares (checked by the CPU test suite).
 EXPORTS = (
@@ -71,6 +74,8 @@ EXPORTS = (
     "svd_kv_attention_workspace_bytes", "svd_kv_attention", "svd_kv_attention_append",
     "svd_paged_cache_bytes", "svd_paged_tables", "svd_paged_advance", "svd_paged_append", "svd_paged_read",
     "svd_paged_attention_workspace_bytes", "svd_paged_attention",
+    "svd_paged8_cache_bytes", "svd_paged8_append", "svd_paged8_read", "svd_paged8_attention_workspace_bytes",
+    "svd_paged8_attention", "svd_paged_fork", "svd_paged_compact", "svd_paged_copy",
 )
 
 
@@ -134,6 +139,18 @@ class Rope:
     @property
     def n_axes(self) -> int:
         return self._s.n_axes
+
+
+class Pools:
+    """The pools of several layers (tensors, which it keeps alive, or addresses) and the bytes of a page in each."""
+
+    def __init__(self, pools, page_bytes: int):
+        self.pools, self.page_bytes = list(pools), int(page_bytes)
+        self._a = (ctypes.c_void_p * max(len(self.pools), 1))(*[_ptr(p) for p in self.pools])
+        self._p = ctypes.addressof(self._a)
+
+    def __len__(self) -> int:
+        return len(self.pools)
 
 
 class Sampler:
@@ -219,6 +236,15 @@ def load(path: str = LIB_PATH):
             "svd_paged_attention_workspace_bytes": (sz, [i32, i32, i32, i32]),
             "svd_paged_attention": (i32, [P, i32, P, P, i32, i32, P, i32, P, i32, i64, i32, i32,
                                           ctypes.c_float, P, i32, P, sz, P]),
+            "svd_paged8_cache_bytes": (sz, [i32, i32, i64]),
+            "svd_paged8_append": (i32, [P, i32, i64, i32, i32, i32, P, P, i64, P, P, i32, P, i32, P, i32, i64, P, P, P]),
+            "svd_paged8_read": (i32, [P, i32, i32, P, i32, i64, P, P, P]),
+            "svd_paged8_attention_workspace_bytes": (sz, [i32, i32, i32, i32]),
+            "svd_paged8_attention": (i32, [P, i32, P, P, i32, i32, P, i32, P, i32, i64, i32, i32,
+                                           ctypes.c_float, P, i32, P, sz, P]),
+            "svd_paged_fork": (i32, [P, P, P, P, i32, i32, P, i32, P, P, i64, P, P, P, P, P, P, P, P, P, P]),
+            "svd_paged_compact": (i32, [P, i32, i32, P, i32, i64, P, P, P, P, P, P, P]),
+            "svd_paged_copy": (i32, [P, i32, i64, i64, P, P, P, i64, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -637,3 +663,63 @@ def svd_paged_attention(q, n_tokens: int, kv_len, q_start, n_requests: int, max_
         _ptr(q), n_tokens, _ptr(kv_len), _ptr(q_start), n_requests, max_new, _ptr(table),
         max_pages, _ptr(pages), page_size, n_pages, n_q_heads, n_kv_heads,
         scale, _ptr(out), out_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def svd_paged8_cache_bytes(n_kv_heads: int, page_size: int, n_pages: int) -> int:
+    return int(load().svd_paged8_cache_bytes(int(n_kv_heads), int(page_size), int(n_pages)))
+
+
+def svd_paged8_append(qkv, ld: int, n_tokens: int, n_q_heads: int, n_kv_heads: int, kv_len, q_start, n_requests: int,
+                      table, max_pages: int, pages, page_size: int, n_pages: int, q, rope: Rope | None = None,
+                      positions=None, positions_ld: int = 0, dtype: int = SVD_F32, status=None, stream=None):
+    _check("svd_paged8_append", load().svd_paged8_append(
+        _ptr(qkv), dtype, ld, n_tokens, n_q_heads, n_kv_heads, None if rope is None else rope._p, _ptr(positions),
+        positions_ld, _ptr(kv_len), _ptr(q_start), n_requests, _ptr(table), max_pages, _ptr(pages), page_size, n_pages,
+        _ptr(q), _ptr(status), _stream(stream)))
+
+
+def svd_paged8_read(slots, n_tokens: int, n_kv_heads: int, pages, page_size: int, n_pages: int, k, v,
+                    stream=None):
+    _check("svd_paged8_read", load().svd_paged8_read(
+        _ptr(slots), n_tokens, n_kv_heads, _ptr(pages), page_size, n_pages, _ptr(k), _ptr(v), _stream(stream)))
+
+
+def svd_paged8_attention_workspace_bytes(n_q_heads: int, n_kv_heads: int, n_requests: int,
+                                         max_new: int) -> int:
+    return int(load().svd_paged8_attention_workspace_bytes(
+        int(n_q_heads), int(n_kv_heads), int(n_requests), int(max_new)))
+
+
+def svd_paged8_attention(q, n_tokens: int, kv_len, q_start, n_requests: int, max_new: int, table,
+                         max_pages: int, pages, page_size: int, n_pages: int, n_q_heads: int,
+                         n_kv_heads: int, scale: float, out, out_dtype: int, workspace,
+                         workspace_bytes: int = 0, stream=None):
+    if not workspace_bytes and workspace is not None and not isinstance(workspace, int):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("svd_paged8_attention", load().svd_paged8_attention(
+        _ptr(q), n_tokens, _ptr(kv_len), _ptr(q_start), n_requests, max_new, _ptr(table),
+        max_pages, _ptr(pages), page_size, n_pages, n_q_heads, n_kv_heads,
+        scale, _ptr(out), out_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def svd_paged_fork(held, window, emitted, parent, n_requests: int, page_size: int, table, max_pages: int, free_ids,
+                   n_free, n_pages: int, held_out, window_out, table_out, free_out, n_free_out, copy_from, copy_to,
+                   n_copies, status, stream=None):
+    _check("svd_paged_fork", load().svd_paged_fork(
+        _ptr(held), _ptr(window), _ptr(emitted), _ptr(parent), n_requests, page_size, _ptr(table), max_pages,
+        _ptr(free_ids), _ptr(n_free), n_pages, _ptr(held_out), _ptr(window_out), _ptr(table_out), _ptr(free_out),
+        _ptr(n_free_out), _ptr(copy_from), _ptr(copy_to), _ptr(n_copies), _ptr(status), _stream(stream)))
+
+
+def svd_paged_compact(held, n_requests: int, page_size: int, table, max_pages: int, n_pages: int, table_out, free_out,
+                      n_free_out, copy_from, copy_to, n_copies, stream=None):
+    _check("svd_paged_compact", load().svd_paged_compact(
+        _ptr(held), n_requests, page_size, _ptr(table), max_pages, n_pages, _ptr(table_out), _ptr(free_out),
+        _ptr(n_free_out), _ptr(copy_from), _ptr(copy_to), _ptr(n_copies), _stream(stream)))
+
+
+def svd_paged_copy(pools: Pools, n_pages: int, copy_from, copy_to, n_copies, max_copies: int, stream=None):
+    """Page copy_from[i] to page copy_to[i] in every pool."""
+    _check("svd_paged_copy", load().svd_paged_copy(
+        pools._p, len(pools), pools.page_bytes, n_pages, _ptr(copy_from), _ptr(copy_to), _ptr(n_copies), max_copies,
+        _stream(stream)))
