@@ -7,24 +7,29 @@
 //   scale = 2^e, e the smallest with 448 2^e >= |y| over the new values of a unit (16 positions of one kv head; K and
 //   V apart), and no smaller than the scale that earlier positions of the unit have;  code = e4m3(y / 2^e)
 //
-// Units.  A scale belongs to 16 positions, so a unit is written by one CTA: the tokens of a request that lie in
-// one unit are a run, and the CTA of the run's first token handles all of it.  Warp w has positions 4w .. 4w + 3 of the
-// unit, a lane four dimensions of each: four codes of a dimension then fill a word of V's row.  Where earlier
-// positions keep a smaller scale, their codes are rounded again in place.
+// Units.  A scale belongs to 16 positions, so a unit is written by one CTA: the tokens of a request that lie in one unit
+// are a run, and the CTA of the run's first token handles all of it: two kv heads, two warps for the keys of one and
+// two for its values, eight positions to a warp.  A lane keeps four dimensions of them in shared memory, where the
+// copies bring them while the angles are worked out (in registers, eight positions took 128 of them; cut down to 64, that
+// spilled).  The largest magnitude takes one exchange.  Where earlier positions keep a smaller scale, their codes
+// are rounded again in place.
 //
 // Codes.  A key next to the border of two codes must get the code that exact arithmetic gives, or the cache
-// would depend on how the angle was rounded.  Keys are carried as sums of two floats with an error bound, as in the
-// 4-bit append: a code is settled where y +- bound round alike, else by the distance from the border
-// between the two codes, and where that is within the bound the token's keys are worked out again in fp64.  The scale in
-// the same way.  Values and dimensions that do not turn are exact as they come.
+// would depend on how the angle was rounded.  Rotated keys are worked out in plain fp32, with an error below
+// 2.5 * 2^-24 (|x_a| + |x_b|); a code is settled where the key plus and minus that bound (the largest of a lane) round alike.  Else (in
+// about one of a hundred heads of a token) the warp works the key out as a sum of two floats good to 2^-27 (|x_a| + |x_b|), as the 4-bit append
+// does for all, and decides by the distance from the border between the two codes; where that is within the
+// bound still, in fp64.  The scale likewise.  Values and dimensions that do not turn are exact as they come.
 #include "paged8.cuh"
 #include "paged_rope.cuh"
 
 namespace svd {
 
-constexpr int kA8Warps = 4;
+constexpr int kA8Warps = 8;
 constexpr int kA8Threads = 32 * kA8Warps;
-constexpr int kA8VRow = 5;  // words of a V row in shared memory (four and one apart)
+constexpr int kA8Pos = 8;                  // positions of a warp
+constexpr int kA8Low = 16 * SVD_ROPE_MAX_PAIRS;
+constexpr float kA8Err = 2.5f * 0x1p-24f;  // of a rotated key, against |x_a| + |x_b|
 
 struct A8Args {
     const void *qkv;
@@ -35,372 +40,487 @@ struct A8Args {
     int32_t *status;
     int64_t n_pages;
     int T, R, width, Hq, Hkv, page;
-    int block, q_heads, kv_heads, q_parts;  // tokens of a CTA; heads of one; CTAs of the query heads
+    int block, kv_parts;  // tokens of a CTA; CTAs of the kv heads (which come first)
+    int row_bits;         // the power of two that holds all pairs
     RopeArgs rope;
 };
 
-// What a lane's four dimensions turn by, and the largest error of cos and sin (0 where they are exact).
-struct A8Turn {
-    float c[4], s[4], cl[4], sl[4], err[4];
-};
+// A lane's four dimensions: whether they turn, and where the other ones of their pairs are.
 struct A8Lane {
-    bool on, up;
-    int mate, d0;
+    bool on, up, inter;
+    int mate, first;  // lane (-1: interleaved); first pair
 };
 __device__ __forceinline__ A8Lane a8_lane(const RopeArgs &R, int lane) {
     A8Lane l;
-    l.d0 = 4 * lane;
-    l.on = l.d0 < 2 * R.pairs;  // pairs is a multiple of four: a lane's dimensions turn alike
-    l.up = !R.interleaved && l.d0 >= R.pairs;
-    l.mate = R.interleaved ? -1 : l.on ? (l.up ? lane - (R.pairs >> 2) : lane + (R.pairs >> 2)) : lane;
+    l.inter = R.interleaved;
+    l.on = 4 * lane < 2 * R.pairs;  // pairs is a multiple of four: a lane's dimensions turn alike
+    l.up = !l.inter && 4 * lane >= R.pairs;
+    l.mate = l.inter ? -1 : l.on ? (l.up ? lane - (R.pairs >> 2) : lane + (R.pairs >> 2)) : lane;
+    l.first = !l.on ? 0 : l.inter ? 2 * lane : 4 * lane - (l.up ? R.pairs : 0);
     return l;
 }
-__device__ __forceinline__ A8Turn a8_turn(const RopeArgs &R, const A8Lane &l, int lane, const float4 *cs_row) {
-    A8Turn t;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int i = R.interleaved ? 2 * lane + (j >> 1) : l.d0 + j - (l.up ? R.pairs : 0);
-        const float4 cs = l.on ? cs_row[i] : make_float4(1.f, 0.f, 0.f, 0.f);
-        const bool plus = R.interleaved ? (j & 1) : l.up;
-        t.c[j] = cs.x;
-        t.cl[j] = cs.y;
-        t.s[j] = plus ? cs.z : -cs.z;
-        t.sl[j] = plus ? cs.w : -cs.w;
-        // (a quarter turn or none: the products are exact)
-        t.err[j] = (cs.x == 0.f || cs.z == 0.f) && cs.y == 0.f && cs.w == 0.f ? 0.f : 0x1p-27f;
-    }
-    return t;
-}
 __device__ __forceinline__ void a8_mates(const A8Lane &l, const float x[4], float xb[4]) {
-    if (l.mate < 0) {
+    if (l.inter) {
         xb[0] = x[1]; xb[1] = x[0]; xb[2] = x[3]; xb[3] = x[2];
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) xb[j] = __shfl_sync(~0u, x[j], l.mate);
     }
 }
-
-// The request of token t: the last one whose first token is not behind it (a count over all of them).
-__device__ __forceinline__ int a8_request(const A8Args &A, int t, int *s_count) {
-    int n = 0;
-    for (int r = threadIdx.x; r < A.R; r += kA8Threads) n += A.q_start[r] <= t;
-    n = __reduce_add_sync(~0u, n);
-    if ((threadIdx.x & 31) == 0) s_count[threadIdx.x >> 5] = n;
-    __syncthreads();
-    n = s_count[0] + s_count[1] + s_count[2] + s_count[3];
-    __syncthreads();
-    return max(n - 1, 0);
+// cos and (signed) sin of the lane's dimensions, y = x c + xb s, from a token's row of them.
+__device__ __forceinline__ void a8_turn(const A8Lane &l, const float2 *row, float c[4], float s[4]) {
+    if (l.inter) {
+        const float4 a = *reinterpret_cast<const float4 *>(row + l.first);
+        c[0] = c[1] = a.x; c[2] = c[3] = a.z;
+        s[0] = -a.y; s[1] = a.y; s[2] = -a.w; s[3] = a.w;
+    } else {
+        const float4 a = *reinterpret_cast<const float4 *>(row + l.first), b = *reinterpret_cast<const float4 *>(row + l.first + 2);
+        c[0] = a.x; c[1] = a.z; c[2] = b.x; c[3] = b.z;
+        s[0] = a.y; s[1] = a.w; s[2] = b.y; s[3] = b.w;
+        if (!l.up) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = -s[j];
+        }
+    }
+}
+// What every angle of a CTA needs, where lanes may read different entries at once (as kernel arguments and constants, an
+// entry a time, they cost as much as the angles).
+struct A8Tables {
+    float4 turn[33];
+    uint64_t phase[SVD_ROPE_MAX_PAIRS];
+    uint8_t axis[SVD_ROPE_MAX_PAIRS];
+};
+__device__ __forceinline__ void a8_tables(const A8Args &A, A8Tables *s) {
+    const int i = threadIdx.x;
+    if (i < SVD_ROPE_MAX_PAIRS) {
+        s->phase[i] = A.rope.phase[i];
+        s->axis[i] = A.rope.axis[i];
+    } else if (i < SVD_ROPE_MAX_PAIRS + 33) {
+        s->turn[i - SVD_ROPE_MAX_PAIRS] = kApTurn[i - SVD_ROPE_MAX_PAIRS];
+    }
+}
+__device__ __forceinline__ void a8_angles(const A8Args &A, int t, int n, float2 *s_cs, const A8Tables &S) {  // (low parts behind all high ones)
+    for (int j = threadIdx.x; j < n << A.row_bits; j += kA8Threads) {
+        const int k = j >> A.row_bits, i = j & ((1 << A.row_bits) - 1);
+        if (i < A.rope.pairs) {
+            uint32_t quad;
+            const int64_t r = ap_reduce(A.rope.positions[S.axis[i] * A.rope.positions_ld + t + k], S.phase[i], &quad);
+            const float4 cs = ap_cos_sin(r, quad, S.turn);
+            s_cs[k * SVD_ROPE_MAX_PAIRS + i] = make_float2(cs.x, cs.z);
+            s_cs[kA8Low + k * SVD_ROPE_MAX_PAIRS + i] = make_float2(cs.y, cs.w);
+        }
+    }
 }
 
-// A token's keys in fp64, where one is in doubt.
-__device__ __noinline__ uint32_t a8_codes_f64(const A8Args &A, int t, float4 x, float4 xb, int lane, int e) {
-    double y[4];
-    ap_turn_f64(A.rope, t, x, xb, lane, y);
-    uint32_t codes = 0;
+// A token's key once more, where plain fp32 leaves something open: as the sum y + low, good to err; what is no number
+// counts as 0 and magnitudes end at the largest, as the plain formula gives them.
+struct A8Key {
+    float y[4], low[4], err[4];
+};
+__device__ __forceinline__ A8Key a8_key(const A8Args &A, const float x[4], const float xb[4], const float2 *cs_row, int lane) {
+    const A8Lane l = a8_lane(A.rope, lane);
+    A8Key k;
+    float c[4], s[4], cl[4], sl[4];
+    if (l.on) {
+        a8_turn(l, cs_row, c, s);
+        a8_turn(l, cs_row + kA8Low, cl, sl);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const double z = fmin(fabs(y[j]) * __longlong_as_double((long long)(1023 - e) << 52), 448.0);
+        k.y[j] = x[j];
+        k.low[j] = k.err[j] = 0.f;
+        if (l.on) {
+            // what the products and the sum drop, and cos' and sin's low parts
+            const float p = __fmul_rn(x[j], c[j]), q = __fmul_rn(xb[j], s[j]), r = __fadd_rn(p, q);
+            const float b = __fsub_rn(r, p), lost = __fadd_rn(__fsub_rn(p, __fsub_rn(r, b)), __fsub_rn(q, b));
+            const float rest = fmaf(x[j], c[j], -p) + fmaf(xb[j], s[j], -q) + lost + fmaf(x[j], cl[j], xb[j] * sl[j]);
+            const float w = __fadd_rn(r, rest);
+            k.y[j] = w;
+            if (fabsf(w) <= kP8MaxAbs) {
+                k.low[j] = __fsub_rn(rest, __fsub_rn(w, r));
+                k.err[j] = c[j] == 0.f || s[j] == 0.f ? 0.f : (fabsf(x[j]) + fabsf(xb[j])) * 0x1p-27f;  // (0: exact)
+            } else {
+                k.y[j] = r;
+            }
+        }
+        k.y[j] = k.y[j] == k.y[j] ? fminf(fmaxf(k.y[j], -kP8MaxAbs), kP8MaxAbs) : 0.f;
+    }
+    return k;
+}
+__device__ __forceinline__ float a8_pick(const float x[4], int j) { return j < 2 ? (j ? x[1] : x[0]) : j == 2 ? x[2] : x[3]; }
+__device__ __forceinline__ int a8_order(uint32_t c) { return c & 0x80u ? -(int)(c & 0x7Fu) : (int)c; }
+
+// The codes of a token's key under the scale 2^e, as exact arithmetic gives them.
+template <typename T>
+__device__ __forceinline__ uint32_t a8_codes(const A8Args &A, int t, const T *key, int lane, int e, const float2 *cs_row) {
+    float x[4], xb[4];
+    ap_floats(ap_raw(key + 4 * lane), x);
+    a8_mates(a8_lane(A.rope, lane), x, xb);
+    const A8Key k = a8_key(A, x, xb, cs_row, lane);
+    const float inv = p8_pow2(-e);
+    uint32_t out = 0, ask = 0;  // ask: bytes still in doubt
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float z = k.y[j] * inv, err = k.err[j] * inv, d = err > 0.f ? fmaf(0x1p-23f, fabsf(z), err) : 0.f;
+        const uint32_t two = p8_encode2(z - d, z + d), c0 = two & 0xFFu;
+        uint32_t c = two >> 8;
+        if (c != c0) {
+            const float border = 0.5f * (p8_floats2(c).x + p8_floats2(c0).x);  // exact
+            const float small = k.low[j] * inv, gap = fmaf(k.y[j], inv, -border) + small;
+            if (!(fabsf(gap) > fmaf(0x1p-22f, fabsf(small), err)) || a8_order(c) - a8_order(c0) > 1) ask |= 0xFFu << (8 * j);
+            if (!(gap > 0.f)) c = c0;
+        }
+        out |= c << (8 * j);
+    }
+    if (!__any_sync(~0u, ask != 0u)) return out;
+    uint32_t exact = 0;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {  // (one at a time: side by side they would take registers from what is not rare)
+        const double y = ap_turn_f64(A.rope, t, a8_pick(x, j), a8_pick(xb, j), lane, j);
+        const double z = fmin(fabs(y) * __longlong_as_double((long long)(1023 - e) << 52), 448.0);
         const int ex = max((int)((unsigned long long)__double_as_longlong(z) >> 52) - 1023, -6);
         const int n = __double2int_rn(z * __longlong_as_double((long long)(1023 + 3 - ex) << 52));
-        const uint32_t c = (uint32_t)min(n + 8 * (ex + 6), 0x7E) | (y[j] < 0.0 ? 0x80u : 0u);
-        codes |= c << (8 * j);
+        exact |= ((uint32_t)min(n + 8 * (ex + 6), 0x7E) | (y < 0.0 ? 0x80u : 0u)) << (8 * j);
     }
-    return codes;
+    return (out & ~ask) | (exact & ask);
 }
-__device__ __noinline__ double a8_top_f64(const A8Args &A, int t, float4 x, float4 xb, int lane) {
-    double y[4];
-    ap_turn_f64(A.rope, t, x, xb, lane, y);
-    const double top = fmax(fmax(fabs(y[0]), fabs(y[1])), fmax(fabs(y[2]), fabs(y[3])));
-    return top > (double)kP8MaxAbs ? (double)kP8MaxAbs : top;  // (NaN stays one, and counts for nothing)
-}
-
-// Codes of earlier positions under a scale 2^down times as large.
+// Codes of earlier positions under a scale 1 / down times as large.
 __device__ __forceinline__ uint32_t a8_again(uint32_t codes, float down) {
     const float2 a = p8_floats2(codes & 0xFFFFu), b = p8_floats2(codes >> 16);
     return p8_encode2(a.x * down, a.y * down) | (p8_encode2(b.x * down, b.y * down) << 16);
 }
+__device__ __forceinline__ int a8_clamp(int e) { return min(max(e, kP8ExpLo), kP8ExpHi); }
+// The largest magnitude of a warp's values (0 where there is none; NaN counts for nothing).
+__device__ __forceinline__ float a8_most(float top) { return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top))); }
 
+// What the two warps of a unit's keys, or of its values, tell each other: a value each, the larger one wins.
+__device__ __forceinline__ uint32_t a8_both(uint32_t mine, uint32_t *s_both, int warp, int lane) {
+    if (lane == 0) s_both[warp] = mine;
+    asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+    const uint32_t theirs = s_both[warp ^ 1];
+    asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+    return max(mine, theirs);
+}
+
+// A run's part in a warp: positions a .. b - 1 of the warp's eight, the first of them token t.
+struct A8Part {
+    int t, a, b;
+};
+// Sixteen or eight bytes into the front of a slot of shared memory.
+__device__ __forceinline__ void a8_fetch(float4 *to, const float *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void a8_fetch(float4 *to, const __nv_bfloat16 *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void a8_fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// The lane's four values of a slot as they were copied.
 template <typename T>
-__global__ void __launch_bounds__(kA8Threads) paged8_append_kernel(const __grid_constant__ A8Args A) {
-    __shared__ float4 s_cs[16 * SVD_ROPE_MAX_PAIRS];
-    __shared__ uint32_t s_v[kPgDim * kA8VRow];
-    __shared__ uint32_t s_top[3][kA8Warps];
-    __shared__ double s_top64[kA8Warps];
-    __shared__ int s_count[kA8Warps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int pairs = A.rope.pairs;
-    const T *const qkv = reinterpret_cast<const T *>(A.qkv);
-    griddep_wait();
-    const int t0 = blockIdx.x * A.block, t1 = min(min(t0 + A.block, A.T), A.q_start[A.R]);
-    if (t0 >= t1) return;
-    const A8Lane l = a8_lane(A.rope, lane);
+__device__ __forceinline__ void a8_slot(const float4 *slot, float x[4]) {
+    ap_floats(ap_raw(reinterpret_cast<const T *>(slot)), x);
+}
+template <typename T>
+__device__ __forceinline__ void a8_put(float4 *slot, const float x[4]) {  // (values that T holds)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<T *>(slot)[j] = (T)x[j];
+}
+__device__ __forceinline__ bool a8_odd(const float x[4]) {  // one is not finite
+    return !(fabsf(x[0]) <= 3.4028235e38f) || !(fabsf(x[1]) <= 3.4028235e38f) || !(fabsf(x[2]) <= 3.4028235e38f) ||
+           !(fabsf(x[3]) <= 3.4028235e38f);
+}
 
-    if ((int)blockIdx.y < A.q_parts) {
-        // ---- queries: a warp takes a head of a token ----------------------------------------------
-        const int h0 = blockIdx.y * A.q_heads, nh = min(A.q_heads, A.Hq - h0), items = (t1 - t0) * nh;
-        auto raw = [&](int it) {
-            const int t = it / nh;
-            return ap_raw(qkv + (t0 + t) * A.ld + (int64_t)(h0 + it - t * nh) * kPgDim + l.d0);
-        };
-        decltype(ap_raw(qkv)) ahead[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (warp + k * kA8Warps < items) ahead[k] = raw(warp + k * kA8Warps);
-        for (int i = tid; i < (t1 - t0) * pairs; i += kA8Threads) {
-            const int t = i / pairs;
-            s_cs[t * SVD_ROPE_MAX_PAIRS + i - t * pairs] = ap_cos_sin(A.rope, t0 + t, i - t * pairs);
+// The exponent (less the lowest) that a warp's part of a run asks for, from its keys in fp64; what is not finite is
+// reported.
+template <typename T>
+__device__ __forceinline__ int a8_need_f64(const A8Args &A, const T *row, int t, int n, int lane) {
+    double top = 0.0;
+    for (; n > 0; --n, ++t) {
+        float x[4], xb[4];
+        ap_floats(ap_raw(row + (int64_t)t * A.ld + 4 * lane), x);
+        a8_mates(a8_lane(A.rope, lane), x, xb);
+        if (__any_sync(~0u, a8_odd(x)) && A.status && lane == 0) atomicOr(A.status + t, SVD_ST_NONFINITE);
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            const double y = ap_turn_f64(A.rope, t, a8_pick(x, j), a8_pick(xb, j), lane, j);
+            top = fmax(top, y == y ? fmin(fabs(y), (double)kP8MaxAbs) : 0.0);
         }
-        __syncthreads();
-        for (int it = warp; it < items; it += kA8Warps) {
-            float x[4], xb[4], y[4];
-            ap_floats(ahead[0], x);
+    }
 #pragma unroll
-            for (int k = 0; k < 3; ++k) ahead[k] = ahead[k + 1];
-            if (it + 4 * kA8Warps < items) ahead[3] = raw(it + 4 * kA8Warps);
-            const int t = it / nh;
+    for (int o = 16; o; o >>= 1) top = fmax(top, __shfl_xor_sync(~0u, top, o));
+    int e = kP8ExpLo;
+    while (e < kP8ExpHi && 448.0 * (double)p8_pow2(e) < top) ++e;
+    return e - kP8ExpLo;
+}
+
+// The keys of a run.  row: the head's key of token 0; i0: the run's first position in the unit; half: the warp's
+// eight positions; s_cs: cos and sin of the run's tokens, the first of which is token t0; slot: the lane's, 32 apart.
+template <typename T>
+__device__ __forceinline__ void a8_keys(const A8Args &A, const T *row, const A8Part P, int i0, int half, int t0, uint8_t *unit,
+                                        const float2 *s_cs, uint32_t *s_both, float4 *slot, int warp,
+                                        int lane) {
+    const A8Lane l = a8_lane(A.rope, lane);
+    const int e0 = i0 > 0 ? p8_exponent(*reinterpret_cast<const float *>(unit + kP8Scales)) : kP8ExpLo;
+    float top = 0.f, none = 0.f, turned = 0.f;  // none: NaN where a value is not finite; turned: not 0 where an angle is no quarter turn
+#pragma unroll 2
+    for (int p = P.a; p < P.b; ++p) {
+        float x[4];
+        a8_slot<T>(slot + 32 * p, x);
+        if (A.rope.pairs) {
+            float xb[4];
             a8_mates(l, x, xb);
+            if (l.on) {
+                float c[4], s[4];
+                a8_turn(l, s_cs + (P.t - t0 + p - P.a) * SVD_ROPE_MAX_PAIRS, c, s);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    turned = fmaxf(turned, fminf(fabsf(c[j]), fabsf(s[j])));
+                    x[j] = fmaf(x[j], c[j], xb[j] * s[j]);
+                }
+            }
+            slot[32 * p] = make_float4(x[0], x[1], x[2], x[3]);
+        } else if (sizeof(T) == 2) {
+            slot[32 * p] = make_float4(x[0], x[1], x[2], x[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            top = fmaxf(top, fabsf(x[j]));
+            none = fmaf(x[j], 0.f, none);
+        }
+    }
+    // What the lane's keys may be off: a turn keeps the length of a pair, so |x_a| + |x_b| is at most twice the larger of
+    // its two keys.
+    const float pair = l.inter ? top : fmaxf(top, __shfl_sync(~0u, top, l.mate));
+    const bool none_open = turned == 0.f;
+    const float off = none_open ? 0.f : fmaf(2.f * kA8Err, pair, 0x1p-23f * top);
+    // The largest key: of the exact ones, and of the others with what they may be off (bits of floats that are not negative
+    // are ordered as they are).  All ones: something is not finite, or too large, and all of the run's keys are open.
+    const float big = a8_most(top), sure = a8_most(none_open ? top : 0.f), near = a8_most(none_open ? 0.f : top), far = a8_most(off);
+    const bool wild = __any_sync(~0u, none != 0.f) || big > kP8MaxAbs;
+    const uint32_t hi = a8_both(wild ? ~0u : __float_as_uint(fmaxf(sure, near > 0.f ? near + far : 0.f)), s_both, warp, lane);
+    const uint32_t lo = a8_both(wild ? 0u : __float_as_uint(fmaxf(sure, near - far)), s_both, warp, lane);
+    int e = a8_clamp(p8_need(__uint_as_float(hi)));
+    uint32_t again = 0;  // positions whose codes are open
+    if (hi == ~0u || a8_clamp(p8_need(__uint_as_float(lo))) != e) {
+        e = (int)a8_both((uint32_t)a8_need_f64(A, row, P.t, P.b - P.a, lane), s_both, warp, lane) + kP8ExpLo;
+        e = max(e, e0);
+        again = (1u << P.b) - (1u << P.a);
+    } else {
+        e = max(e, e0);
+        const float inv = p8_pow2(-e), d = off * inv;
+#pragma unroll 2
+        for (int p = P.a; p < P.b; ++p) {
+            const float4 y = slot[32 * p];
+            const float y4[4] = {y.x, y.y, y.z, y.w};
+            float a[4], b[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int i = A.rope.interleaved ? 2 * lane + (j >> 1) : l.d0 + j - (l.up ? pairs : 0);
-                const float2 cs = l.on ? *reinterpret_cast<const float2 *>(&s_cs[t * SVD_ROPE_MAX_PAIRS + i].x) : make_float2(1.f, 0.f);
-                const float sn = l.on ? s_cs[t * SVD_ROPE_MAX_PAIRS + i].z : 0.f;
-                const bool plus = A.rope.interleaved ? (j & 1) : l.up;
-                const float r = __fadd_rn(__fmul_rn(x[j], cs.x), __fmul_rn(xb[j], plus ? sn : -sn));
-                y[j] = l.on ? r : x[j];
+                a[j] = fmaf(y4[j], inv, d);
+                b[j] = fmaf(y4[j], inv, -d);
             }
-            const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
-            uint2 o;
-            o.x = reinterpret_cast<const uint32_t &>(a);
-            o.y = reinterpret_cast<const uint32_t &>(b);
-            *reinterpret_cast<uint2 *>(A.q + ((int64_t)(t0 + t) * A.Hq + h0 + it - t * nh) * kPgDim + l.d0) = o;
+            const uint32_t codes = p8_encode2(a[0], a[1]) | (p8_encode2(a[2], a[3]) << 16);
+            const uint32_t other = p8_encode2(b[0], b[1]) | (p8_encode2(b[2], b[3]) << 16);
+            if (__any_sync(~0u, codes != other)) again |= 1u << p;
+            const int i = kA8Pos * half + p;
+            *reinterpret_cast<uint32_t *>(unit + i * kPgDim + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4) = codes;
+        }
+    }
+    for (; again; again &= again - 1u) {
+        const int p = __ffs(again) - 1, t = P.t + p - P.a, i = kA8Pos * half + p;
+        const uint32_t codes = a8_codes(A, t, row + (int64_t)t * A.ld, lane, e, s_cs + (t - t0) * SVD_ROPE_MAX_PAIRS);
+        *reinterpret_cast<uint32_t *>(unit + i * kPgDim + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4) = codes;
+    }
+    if (e > e0 && i0 > 0) {
+        uint32_t *const words = reinterpret_cast<uint32_t *>(unit) + 32 * half + lane;  // of earlier positions, 64 apart
+        const float down = p8_pow2(e0 - e);
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (half + 2 * k < i0) w[k] = words[64 * k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (half + 2 * k < i0) words[64 * k] = a8_again(w[k], down);
+    }
+    if (half == 0 && lane == 0) *reinterpret_cast<float *>(unit + kP8Scales) = p8_pow2(e);
+}
+
+// The values of a run; n: its length.
+template <typename T>
+__device__ __forceinline__ void a8_values(const A8Args &A, const A8Part P, int i0, int n, int half, uint8_t *unit, uint32_t *s_both,
+                                          float4 *slot, int warp, int lane) {
+    uint2 *const rows = reinterpret_cast<uint2 *>(unit + kP8VCodes) + 8 * lane + half;  // of the lane's dimensions, 16 bytes apart
+    uint2 old[4];
+    if (n < 16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) old[j] = rows[2 * j];
+    }
+    const int e0 = i0 > 0 ? p8_exponent(*reinterpret_cast<const float *>(unit + kP8Scales + 4)) : kP8ExpLo;
+    float top = 0.f, none = 0.f;
+#pragma unroll 2
+    for (int p = P.a; p < P.b; ++p) {
+        float x[4];
+        a8_slot<T>(slot + 32 * p, x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            top = fmaxf(top, fabsf(x[j]));
+            none = fmaf(x[j], 0.f, none);
+        }
+    }
+    if (__any_sync(~0u, none != 0.f || top > kP8MaxAbs)) {  // what is no number counts as 0, and magnitudes end
+        top = 0.f;
+        for (int p = P.a; p < P.b; ++p) {
+            float x[4];
+            a8_slot<T>(slot + 32 * p, x);
+            if (__any_sync(~0u, a8_odd(x)) && A.status && lane == 0) atomicOr(A.status + P.t + p - P.a, SVD_ST_NONFINITE);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] = x[j] == x[j] ? fminf(fmaxf(x[j], -kP8MaxAbs), kP8MaxAbs) : 0.f;
+                top = fmaxf(top, fabsf(x[j]));
+            }
+            a8_put<T>(slot + 32 * p, x);
+        }
+    }
+    const float big = __uint_as_float(a8_both(__float_as_uint(a8_most(top)), s_both, warp, lane));
+    const int e = max(a8_clamp(p8_need(big)), e0);
+    const float inv = p8_pow2(-e), down = p8_pow2(e0 - e);
+    const bool grown = i0 > 0 && e > e0;
+    uint32_t w[4][2];  // [dimension][four positions]
+#pragma unroll
+    for (int p = 0; p < kA8Pos; p += 2) {  // (slots of no position hold anything: their bytes are not used)
+        float a4[4], b4[4];
+        a8_slot<T>(slot + 32 * p, a4);
+        a8_slot<T>(slot + 32 * p + 32, b4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t two = p8_encode2(a4[j] * inv, b4[j] * inv);
+            if (p & 2) w[j][p >> 2] |= two << 16;
+            else w[j][p >> 2] = two;
+        }
+    }
+    // New bytes i0 .. i0 + n - 1, earlier ones under the scale as it is now, later ones as they were.
+    if (n < 16) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int first = kA8Pos * half + 4 * g;
+            const int a = min(max(i0 - first, 0), 4), b = min(max(i0 + n - first, 0), 4);  // new bytes of the word
+            const uint32_t ma = a < 4 ? ~0u << (8 * a) : 0u, mb = b < 4 ? ~0u << (8 * b) : 0u, fresh = ma & ~mb;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t keep = g ? old[j].y : old[j].x;
+                if (grown && a > 0) keep = (a8_again(keep, down) & ~ma) | (keep & ma);
+                w[j][g] = (w[j][g] & fresh) | (keep & ~fresh);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rows[2 * j] = make_uint2(w[j][0], w[j][1]);
+    if (half == 0 && lane == 0) *reinterpret_cast<float *>(unit + kP8Scales + 4) = p8_pow2(e);
+}
+
+constexpr size_t kA8Smem = kA8Warps * kA8Pos * 32 * sizeof(float4) + 2 * kA8Low * sizeof(float2);
+
+template <typename T>
+__global__ void __launch_bounds__(kA8Threads, 3) paged8_append_kernel(const __grid_constant__ A8Args A) {
+    extern __shared__ float4 s_x[];  // [warp][position][lane], then the angles
+    __shared__ __align__(16) A8Tables s_tab;
+    __shared__ uint32_t s_both[kA8Warps];
+    __shared__ int s_r;
+    float2 *const s_cs = reinterpret_cast<float2 *>(s_x + kA8Warps * kA8Pos * 32);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const T *const qkv = reinterpret_cast<const T *>(A.qkv) + 4 * lane;
+    const int t0 = blockIdx.x * A.block, t1 = min(t0 + A.block, A.T);
+    a8_tables(A, &s_tab);
+    if (tid == kA8Threads - 1) s_r = -1;
+    __syncthreads();
+    griddep_wait();
+
+    if ((int)blockIdx.y >= A.kv_parts) {
+        // ---- queries: a warp takes a head of the block's tokens -----------------------------------
+        const int head = ((int)blockIdx.y - A.kv_parts) * kA8Warps + warp, end = A.q_start[A.R];
+        const bool there = head < A.Hq;
+        const T *row = qkv + t0 * A.ld + (int64_t)head * kPgDim;
+        constexpr int kAhead = sizeof(T) == 2 ? 8 : 4;
+        decltype(ap_raw(qkv)) ahead[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (there && t0 + k < t1) ahead[k] = ap_raw(row + k * A.ld);
+        a8_angles(A, t0, t1 - t0, s_cs, s_tab);
+        __syncthreads();
+        if (!there) return;
+        const A8Lane l = a8_lane(A.rope, lane);
+        __nv_bfloat16 *q = A.q + ((int64_t)t0 * A.Hq + head) * kPgDim + 4 * lane;
+        const int n = min(t1, end) - t0;
+        for (int g = 0; g < n; g += kAhead) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int t = g + k;
+                if (t >= n) break;
+                float x[4], xb[4];
+                ap_floats(ahead[k], x);
+                if (t0 + t + kAhead < t1) ahead[k] = ap_raw(row + (int64_t)(t + kAhead) * A.ld);
+                if (A.rope.pairs) {
+                    a8_mates(l, x, xb);
+                    if (l.on) {
+                        float c[4], s[4];
+                        a8_turn(l, s_cs + t * SVD_ROPE_MAX_PAIRS, c, s);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], c[j], xb[j] * s[j]);
+                    }
+                }
+                const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+                uint2 o;
+                o.x = reinterpret_cast<const uint32_t &>(a);
+                o.y = reinterpret_cast<const uint32_t &>(b);
+                *reinterpret_cast<uint2 *>(q) = o;
+                q += A.Hq * kPgDim;
+            }
         }
         return;
     }
 
-    // ---- keys and values: the runs that begin in this block of tokens --------------------------------
-    const int h0 = ((int)blockIdx.y - A.q_parts) * A.kv_heads, h1 = min(h0 + A.kv_heads, A.Hkv);
-    int r = a8_request(A, t0, s_count);
+    // ---- keys and values: the runs that begin in this block of tokens, two kv heads ------------------
+    const int h = 2 * (int)blockIdx.y + (warp >> 2), is_v = (warp >> 1) & 1, half = warp & 1;
+    for (int r = tid; r < A.R; r += kA8Threads) {
+        if (A.q_start[r] <= t0 && t0 < A.q_start[r + 1]) atomicMax(&s_r, r);
+    }
+    __syncthreads();
+    int r = s_r;
+    if (r < 0) return;  // behind the last request
     for (int t = t0; t < t1;) {
         while (r + 1 < A.R && A.q_start[r + 1] <= t) ++r;
-        if (A.q_start[r] > t) {  // (a token before the first request's)
-            t = A.q_start[r];
-            continue;
-        }
-        const int q0 = max(A.q_start[r], 0), q1 = min(A.q_start[r + 1], A.T);
-        const int64_t at = (int64_t)A.kv_len[r] - (A.q_start[r + 1] - (int64_t)A.q_start[r]) + (t - q0);  // position of token t
+        const int q0 = A.q_start[r], q2 = A.q_start[r + 1], q1 = min(q2, A.T);
+        const int64_t at = (int64_t)A.kv_len[r] - ((int64_t)q2 - q0) + ((int64_t)t - q0);  // position of token t
         const int i0 = (int)(at & 15), end = min(t + 16 - i0, q1);
-        if (end <= t) return;  // (a q_start that does not ascend)
+        if (end <= t || t < q0) return;  // (behind the last request, or a q_start that does not ascend)
         if (t != q0 && i0 != 0) {  // the run began in another block
             t = end;
             continue;
         }
         const int n = end - t;  // positions i0 .. i0 + n - 1 of the unit
+        const T *const row = qkv + (int64_t)(A.Hq + h + is_v * A.Hkv) * kPgDim;
+        A8Part P;
+        P.a = min(max(i0 - kA8Pos * half, 0), kA8Pos);
+        P.b = min(max(i0 + n - kA8Pos * half, 0), kA8Pos);
+        P.t = t + (half ? max(kA8Pos - i0, 0) : 0);
+        float4 *const slot = s_x + warp * (kA8Pos * 32) + lane;
+        if (h < A.Hkv)
+            for (int p = P.a; p < P.b; ++p) a8_fetch(slot + 32 * p, row + (int64_t)(P.t + p - P.a) * A.ld);
         int64_t pg = -1;
         if (at >= 0 && at < (int64_t)A.width * A.page) pg = A.table[(int64_t)r * A.width + (uint32_t)at / (uint32_t)A.page];
         if (pg < 0 || pg >= A.n_pages) {
-            if (A.status && h0 == 0 && tid < n) atomicOr(A.status + t + tid, SVD_ST_BAD_SLOT);
+            if (A.status && h == 0 && warp == 0 && lane < n) atomicOr(A.status + t + lane, SVD_ST_BAD_SLOT);
+            a8_fetched();
             t = end;
             continue;
         }
-        const int upp = A.page >> 4, place = (int)((uint32_t)at % (uint32_t)A.page) >> 4;
-        for (int h = h0; h < h1; ++h) {
-            uint8_t *const unit = A.pages + ((pg * A.Hkv + h) * upp + place) * (int64_t)kP8UnitBytes;
-            // Warp w's positions 4w + k: those of the run are tokens tw + k.
-            const int tw = t + 4 * warp - i0;
-            decltype(ap_raw(qkv)) kr[4], vr[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (tw + k >= t && tw + k < end) {
-                    const T *const row = qkv + (tw + k) * A.ld + (int64_t)(A.Hq + h) * kPgDim + l.d0;
-                    kr[k] = ap_raw(row);
-                    vr[k] = ap_raw(row + (int64_t)A.Hkv * kPgDim);
-                }
-            // V's row of dimension tid and the scales, where they hold other positions
-            uint4 old = {0u, 0u, 0u, 0u};
-            int ek0 = kP8ExpLo, ev0 = kP8ExpLo;
-            if (n < 16) old = *reinterpret_cast<const uint4 *>(unit + kP8VCodes + 16 * tid);
-            if (i0 > 0) {
-                const float2 sc = *reinterpret_cast<const float2 *>(unit + kP8Scales);
-                ek0 = p8_exponent(sc.x);
-                ev0 = p8_exponent(sc.y);
-            }
-            if (h == h0) {
-                __syncthreads();  // (the angles of the run before are read)
-                for (int i = tid; i < n * pairs; i += kA8Threads) {
-                    const int k = i / pairs;
-                    s_cs[k * SVD_ROPE_MAX_PAIRS + i - k * pairs] = ap_cos_sin(A.rope, t + k, i - k * pairs);
-                }
-                __syncthreads();
-            }
-            float y[4][4], low[4][4], err[4][4], v[4][4];
-            float top_k = 0.f, top_v = 0.f, top_err = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const bool here = tw + k >= t && tw + k < end;  // the same for the warp
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[k][j] = low[k][j] = err[k][j] = v[k][j] = 0.f;
-                if (!here) continue;
-                float x[4], xb[4];
-                ap_floats(kr[k], x);
-                ap_floats(vr[k], v[k]);
-                a8_mates(l, x, xb);
-                bool odd = false;
-                if (l.on) {
-                    const A8Turn tn = a8_turn(A.rope, l, lane, s_cs + (tw + k - t) * SVD_ROPE_MAX_PAIRS);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // with what the products and the sum dropped, and cos' and sin's low parts
-                        const float p = __fmul_rn(x[j], tn.c[j]), q = __fmul_rn(xb[j], tn.s[j]), s = __fadd_rn(p, q);
-                        const float b = __fsub_rn(s, p), lost = __fadd_rn(__fsub_rn(p, __fsub_rn(s, b)), __fsub_rn(q, b));
-                        const float rest = fmaf(x[j], tn.c[j], -p) + fmaf(xb[j], tn.s[j], -q) + lost +
-                                           fmaf(x[j], tn.cl[j], xb[j] * tn.sl[j]);
-                        const float w = __fadd_rn(s, rest);
-                        y[k][j] = w;
-                        low[k][j] = __fsub_rn(rest, __fsub_rn(w, s));
-                        err[k][j] = (fabsf(x[j]) + fabsf(xb[j])) * tn.err[j];
-                        if (!(fabsf(w) <= kP8MaxAbs)) {  // too large, or no number: as the formula gives it
-                            y[k][j] = s;
-                            low[k][j] = err[k][j] = 0.f;
-                        }
-                        odd |= !(fabsf(x[j]) <= 3.4028235e38f);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y[k][j] = x[j];
-                        odd |= !(fabsf(x[j]) <= 3.4028235e38f);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    odd |= !(fabsf(v[k][j]) <= 3.4028235e38f);
-                    // what is no number counts as 0, and magnitudes end at the largest
-                    y[k][j] = y[k][j] == y[k][j] ? fminf(fmaxf(y[k][j], -kP8MaxAbs), kP8MaxAbs) : 0.f;
-                    v[k][j] = v[k][j] == v[k][j] ? fminf(fmaxf(v[k][j], -kP8MaxAbs), kP8MaxAbs) : 0.f;
-                    top_k = fmaxf(top_k, fabsf(y[k][j]));
-                    top_v = fmaxf(top_v, fabsf(v[k][j]));
-                    top_err = fmaxf(top_err, err[k][j]);
-                }
-                if (__any_sync(~0u, odd) && A.status && lane == 0) atomicOr(A.status + tw + k, SVD_ST_NONFINITE);
-            }
-            // (floats that are not negative are ordered as their bits)
-            const uint32_t w_k = __reduce_max_sync(~0u, __float_as_uint(top_k)), w_v = __reduce_max_sync(~0u, __float_as_uint(top_v));
-            const uint32_t w_e = __reduce_max_sync(~0u, __float_as_uint(top_err));
-            if (lane == 0) {
-                s_top[0][warp] = w_k;
-                s_top[1][warp] = w_v;
-                s_top[2][warp] = w_e;
-            }
-            __syncthreads();
-            auto most = [&](int i) { return __uint_as_float(max(max(s_top[i][0], s_top[i][1]), max(s_top[i][2], s_top[i][3]))); };
-            const float big_k = most(0), big_v = most(1), big_e = most(2);
-            int ek = p8_need(big_k);
-            if (big_e > 0.f) {
-                // the largest key's exact magnitude lies between these
-                const float d = big_e + 0x1p-23f * big_k;
-                const int e_hi = p8_need(big_k + d);
-                if (p8_need(fmaxf(big_k - d, 0.f)) != e_hi) {
-                    double top = 0.0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (tw + k >= t && tw + k < end) {
-                            float x[4], xb[4];
-                            ap_floats(kr[k], x);
-                            a8_mates(l, x, xb);
-                            const double one = a8_top_f64(A, tw + k, make_float4(x[0], x[1], x[2], x[3]), make_float4(xb[0], xb[1], xb[2], xb[3]), lane);
-                            top = fmax(top, one);
-                        }
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) top = fmax(top, __shfl_xor_sync(~0u, top, o));
-                    if (lane == 0) s_top64[warp] = top;
-                    __syncthreads();
-                    top = fmax(fmax(s_top64[0], s_top64[1]), fmax(s_top64[2], s_top64[3]));
-                    const float low_e = p8_pow2(max(e_hi - 1, kP8ExpLo));
-                    ek = top > 448.0 * (double)low_e ? e_hi : e_hi - 1;
-                }
-            }
-            ek = max(min(max(ek, kP8ExpLo), kP8ExpHi), ek0);
-            const int ev = max(min(max(p8_need(big_v), kP8ExpLo), kP8ExpHi), ev0);
-            const float inv_k = p8_pow2(-ek), inv_v = p8_pow2(-ev);
-
-            uint32_t kc[4], vw[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                // what the key's exact value lies between rounds alike, or the border between the two codes decides
-                uint32_t hi2[2], lo2[2];
-#pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                    float a[2], b[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float z = y[k][j + i] * inv_k, e = err[k][j + i];
-                        const float d = e > 0.f ? fmaf(e, inv_k, 0x1p-23f * fabsf(z)) : 0.f;
-                        a[i] = z + d;
-                        b[i] = z - d;
-                    }
-                    hi2[j >> 1] = p8_encode2(a[0], a[1]);
-                    lo2[j >> 1] = p8_encode2(b[0], b[1]);
-                }
-                kc[k] = hi2[0] | (hi2[1] << 16);
-                const uint32_t kd = lo2[0] | (lo2[1] << 16);
-                if (__any_sync(~0u, kc[k] != kd) && tw + k >= t && tw + k < end) {
-                    uint32_t out = 0, ask = 0;  // ask: the bytes still in doubt
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t c = (kc[k] >> (8 * j)) & 0xFFu;
-                        const uint32_t c0 = (kd >> (8 * j)) & 0xFFu;
-                        if (c != c0) {
-                            const float border = 0.5f * (p8_floats2(c).x + p8_floats2(c0).x);  // exact
-                            const float small = low[k][j] * inv_k, gap = fmaf(y[k][j], inv_k, -border) + small;
-                            if (!(fabsf(gap) > fmaf(err[k][j], inv_k, 0x1p-22f * fabsf(small)))) ask |= 0xFFu << (8 * j);
-                            c = gap > 0.f ? c : c0;
-                        }
-                        out |= c << (8 * j);
-                    }
-                    kc[k] = out;
-                    if (__any_sync(~0u, ask != 0u)) {
-                        float x[4], xb[4];
-                        ap_floats(kr[k], x);
-                        a8_mates(l, x, xb);
-                        const uint32_t exact = a8_codes_f64(A, tw + k, make_float4(x[0], x[1], x[2], x[3]), make_float4(xb[0], xb[1], xb[2], xb[3]), lane, ek);
-                        kc[k] = (out & ~ask) | (exact & ask);
-                    }
-                }
-                if (tw + k >= t && tw + k < end) {
-                    const int p = 4 * warp + k;
-                    *reinterpret_cast<uint32_t *>(unit + p * kPgDim + (((lane >> 2) ^ (p & 7)) << 4) + (lane & 3) * 4) = kc[k];
-                }
-                const uint32_t va = p8_encode2(v[k][0] * inv_v, v[k][1] * inv_v), vb = p8_encode2(v[k][2] * inv_v, v[k][3] * inv_v);
-                const int sh = 8 * k;
-                vw[0] |= (va & 0xFFu) << sh;
-                vw[1] |= (va >> 8) << sh;
-                vw[2] |= (vb & 0xFFu) << sh;
-                vw[3] |= (vb >> 8) << sh;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s_v[(l.d0 + j) * kA8VRow + warp] = vw[j];
-            __syncthreads();
-            // V's row: new bytes i0 .. i0 + n - 1, earlier ones under the scale as it is now, later ones as they were
-            uint32_t row[4], was[4] = {old.x, old.y, old.z, old.w};
-            const float down_v = p8_pow2(ev0 - ev), down_k = p8_pow2(ek0 - ek);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int a = min(max(i0 - 4 * w, 0), 4), b = min(max(i0 + n - 4 * w, 0), 4);  // new bytes of the word
-                const uint32_t ma = a < 4 ? ~0u << (8 * a) : 0u, mb = b < 4 ? ~0u << (8 * b) : 0u, fresh = ma & ~mb;
-                uint32_t keep = was[w];
-                if (i0 > 0 && ev > ev0 && a > 0) {
-                    const uint32_t again = a8_again(keep, down_v);
-                    keep = (again & ~ma) | (keep & ma);
-                }
-                row[w] = (s_v[tid * kA8VRow + w] & fresh) | (keep & ~fresh);
-            }
-            *reinterpret_cast<uint4 *>(unit + kP8VCodes + 16 * tid) = make_uint4(row[0], row[1], row[2], row[3]);
-            if (i0 > 0 && ek > ek0)
-                for (int i = tid; i < i0 * (kPgDim / 4); i += kA8Threads) {
-                    uint32_t *const w = reinterpret_cast<uint32_t *>(unit) + i;
-                    *w = a8_again(*w, down_k);
-                }
-            if (tid == 0) *reinterpret_cast<float2 *>(unit + kP8Scales) = make_float2(p8_pow2(ek), p8_pow2(ev));
-            // (s_top is written again only behind the barrier above; s_v only behind that of the next head's s_top)
+        __syncthreads();  // (the angles of the run before are read)
+        a8_angles(A, t, n, s_cs, s_tab);
+        a8_fetched();
+        __syncthreads();
+        if (h < A.Hkv) {
+            const int place = (int)((uint32_t)at % (uint32_t)A.page) >> 4;
+            uint8_t *const unit = A.pages + ((pg * A.Hkv + h) * (A.page >> 4) + place) * (int64_t)kP8UnitBytes;
+            if (is_v) a8_values<T>(A, P, i0, n, half, unit, s_both, slot, warp, lane);
+            else a8_keys(A, row - 4 * lane, P, i0, half, t, unit, s_cs, s_both, slot, warp, lane);
         }
         t = end;
     }
@@ -439,18 +559,20 @@ int paged8_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv
     A.Hq = Hq;
     A.Hkv = Hkv;
     A.page = page;
-    // Few tokens: a CTA to each token and kv head, and to each four of its query heads.  Many: sixteen tokens share a
-    // CTA, and two kv heads or eight query heads their angles.
-    const bool many = (int64_t)T * Hkv > 24ll * sms;
-    A.block = many ? 16 : 1;
-    A.q_heads = many ? 8 : 4;
-    A.kv_heads = many && Hkv > 1 ? 2 : 1;
-    A.q_parts = (Hq + A.q_heads - 1) / A.q_heads;
-    const dim3 grid((unsigned)((T + A.block - 1) / A.block), (unsigned)(A.q_parts + (Hkv + A.kv_heads - 1) / A.kv_heads));
-    if (dtype == SVD_F32)
-        SVD_CUDA_TRY(launch(paged8_append_kernel<float>, grid, dim3(kA8Threads), 0, stream, true, A));
-    else
-        SVD_CUDA_TRY(launch(paged8_append_kernel<__nv_bfloat16>, grid, dim3(kA8Threads), 0, stream, true, A));
+    // As many tokens to a CTA, up to sixteen, as let nearly all CTAs be there at once.
+    A.kv_parts = (Hkv + 1) / 2;
+    while (1 << A.row_bits < A.rope.pairs) ++A.row_bits;
+    const int parts = A.kv_parts + (Hq + kA8Warps - 1) / kA8Warps;
+    A.block = 1;
+    while (A.block < 16 && (int64_t)T * parts > 4ll * sms * A.block) A.block *= 2;
+    const dim3 grid((unsigned)((T + A.block - 1) / A.block), (unsigned)parts);
+    if (dtype == SVD_F32) {
+        SVD_CUDA_TRY((allow_smem<paged8_append_kernel<float>>(kA8Smem)));
+        SVD_CUDA_TRY(launch(paged8_append_kernel<float>, grid, dim3(kA8Threads), kA8Smem, stream, true, A));
+    } else {
+        SVD_CUDA_TRY((allow_smem<paged8_append_kernel<__nv_bfloat16>>(kA8Smem)));
+        SVD_CUDA_TRY(launch(paged8_append_kernel<__nv_bfloat16>, grid, dim3(kA8Threads), kA8Smem, stream, true, A));
+    }
     return SVD_OK;
 }
 

@@ -28,11 +28,13 @@ __device__ __forceinline__ void ap_floats(const uint2 &v, float x[4]) {
 }
 
 // Pair i's angle at token t, less the nearest multiple of a quarter turn (*quad): 2^-64 turns.
-__device__ __forceinline__ int64_t ap_phase(const RopeArgs &A, int t, int i, uint32_t *quad) {
-    const int64_t pos = A.positions[A.axis[i] * A.positions_ld + t];
-    const uint64_t ph = (uint64_t)pos * A.phase[i], q = (ph + (1ull << 61)) >> 62;
+__device__ __forceinline__ int64_t ap_reduce(int64_t pos, uint64_t phase, uint32_t *quad) {
+    const uint64_t ph = (uint64_t)pos * phase, q = (ph + (1ull << 61)) >> 62;
     *quad = (uint32_t)q;
     return (int64_t)(ph - (q << 62));
+}
+__device__ __forceinline__ int64_t ap_phase(const RopeArgs &A, int t, int i, uint32_t *quad) {
+    return ap_reduce(A.positions[A.axis[i] * A.positions_ld + t], A.phase[i], quad);
 }
 
 // cos and sin of k / 256 turns (high and low parts), k = 0..32.
@@ -56,13 +58,12 @@ static __constant__ float4 kApTurn[33] = {
     {0.707106769f, 1.21016175e-08f, 0.707106769f, 1.21016175e-08f},
 };
 // cos and sin of the pair's angle as sums of two floats, to 2^-28: an entry of the table, turned by what
-// is left (at most a 512th of a turn), whose fp32 errors count for an 80th.
-__device__ __forceinline__ float4 ap_cos_sin(const RopeArgs &A, int t, int i) {
-    uint32_t quad;
-    const int64_t r = ap_phase(A, t, i, &quad);
+// is left (at most a 512th of a turn), whose fp32 errors count for an 80th.  turn: the table, here or copied to where
+// lanes may read different entries at once.
+__device__ __forceinline__ float4 ap_cos_sin(int64_t r, uint32_t quad, const float4 *turn) {
     const int k = (int)((r + (1ll << 55)) >> 56);
     const float a = __ll2float_rn(r - ((int64_t)k << 56)) * (6.283185307f * 0x1p-64f), z = a * a;
-    float4 e = kApTurn[k < 0 ? -k : k];
+    float4 e = turn[k < 0 ? -k : k];
     if (k < 0) { e.z = -e.z; e.w = -e.w; }
     const float sa = a * fmaf(z, -1.f / 6.f, 1.f), ca = z * fmaf(z, 1.f / 24.f, -0.5f);  // sin a, cos a - 1
     const float dc = fmaf(e.x, ca, -e.z * sa) + e.y, ds = fmaf(e.z, ca, e.x * sa) + e.w;
@@ -76,7 +77,14 @@ __device__ __forceinline__ float4 ap_cos_sin(const RopeArgs &A, int t, int i) {
     return o;
 }
 
-// Four rotated dimensions of a lane in fp64: x (xa) with the other dimensions of their pairs (xo).
+__device__ __forceinline__ float4 ap_cos_sin(const RopeArgs &A, int t, int i) {
+    uint32_t quad;
+    const int64_t r = ap_phase(A, t, i, &quad);
+    return ap_cos_sin(r, quad, kApTurn);
+}
+
+// Four rotated dimensions of a lane in fp64: x (xa) with the other dimensions of their pairs (xo).  (The series are written out
+// here and below: through a function for any number of angles, the 4-bit append spilled more.)
 __device__ __forceinline__ void ap_turn_f64(const RopeArgs &A, int t, float4 xa, float4 xo, int lane, double y[4]) {
     const float xa4[4] = {xa.x, xa.y, xa.z, xa.w}, xb4[4] = {xo.x, xo.y, xo.z, xo.w};
     const int pairs = A.pairs, d0 = 4 * lane;
@@ -110,6 +118,30 @@ __device__ __forceinline__ void ap_turn_f64(const RopeArgs &A, int t, float4 xa,
         const double r = __dadd_rn(__dmul_rn((double)xa4[j], cc), __dmul_rn((double)xb4[j], ss));
         y[j] = on ? r : (double)xa4[j];
     }
+}
+// One of them, j.
+__device__ __forceinline__ double ap_turn_f64(const RopeArgs &A, int t, float xa, float xo, int lane, int j) {
+    const int pairs = A.pairs, d0 = 4 * lane;
+    if (d0 >= 2 * pairs) return xa;
+    const bool up = !A.interleaved && d0 >= pairs;
+    uint32_t quad;
+    const int64_t r = ap_phase(A, t, A.interleaved ? 2 * lane + (j >> 1) : d0 + j - (up ? pairs : 0), &quad);
+    const double x = (double)r * (3.14159265358979323846 * 0x1p-63), z = x * x;
+    const double fc[9] = {1.0 / 20922789888000.0, -1.0 / 87178291200.0, 1.0 / 479001600.0, -1.0 / 3628800.0, 1.0 / 40320.0,
+                          -1.0 / 720.0, 1.0 / 24.0, -0.5, 1.0};
+    const double fs[9] = {1.0 / 355687428096000.0, -1.0 / 1307674368000.0, 1.0 / 6227020800.0, -1.0 / 39916800.0,
+                          1.0 / 362880.0, -1.0 / 5040.0, 1.0 / 120.0, -1.0 / 6.0, 1.0};
+    double c = fc[0], s = fs[0];
+#pragma unroll
+    for (int k = 1; k < 9; ++k) {
+        c = fma(c, z, fc[k]);
+        s = fma(s, z, fs[k]);
+    }
+    s *= x;
+    if (quad & 1) { const double w = s; s = c; c = -w; }
+    if (quad & 2) { s = -s; c = -c; }
+    if (!(A.interleaved ? (j & 1) : up)) s = -s;
+    return __dadd_rn(__dmul_rn((double)xa, c), __dmul_rn((double)xo, s));
 }
 
 // Turns per position of a frequency in radians, as a fraction of 2^64 modulo a turn:
