@@ -42,6 +42,34 @@ __device__ __forceinline__ void p8_mma_ss(uint32_t d, uint64_t a, uint64_t b, ui
         : "memory");
 }
 
+// n (4 or 8) columns of a warp's lanes.
+template <int n>
+__device__ __forceinline__ void p8_ld(uint32_t t, float *f) {
+    if (n == 8) {
+        pa_ld8(t, f);
+    } else {
+        uint32_t *const v = reinterpret_cast<uint32_t *>(f);
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(t)
+                     : "memory");
+    }
+}
+template <int n>
+__device__ __forceinline__ void p8_st(uint32_t t, const float *f) {
+    const uint32_t *const v = reinterpret_cast<const uint32_t *>(f);
+    if (n == 8) pa_st8(t, v);
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                     : "memory");
+}
+
+template <int n>
+__device__ __forceinline__ void p8_line(uint8_t *to, const uint32_t *w) {  // n fp16
+    if (n == 8) *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[n == 8 ? 2 : 0], w[n == 8 ? 3 : 0]);
+    else *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+}
+
 struct P8Seg {
     int token0, head0, row0, rows;  // first token of the request, first query head, rows of the tile
     int base, len, slot;            // position of token 0; workspace slot, or -1: write the output
@@ -49,14 +77,65 @@ struct P8Seg {
     int tiles;                      // of this segment
 };
 
-// Warps: four for V, four for each softmax group (of up to 32 rows), one that copies, two that issue the MMAs of S
+// Query rows row0 + step i + (0, 1), i < n, of a segment: fetched, split and laid out by a warp, sixteen lanes to a row.
+template <int RP, int n>
+__device__ __forceinline__ void p8_queries(const PaArgs &A, const P8Seg &g, int row0, int step, uint8_t *q, float *qs, int lane) {
+    const int ch = lane & 15;
+    uint4 w[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+        const int row = row0 + step * i + (lane >> 4);
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < g.rows) {
+            const int rr = g.row0 + row, tok = rr / A.G;
+            w[i] = *reinterpret_cast<const uint4 *>(A.q + ((int64_t)(g.token0 + tok) * A.Hq + g.head0 + rr - tok * A.G) * kPgDim + ch * 8);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+        const int row = row0 + step * i + (lane >> 4);
+        const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t top = 0u;  // magnitudes of bf16 are ordered as their bits
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = __vmaxu2(top, ww[j] & 0x7FFF7FFFu);
+        top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+        const bool finite = top < 0x7F80u;
+        const int e = max(p8_need(__uint_as_float(top << 16)), -118);
+        const float inv = finite ? p8_pow2(-e) : 0.f;
+        uint32_t hi4[2], lo4[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // (0 where the row is not finite: its factor makes it NaN)
+            const float a = finite ? __uint_as_float(ww[j] << 16) * inv : 0.f;
+            const float b = finite ? __uint_as_float(ww[j] & 0xFFFF0000u) * inv : 0.f;
+            const uint32_t c = p8_encode2(a, b);
+            const float2 f = p8_floats2(c);
+            const uint32_t d = p8_encode2((a - f.x) * 16.f, (b - f.y) * 16.f);  // at most 256
+            if (j & 1) {
+                hi4[j >> 1] |= c << 16;
+                lo4[j >> 1] |= d << 16;
+            } else {
+                hi4[j >> 1] = c;
+                lo4[j >> 1] = d;
+            }
+        }
+        uint8_t *const to = q + row * 128 + (((ch >> 1) ^ (row & 7)) * 16) + (ch & 1) * 8;
+        *reinterpret_cast<uint2 *>(to) = make_uint2(hi4[0], hi4[1]);
+        *reinterpret_cast<uint2 *>(to + RP * 128) = make_uint2(lo4[0], lo4[1]);
+        if (ch == 0) qs[row] = finite ? p8_pow2(e) : __int_as_float(0x7FC00000);
+    }
+}
+
+// Warps: four for V, four for each softmax group (two groups for up to 32 rows, four for more), one that copies, two that issue the MMAs of S
 // and of O, one that fetches and splits queries.  Two CTAs to an SM where registers and tensor memory allow.
 template <int RP, bool F32>
 struct P8Cfg {
     static constexpr int N = RP < 16 ? 16 : (RP + 15) / 16 * 16;
     static constexpr int NS = 2 * RP;            // columns of S: both parts of the queries
     static constexpr int NO = F32 ? 2 * RP : N;  // columns of O: for fp32 outputs P's two parts, rows j and RP + j
-    static constexpr int kGroups = RP > 32 ? RP / 32 : 1, RG = RP / kGroups;  // softmax groups, rows of each
+    static constexpr int kGroups = RP == 8 ? 1 : RP <= 32 ? 2 : 4, RG = RP / kGroups;  // softmax groups, rows of each
     static constexpr int kThreads = (4 + 4 * kGroups + 4) * 32;
     static constexpr int kCtas = RP <= (F32 ? 16 : 24) ? 2 : 1;  // per SM
     static constexpr uint32_t kCols = kCtas == 2 ? 256 : 512;
@@ -107,7 +186,8 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
     const uint32_t b_s = b_sf + 32, b_pv = b_sf + 48;           // S(t), O(t) complete
     const uint32_t b_vfree = b_sf + 64;                         // V's columns read
     const uint32_t b_q = b_sf + 80, b_qfree = b_sf + 96;        // queries of a segment there, read
-    const uint32_t b_end = b_sf + 112, b_seg = b_sf + 120;      // segment descriptors (kP8Ring of them)
+    const uint32_t b_end = b_sf + 112, b_q0 = b_sf + 120;       // b_q0: those of the first segment
+    const uint32_t b_seg = b_sf + 128;                          // segment descriptors (kP8Ring of them)
 
     if (tid == 0) {
         for (int i = 0; i < A.stages; ++i) {
@@ -124,6 +204,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
             mbar_init(b_qfree + 8 * i, 1);
         }
         mbar_init(b_end, 2);
+        mbar_init(b_q0, kCopyWarp);
         for (int i = 0; i < kP8Ring; ++i) mbar_init(b_seg + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -131,6 +212,13 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
         s_info[tid] = PaTileInfo{};
         s_seg[tid] = P8Seg{};
         if (tid < 2 * Cfg::kGroups) s_quit[tid >> 1][tid & 1] = 0;
+    }
+    // (before the wait: the kernel ahead on the stream has none, or has ended)
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(Cfg::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -174,15 +262,13 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
     if (blockIdx.x == 0)
         for (int r = tid; r <= A.R; r += kThreads) A.prefix[r] = s_pre[r];
     const int lo = pa_lo(n_tiles, gridDim.x, blockIdx.x), hi = pa_lo(n_tiles, gridDim.x, blockIdx.x + 1);
-    if (n_tiles == 0 || hi <= lo) return;
+    if (n_tiles == 0 || hi <= lo) {
+        if (warp == 0)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "r"(Cfg::kCols) : "memory");
+        return;
+    }
     const uint32_t count = hi - lo;
 
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
-                     "r"(Cfg::kCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
     pa_fence_before();
     __syncthreads();
     pa_fence_after();
@@ -195,6 +281,17 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
     // Tile t's phase of a barrier that counts the tiles of one of two buffers, or of n.
     auto phase = [](uint32_t t, uint32_t n) { return (t / n) & 1u; };
 
+    if (warp < kCopyWarp) {  // the first segment's queries: the V and the softmax warps, which have nothing to do yet
+        if (pa_wait(b_seg, 0u, &s_ctl)) {
+            const P8Seg g = s_seg[0];
+            constexpr int kWarps = kCopyWarp, kEach = (RP / 2 + kWarps - 1) / kWarps;
+            if (2 * warp + 2 * kWarps * (kEach - 1) < RP) p8_queries<RP, kEach>(A, g, 2 * warp, 2 * kWarps, s_q, s_qs[0], lane);
+            else if (kEach > 1) p8_queries<RP, kEach - (kEach > 1)>(A, g, 2 * warp, 2 * kWarps, s_q, s_qs[0], lane);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) pa_arrive(b_q0);
+    }
     if (warp >= kCopyWarp && Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsRest));
     if (warp == kCopyWarp) {
         // ---- copies: lane j < 8 brings unit j of each tile ---------------------------------
@@ -210,6 +307,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
             }
             r = a;
         }
+        const bool copies = s_ctl.limit != 0u;  // (a limit of no polls, the test hook: as if the copy engine had stopped)
         int u = lo, k = 0, n_seg = 0, st = 0;
         uint32_t st_phase = 0;
         PaReq x = pa_req(A, r);
@@ -272,10 +370,10 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
                     const bool first = tile == 0 || u == lo;
                     t.flags = (first ? 1u : 0u) | (u + 1 == end ? 2u : 0u) | ((uint32_t)si << 2);
                     s_info[k % kP8Ring] = t;
-                    mbar_expect_tx(b_full + 8 * st, __popc(mask) * kP8UnitBytes);
+                    if (copies) mbar_expect_tx(b_full + 8 * st, __popc(mask) * kP8UnitBytes);
                 }
                 __syncwarp();
-                if (ok) {
+                if (ok && copies) {
                     const int j = tile * kPaTileUnits + lane, unit = j - page_of(j) * upp;
                     const uint8_t *const src = A.pages + (((int64_t)pg * A.Hkv + h) * upp + unit) * kP8UnitBytes;
                     bulk_g2s(smem_u32(s_k + st * kP8StageK + lane * 2048), src, 2048, b_full + 8 * st);
@@ -291,7 +389,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
         }
         // Whatever the other warps do (one may still give up a wait once this one has no more to copy), the
         // copies in flight land before the CTA ends.
-        for (int j = max(0, k - A.stages); j < k; ++j)
+        for (int j = max(0, k - A.stages); copies && j < k; ++j)
             mbar_wait_ok(b_full + 8 * (j % A.stages), (uint32_t)(j / A.stages) & 1u);
         __syncwarp();
     } else if (warp == kSWarp) {
@@ -302,7 +400,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
         for (uint32_t t = 0; t < count; ++t) {
             pa_wait(b_full + 8 * st, st_phase, &s_ctl);
             const uint32_t flags = s_info[t % kP8Ring].flags;
-            if (flags & 1u) pa_wait(b_q + 8 * (n_seg & 1), phase(n_seg, 2), &s_ctl);
+            if (flags & 1u) pa_wait(n_seg ? b_q + 8 * (n_seg & 1) : b_q0, n_seg ? phase(n_seg - (~n_seg & 1u), 2) : 0u, &s_ctl);
             if (t >= SB) pa_wait(b_sf + 8 * (t % SB), phase(t - SB, SB), &s_ctl);
             if (lane == 0) {
                 pa_fence_after();
@@ -350,7 +448,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
         }
         __syncwarp();
     } else if (warp == kOWarp + 1) {
-        // ---- queries: two rows at a time, sixteen lanes to each ----------------------------
+        // ---- queries, of all segments but the first ----------------------------------------
         // Segment n + 2 takes n's buffer once the last S of n is complete.  The rows' factors have four: that S
         // waited for softmax warps to have read S, and the factors with it, two tiles before.
         uint32_t done = 0;
@@ -360,59 +458,11 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
             if (!pa_wait(b_seg + 8 * si, phase(n, kP8Ring), &s_ctl)) break;
             const P8Seg g = s_seg[si];
             done += g.tiles;
+            if (n == 0) continue;
             if (n >= 2) pa_wait(b_qfree + 8 * (n & 1), phase(n - 2, 2), &s_ctl);
             uint8_t *const q = s_q + (n & 1) * Cfg::kQ;
-            const int ch = lane & 15;
             constexpr int kDeep = RP / 2 < 8 ? RP / 2 : 4;
-#pragma unroll 1
-            for (int i0 = 0; i0 < RP / 2; i0 += kDeep) {
-                uint4 w[kDeep];
-#pragma unroll
-                for (int i = 0; i < kDeep; ++i) {
-                    const int row = 2 * (i0 + i) + (lane >> 4);
-                    w[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < g.rows) {
-                        const int rr = g.row0 + row, tok = rr / A.G;
-                        w[i] = *reinterpret_cast<const uint4 *>(
-                            A.q + ((int64_t)(g.token0 + tok) * A.Hq + g.head0 + rr - tok * A.G) * kPgDim + ch * 8);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kDeep; ++i) {
-                    const int row = 2 * (i0 + i) + (lane >> 4);
-                    const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    uint32_t top = 0u;  // magnitudes of bf16 are ordered as their bits
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) top = __vmaxu2(top, ww[j] & 0x7FFF7FFFu);
-                    top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-                    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-                    const bool finite = top < 0x7F80u;
-                    const int e = max(p8_need(__uint_as_float(top << 16)), -118);
-                    const float inv = finite ? p8_pow2(-e) : 0.f;
-                    uint32_t hi4[2], lo4[2];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        // (0 where the row is not finite: its factor makes it NaN)
-                        const float a = finite ? __uint_as_float(ww[j] << 16) * inv : 0.f;
-                        const float b = finite ? __uint_as_float(ww[j] & 0xFFFF0000u) * inv : 0.f;
-                        const uint32_t c = p8_encode2(a, b);
-                        const float2 f = p8_floats2(c);
-                        const uint32_t d = p8_encode2((a - f.x) * 16.f, (b - f.y) * 16.f);  // at most 256
-                        if (j & 1) {
-                            hi4[j >> 1] |= c << 16;
-                            lo4[j >> 1] |= d << 16;
-                        } else {
-                            hi4[j >> 1] = c;
-                            lo4[j >> 1] = d;
-                        }
-                    }
-                    uint8_t *const to = q + row * 128 + (((ch >> 1) ^ (row & 7)) * 16) + (ch & 1) * 8;
-                    *reinterpret_cast<uint2 *>(to) = make_uint2(hi4[0], hi4[1]);
-                    *reinterpret_cast<uint2 *>(to + RP * 128) = make_uint2(lo4[0], lo4[1]);
-                    if (ch == 0) s_qs[n & 3][row] = finite ? p8_pow2(e) : __int_as_float(0x7FC00000);
-                }
-            }
+            for (int i = 0; i < RP / 2; i += kDeep) p8_queries<RP, kDeep>(A, g, 2 * i, 2, q, s_qs[n & 3], lane);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) pa_arrive(b_q + 8 * (n & 1));
@@ -469,6 +519,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
 
         // l: sums of p over this lane's positions.  acc (fp32 outputs): o, added up here tile by tile,
         // since the tensor core truncates what it adds to its accumulators (2^-24 a time).
+        constexpr int kStep = RG % 8 ? 4 : 8;           // rows taken together
         int pos0 = 0, off0 = 0, whole_to = 0, len = 0;  // of the segment
         f2 l[RG / 2], acc[F32 ? RG / 2 : 1];
         const f2 lo_step = pa_f2(0x1p-11f, 0x1p-11f), q_step = pa_f2(0x1p-4f, 0x1p-4f);
@@ -478,7 +529,13 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
             f2 s[RG / 2];
             // A wait that gave up must not let the group's threads disagree on what comes next: the
             // vote below carries it, and then all of them leave.
-            if (!pa_wait(b_s + 8 * (t % SB), phase(t, SB), &s_ctl) || !pa_wait(b_full + 8 * st, st_phase, &s_ctl)) s_quit[sg][t & 1] = 1;
+            // (Three questions at once, each as long as a whole wait; mostly all are answered.)
+            uint32_t got = mbar_poll(b_s + 8 * (t % SB), phase(t, SB), true) ? 1u : 0u;
+            if (mbar_poll(b_full + 8 * st, st_phase, true)) got |= 2u;
+            if (t < Cfg::PB || mbar_poll(b_pv + 8 * ((t - Cfg::PB) & 1), phase(t - Cfg::PB, 2), false)) got |= 4u;  // P is read
+            got = __reduce_and_sync(~0u, got);
+            if ((got & 3u) != 3u && (!pa_wait(b_s + 8 * (t % SB), phase(t, SB), &s_ctl) || !pa_wait(b_full + 8 * st, st_phase, &s_ctl)))
+                s_quit[sg][t & 1] = 1;
             const PaTileInfo ti = s_info[t % kP8Ring];
             const bool first = ti.flags & 1u, last = ti.flags & 2u;
             const P8Seg &g = s_seg[ti.flags >> 2];
@@ -495,16 +552,28 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
             const float lv = (float)ev, iv = p8_pow2(-ev);
             const f2 c2 = pa_f2(ck, ck), lv2 = pa_f2(lv, lv), iv2 = pa_f2(iv, iv);
             pa_fence_after();
+            {
+                // the next columns are on their way while these are joined
+                float h[2][kStep], f[2][kStep];
+                const uint32_t col = tmem + quarter + Cfg::kColS + NS * (t % SB) + rb;
+                p8_ld<kStep>(col, h[0]);
+                p8_ld<kStep>(col + RP, f[0]);
 #pragma unroll
-            for (int j = 0; j < RG; j += 8) {
-                float h[8], f[8];
-                pa_ld8(tmem + quarter + Cfg::kColS + NS * (t % SB) + rb + j, h);
-                pa_ld8(tmem + quarter + Cfg::kColS + NS * (t % SB) + RP + rb + j, f);
-                pa_wait_ld();
+                for (int j = 0; j < RG; j += kStep) {
+                    constexpr int kHalf = kStep / 2;
+                    const int now = (j / kStep) & 1;
+                    pa_wait_ld();
+                    if (j + kStep < RG) {
+                        p8_ld<kStep>(col + j + kStep, h[now ^ 1]);
+                        p8_ld<kStep>(col + RP + j + kStep, f[now ^ 1]);
+                    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f2 q = *reinterpret_cast<const f2 *>(s_qs[n_seg & 3] + rb + j + 2 * i);
-                    s[j / 2 + i] = pa_mul2(pa_fma2(pa_f2(f[2 * i], f[2 * i + 1]), q_step, pa_f2(h[2 * i], h[2 * i + 1])), q);
+                    for (int i = 0; i < kHalf; i += 2) {
+                        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(s_qs[n_seg & 3] + rb + j + 2 * i);
+                        s[j / 2 + i] = pa_mul2(pa_fma2(pa_f2(f[now][2 * i], f[now][2 * i + 1]), q_step, pa_f2(h[now][2 * i], h[now][2 * i + 1])), q.x);
+                        s[j / 2 + i + 1] =
+                            pa_mul2(pa_fma2(pa_f2(f[now][2 * i + 2], f[now][2 * i + 3]), q_step, pa_f2(h[now][2 * i + 2], h[now][2 * i + 3])), q.y);
+                    }
                 }
             }
             pa_fence_before();
@@ -612,30 +681,30 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
                         pa_wait(b_pv + 8 * ((t - 1) & 1), phase(t - 1, 2), &s_ctl);
                         pa_fence_after();
 #pragma unroll
-                        for (int j = 0; j < RG; j += 8) {
-                            float o[8];
-                            pa_ld8(tmem + quarter + Cfg::kColO + rb + j, o);
+                        for (int j = 0; j < RG; j += kStep) {
+                            float o[kStep];
+                            p8_ld<kStep>(tmem + quarter + Cfg::kColO + rb + j, o);
                             pa_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] *= s_fac[rb + j + i];
-                            pa_st8(tmem + quarter + Cfg::kColO + rb + j, reinterpret_cast<const uint32_t *>(o));
+                            for (int i = 0; i < kStep; ++i) o[i] *= s_fac[rb + j + i];
+                            p8_st<kStep>(tmem + quarter + Cfg::kColO + rb + j, o);
                         }
                         pa_wait_st();
                         pa_fence_before();
                     }
                 }
             }
-            if (t >= Cfg::PB) pa_wait(b_pv + 8 * ((t - Cfg::PB) & 1), phase(t - Cfg::PB, 2), &s_ctl);  // P is read
+            if (!(got & 4u)) pa_wait(b_pv + 8 * ((t - Cfg::PB) & 1), phase(t - Cfg::PB, 2), &s_ctl);  // P is read
             if (F32 && !first) {
                 pa_fence_after();
 #pragma unroll
-                for (int j = 0; j < RG; j += 8) {
-                    float o[8], lo[8];
-                    pa_ld8(tmem + quarter + Cfg::kColO + rb + j, o);
-                    pa_ld8(tmem + quarter + Cfg::kColO + RP + rb + j, lo);
+                for (int j = 0; j < RG; j += kStep) {
+                    float o[kStep], lo[kStep];
+                    p8_ld<kStep>(tmem + quarter + Cfg::kColO + rb + j, o);
+                    p8_ld<kStep>(tmem + quarter + Cfg::kColO + RP + rb + j, lo);
                     pa_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < kStep / 2; ++i)
                         acc[j / 2 + i] = pa_add2(acc[j / 2 + i], pa_fma2(pa_f2(lo[2 * i], lo[2 * i + 1]), lo_step, pa_f2(o[2 * i], o[2 * i + 1])));
                 }
                 pa_fence_before();
@@ -644,29 +713,29 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
                     for (int j = 0; j < RG / 2; ++j) acc[j] = pa_mul2(acc[j], *reinterpret_cast<const f2 *>(s_fac + rb + 2 * j));
                 }
             }
-            uint8_t *const prow = s_p + t % Cfg::PB * Cfg::kP + (gt >> 3) * 128 + (gt & 7) * 16 + (rb >> 3) * 2048;
+            uint8_t *const prow = s_p + t % Cfg::PB * Cfg::kP + (gt >> 3) * 128 + (gt & 7) * 16;
 #pragma unroll
-            for (int j = 0; j < RG; j += 8) {
-                float p[8];
+            for (int j = 0; j < RG; j += kStep) {
+                float p[kStep];
+                uint32_t w[kStep / 2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kStep / 2; ++i) {
                     const float2 v = pa_un2(s[j / 2 + i]);
                     p[2 * i] = pa_ex2(v.x);
                     p[2 * i + 1] = pa_ex2(v.y);
                     l[j / 2 + i] = pa_fma2(pa_f2(p[2 * i], p[2 * i + 1]), iv2, l[j / 2 + i]);
+                    w[i] = pa_pack(p[2 * i], p[2 * i + 1]);
                 }
-                uint4 w = make_uint4(pa_pack(p[0], p[1]), pa_pack(p[2], p[3]), pa_pack(p[4], p[5]), pa_pack(p[6], p[7]));
-                *reinterpret_cast<uint4 *>(prow + (j >> 3) * 2048) = w;
+                // rows in lines of eight
+                p8_line<kStep>(prow + ((rb + j) >> 3) * 2048 + ((rb + j) & 7) * 2, w);
                 if (F32) {
-                    const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t lo2[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = __half22float2(reinterpret_cast<const __half2 &>(h[i]));
+                    for (int i = 0; i < kStep / 2; ++i) {
+                        const float2 f = __half22float2(reinterpret_cast<const __half2 &>(w[i]));
                         // 2^11 (p - f), exact before the rounding
-                        lo2[i] = pa_pack(fmaf(f.x, -2048.f, p[2 * i] * 2048.f), fmaf(f.y, -2048.f, p[2 * i + 1] * 2048.f));
+                        w[i] = pa_pack(fmaf(f.x, -2048.f, p[2 * i] * 2048.f), fmaf(f.y, -2048.f, p[2 * i + 1] * 2048.f));
                     }
-                    *reinterpret_cast<uint4 *>(prow + (RP >> 3) * 2048 + (j >> 3) * 2048) = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
+                    p8_line<kStep>(prow + ((RP + rb + j) >> 3) * 2048 + ((RP + rb + j) & 7) * 2, w);
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -676,7 +745,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
             if (last) {
                 // The segment's sums over positions (each step of the exchange halves the rows a lane
                 // holds, so that lane i ends with row i), then o.
-                constexpr int RX = RG == 24 ? 32 : RG;
+                constexpr int RX = RG == 12 ? 16 : RG;
                 float v[RX];
 #pragma unroll
                 for (int j = 0; j < RX; j += 2) {
@@ -715,16 +784,16 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
                 pa_fence_after();
                 float o[RG];
 #pragma unroll
-                for (int j = 0; j < RG; j += 8) pa_ld8(tmem + quarter + Cfg::kColO + rb + j, o + j);
+                for (int j = 0; j < RG; j += kStep) p8_ld<kStep>(tmem + quarter + Cfg::kColO + rb + j, o + j);
                 pa_wait_ld();
                 if (F32) {
 #pragma unroll
-                    for (int j = 0; j < RG; j += 8) {
-                        float lo[8];
-                        pa_ld8(tmem + quarter + Cfg::kColO + RP + rb + j, lo);
+                    for (int j = 0; j < RG; j += kStep) {
+                        float lo[kStep];
+                        p8_ld<kStep>(tmem + quarter + Cfg::kColO + RP + rb + j, lo);
                         pa_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < kStep; ++i) {
                             const float2 x = pa_un2(acc[(j + i) / 2]);
                             o[j + i] = fmaf(lo[i], 0x1p-11f, o[j + i]) + (i & 1 ? x.y : x.x);
                         }
