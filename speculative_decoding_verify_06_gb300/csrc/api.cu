@@ -60,6 +60,7 @@ int paged8_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv
                   cudaStream_t stream);
 int paged8_read(const int64_t *slots, int T, int Hkv, const void *pages, int page, int64_t n_pages, float *k, float *v,
                 cudaStream_t stream);
+size_t paged8_attention_ws_bytes(int Hq, int Hkv, int R, int max_new);
 int paged8_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,
                      int max_new, const int32_t *table, int width, const void *pages, int page,
                      int64_t n_pages, int Hq, int Hkv, float scale, void *out, int out_dtype, void *ws,
@@ -286,7 +287,7 @@ int svd_paged8_read(const int64_t *slots, int T, int Hkv, const void *pages, int
 }
 
 size_t svd_paged8_attention_workspace_bytes(int Hq, int Hkv, int R, int max_new) {
-    return svd::paged_attention_ws_bytes(Hq, Hkv, R, max_new);
+    return svd::paged8_attention_ws_bytes(Hq, Hkv, R, max_new);
 }
 
 int svd_paged8_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,

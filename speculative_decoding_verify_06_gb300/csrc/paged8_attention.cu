@@ -70,6 +70,11 @@ __device__ __forceinline__ void p8_line(uint8_t *to, const uint32_t *w) {  // n 
     else *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
 }
 
+// What a CTA leaves to be joined: the row tile that begins among its tiles and goes on in the next CTAs, up to CTA last.
+struct P8Split {
+    int token0, head0, row0, rows;  // rows 0: none
+    int last, pad[3];
+};
 struct P8Seg {
     int token0, head0, row0, rows;  // first token of the request, first query head, rows of the tile
     int base, len, slot;            // position of token 0; workspace slot, or -1: write the output
@@ -157,7 +162,7 @@ struct P8Cfg {
 
 template <int RP, bool F32>
 __global__ void __launch_bounds__(P8Cfg<RP, F32>::kThreads, P8Cfg<RP, F32>::kCtas)
-paged8_attention_kernel(const __grid_constant__ PaArgs A) {
+paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ splits) {
     using Cfg = P8Cfg<RP, F32>;
     constexpr int NS = Cfg::NS, VB = Cfg::VB, SB = Cfg::SB, RG = Cfg::RG, kThreads = Cfg::kThreads;
     constexpr int kCopyWarp = 4 + 4 * Cfg::kGroups, kSWarp = kCopyWarp + 1, kOWarp = kCopyWarp + 2;
@@ -259,10 +264,9 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
         s_ctl.status = A.status;
     }
     __syncthreads();
-    if (blockIdx.x == 0)
-        for (int r = tid; r <= A.R; r += kThreads) A.prefix[r] = s_pre[r];
     const int lo = pa_lo(n_tiles, gridDim.x, blockIdx.x), hi = pa_lo(n_tiles, gridDim.x, blockIdx.x + 1);
     if (n_tiles == 0 || hi <= lo) {
+        if (tid == 0) splits[blockIdx.x].rows = 0;
         if (warp == 0)
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "r"(Cfg::kCols) : "memory");
         return;
@@ -312,6 +316,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
         uint32_t st_phase = 0;
         PaReq x = pa_req(A, r);
         int head_tiles = pa_head_tiles<RP>(A, x);
+        P8Split split = {};
         while (u < hi) {
             while (s_pre[r + 1] <= u) {
                 ++r;
@@ -342,6 +347,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
                 g.tiles = end - u;
                 s_seg[si] = g;
                 pa_arrive(b_seg + 8 * si);
+                if (u == s0 && end < s0 + nt) split = {g.token0, g.head0, g.row0, g.rows, pa_cta_of(n_tiles, gridDim.x, s0 + nt - 1), {}};
             }
             const int upp = A.page / kPgUnitPos;
             // j / upp for j < 2^28 (upp <= 16)
@@ -387,6 +393,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
             }
             ++n_seg;
         }
+        if (lane == 0) splits[blockIdx.x] = split;
         // Whatever the other warps do (one may still give up a wait once this one has no more to copy), the
         // copies in flight land before the CTA ends.
         for (int j = max(0, k - A.stages); copies && j < k; ++j)
@@ -826,8 +833,103 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Cfg::kCols) : "memory");
 }
 
+// Joins the segments of a row that several CTAs hold.  CTA (i, j) takes the i-th row tile that was split, and of it 8 / W rows, W
+// warps to each, every one over every W-th segment with all of its loads in flight together.
+template <int RP, bool F32, int W>
+__global__ void __launch_bounds__(256) paged8_join_kernel(const __grid_constant__ PaArgs A, const P8Split *__restrict__ splits, int ctas) {
+    __shared__ float4 s_acc[8][32];
+    __shared__ float2 s_ml[8];
+    __shared__ P8Split s_split;
+    __shared__ int s_first, s_count[8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s_first = -1;
+    griddep_wait();
+    griddep_launch_dependents();
+    int before = 0;  // split tiles of the CTAs gone through
+    for (int b0 = 0; b0 < ctas; b0 += 256) {
+        const int b = b0 + tid;
+        P8Split x = {};
+        if (b < ctas) x = splits[b];
+        const uint32_t there = __ballot_sync(~0u, x.rows > 0);
+        __syncthreads();
+        if (lane == 0) s_count[warp] = __popc(there);
+        __syncthreads();
+        int mine = before, all = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) mine += s_count[w];
+            all += s_count[w];
+        }
+        if (x.rows > 0 && mine + __popc(there & ((1u << lane) - 1u)) == (int)blockIdx.x) {
+            s_split = x;
+            s_first = b;
+        }
+        before += all;
+    }
+    __syncthreads();
+    const int f = s_first;
+    if (f < 0) return;
+    constexpr int kRows = 8 / W;
+    const int row = blockIdx.y * kRows + warp / W, wj = warp % W, e = s_split.last;
+    const bool mine = row < s_split.rows;
+    // (ref, sum, acc) += (r, l, o), a part that saw nothing (r = -inf) left out.
+    float ref = -INFINITY, sum = 0.f;
+    float4 acc = {0.f, 0.f, 0.f, 0.f};
+    auto join = [&](float r1, float l1, const float4 &o1) {
+        if (r1 == -INFINITY) return;
+        const float top = ref > r1 ? ref : r1;  // (NaN: r1)
+        const float k0 = ref == -INFINITY ? 0.f : pa_ex2(ref - top), k1 = pa_ex2(r1 - top);
+        sum = sum * k0 + l1 * k1;
+        acc.x = acc.x * k0 + o1.x * k1;
+        acc.y = acc.y * k0 + o1.y * k1;
+        acc.z = acc.z * k0 + o1.z * k1;
+        acc.w = acc.w * k0 + o1.w * k1;
+        ref = top;
+    };
+    constexpr int kDeep = W == 1 ? 4 : 8;
+    for (int c0 = f + wj; mine && c0 <= e; c0 += kDeep * W) {
+        float4 o[kDeep];
+        float2 ml[kDeep];
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const int c = c0 + j * W;
+            ml[j] = make_float2(-INFINITY, 0.f);
+            if (c <= e) {
+                const int64_t slot = (int64_t)(c == f ? 2 * f + 1 : 2 * c) * RP + row;
+                ml[j] = A.part_ml[slot];
+                o[j] = *reinterpret_cast<const float4 *>(A.part + slot * kPgDim + 4 * lane);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) join(ml[j].x, ml[j].y, o[j]);
+    }
+    if (W > 1) {
+        s_acc[warp][lane] = acc;
+        if (lane == 0) s_ml[warp] = make_float2(ref, sum);
+        __syncthreads();
+        if (wj) return;
+#pragma unroll
+        for (int j = 1; j < W; ++j) join(s_ml[warp + j].x, s_ml[warp + j].y, s_acc[warp + j][lane]);
+    }
+    if (!mine) return;
+    const float inv = ref == -INFINITY ? 0.f : 1.f / sum;
+    const int rr = s_split.row0 + row, tok = rr / A.G;
+    const int64_t at = ((int64_t)(s_split.token0 + tok) * A.Hq + s_split.head0 + rr - tok * A.G) * kPgDim + 4 * lane;
+    if (F32) {
+        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(A.out) + at) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 q = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        uint2 v;
+        v.x = reinterpret_cast<const uint32_t &>(p);
+        v.y = reinterpret_cast<const uint32_t &>(q);
+        *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(A.out) + at) = v;
+    }
+}
+
 template <int RP, bool F32>
-static int p8_launch(PaArgs A, cudaStream_t stream) {
+static int p8_launch(PaArgs A, P8Split *splits, cudaStream_t stream) {
     using Cfg = P8Cfg<RP, F32>;
     const size_t most = Cfg::kCtas == 2 ? 110 * 1024 : 216 * 1024;  // with the static part and 1 KB reserved a CTA
     A.stages = kP8MaxStages;
@@ -843,8 +945,24 @@ static int p8_launch(PaArgs A, cudaStream_t stream) {
         regs.store(at.numRegs, std::memory_order_relaxed);
     }
     if (Cfg::kSplit && regs.load(std::memory_order_relaxed) < Cfg::kRegs) return SVD_ERR_UNSUPPORTED;
-    SVD_CUDA_TRY(launch(paged8_attention_kernel<RP, F32>, dim3(grid), dim3(Cfg::kThreads), smem, stream, true, A));
-    return pa_merge<RP, F32, false>(A, grid, stream);
+    SVD_CUDA_TRY(launch(paged8_attention_kernel<RP, F32>, dim3(grid), dim3(Cfg::kThreads), smem, stream, true, A, splits));
+    // No more row tiles are split than there are, nor more than there are borders between CTAs.  Few row tiles are split over
+    // many CTAs each, and then eight warps join a row.
+    const int most_new = A.max_new < A.T ? A.max_new : A.T;
+    const int64_t by_request = (int64_t)A.R * (((int64_t)most_new * A.G + RP - 1) / RP), by_rows = ((int64_t)A.T * A.G + RP - 1) / RP + A.R;
+    const int64_t tiles = A.Hkv * (by_request < by_rows ? by_request : by_rows);
+    const int n = (int)(tiles < grid ? tiles : grid);
+    if (tiles * 4 <= grid)
+        SVD_CUDA_TRY(launch(paged8_join_kernel<RP, F32, 8>, dim3(n, RP), dim3(256), 0, stream, true, A, (const P8Split *)splits, grid));
+    else
+        SVD_CUDA_TRY(launch(paged8_join_kernel<RP, F32, 1>, dim3(n, (RP + 7) / 8), dim3(256), 0, stream, true, A, (const P8Split *)splits, grid));
+    return SVD_OK;
+}
+
+// The workspace of the 4-bit cache's attention, with the descriptions of what CTAs leave to be joined behind it.
+size_t paged8_attention_ws_bytes(int Hq, int Hkv, int R, int max_new) {
+    const size_t n = paged_attention_ws_bytes(Hq, Hkv, R, max_new);
+    return n ? align_up(n, 256) + (size_t)2 * sm_count() * sizeof(P8Split) : 0;
 }
 
 int paged8_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,
@@ -855,15 +973,18 @@ int paged8_attention(const uint16_t *q, int T, const int32_t *kv_len, const int3
     int rp;
     const int rc = pa_arguments(&A, &rp, q, T, kv_len, q_start, R, max_new, table, width, pages, page, n_pages, Hq, Hkv,
                                 scale, out, out_dtype, ws, ws_bytes);
-    if (rc != SVD_OK || T == 0) return rc;
-#define SVD_P8(RP) (out_dtype == SVD_F32 ? p8_launch<RP, true>(A, stream) : p8_launch<RP, false>(A, stream))
+    if (rc != SVD_OK) return rc;
+    if (ws_bytes < paged8_attention_ws_bytes(Hq, Hkv, R, max_new)) return SVD_ERR_WORKSPACE;
+    if (T == 0) return SVD_OK;
+    P8Split *const splits = (P8Split *)((uint8_t *)ws + align_up(paged_attention_ws_bytes(Hq, Hkv, R, max_new), 256));
+#define SVD_P8(RP) (out_dtype == SVD_F32 ? p8_launch<RP, true>(A, splits, stream) : p8_launch<RP, false>(A, splits, stream))
     switch (rp) {
         case 8: return SVD_P8(8);
         case 16: return SVD_P8(16);
         case 24: return SVD_P8(24);
         case 32: return SVD_P8(32);
-        case 64: return p8_launch<64, false>(A, stream);
-        default: return p8_launch<128, false>(A, stream);
+        case 64: return p8_launch<64, false>(A, splits, stream);
+        default: return p8_launch<128, false>(A, splits, stream);
     }
 #undef SVD_P8
 }
