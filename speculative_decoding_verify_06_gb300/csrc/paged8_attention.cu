@@ -840,31 +840,32 @@ __global__ void __launch_bounds__(256) paged8_join_kernel(const __grid_constant_
     __shared__ float4 s_acc[8][32];
     __shared__ float2 s_ml[8];
     __shared__ P8Split s_split;
-    __shared__ int s_first, s_count[8];
+    __shared__ int s_first, s_count[16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s_first = -1;
     griddep_wait();
     griddep_launch_dependents();
-    int before = 0;  // split tiles of the CTAs gone through
-    for (int b0 = 0; b0 < ctas; b0 += 256) {
-        const int b = b0 + tid;
-        P8Split x = {};
-        if (b < ctas) x = splits[b];
-        const uint32_t there = __ballot_sync(~0u, x.rows > 0);
-        __syncthreads();
-        if (lane == 0) s_count[warp] = __popc(there);
-        __syncthreads();
-        int mine = before, all = 0;
+    // (at most 512 CTAs: two to an SM)
+    P8Split x[2] = {};
+    uint32_t there[2];
 #pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            if (w < warp) mine += s_count[w];
-            all += s_count[w];
+    for (int i = 0; i < 2; ++i)
+        if (tid + 256 * i < ctas) x[i] = splits[tid + 256 * i];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        there[i] = __ballot_sync(~0u, x[i].rows > 0);
+        if (lane == 0) s_count[warp + 8 * i] = __popc(there[i]);
+    }
+    __syncthreads();
+    int before = 0;  // split tiles of the CTAs before
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        if ((w & 7) == warp && x[w >> 3].rows > 0 &&
+            before + __popc(there[w >> 3] & ((1u << lane) - 1u)) == (int)blockIdx.x) {
+            s_split = x[w >> 3];
+            s_first = tid + 256 * (w >> 3);
         }
-        if (x.rows > 0 && mine + __popc(there & ((1u << lane) - 1u)) == (int)blockIdx.x) {
-            s_split = x;
-            s_first = b;
-        }
-        before += all;
+        before += s_count[w];
     }
     __syncthreads();
     const int f = s_first;
