@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kTbThreads) paged_compact_kernel(const CpArgs 
     for (int r = wide ? 0 : warp; r < A.R; r += wide ? 1 : kTbWarps) {
         const int n = pages_of(r);
         const int32_t *const row = A.table + (int64_t)r * A.width;
-#pragma unroll 4
+#pragma unroll 8
         for (int c = wide ? tid : lane; c < n; c += wide ? kTbThreads : 32) {
             const int id = row[c];
             if (id >= 0 && id < A.n_pages) atomicOr(bits + (id >> 5), 1u << (id & 31));
@@ -302,39 +302,46 @@ int paged_compact(const int32_t *held, int R, int page, const int32_t *table, in
 }
 
 // ---- copying ---------------------------------------------------------------------------------
-// Work items of 16 KB, ordered by copy, pool and place; a CTA takes every grid-th.  A thread has four 16-byte
-// loads in flight.  Bounded by memory: every byte is read once and written once.
+// A page is cut into equal parts of up to 16 KB.  Work items, ordered by copy, pool and part; a CTA takes every
+// grid-th.  A thread has four 16-byte loads in flight.  Bounded by memory: every byte is read once and written once, and a
+// page that goes to several others is read from memory once if the parts in flight lie close together, so that more CTAs
+// are not better: 64 requests forked from eight of up to 4K, 860 MB written, 172 us with four CTAs to an SM (0.85 of the copy
+// peak), 164 with three, 195 with eight; a compaction of 640 MB 190 us (1.0), 203 and 207.  A CTA for every part
+// that the list has room for: 151, but 276 for the compaction, whose list is two thirds empty.  Loads of the next part ahead of the stores
+// of this one: 189 and 208.
 constexpr int kPcThreads = 256;
 constexpr int kPcDeep = 4;
-constexpr int kPcItem = kPcThreads * 16 * kPcDeep;
+constexpr int kPcPart = kPcThreads * 16 * kPcDeep;
+constexpr int kPcCtas = 4;  // to an SM
 
 struct PcArgs {
     void *pool[SVD_PAGED_MAX_POOLS];
     const int32_t *from, *to, *n_copies;
     int64_t page_bytes, n_pages;
-    int pools, most, items;  // work items of a page
+    int pools, most, parts, part;  // parts of a page, bytes of one
 };
 
-__global__ void __launch_bounds__(kPcThreads, 8) paged_copy_kernel(const __grid_constant__ PcArgs A) {
+__global__ void __launch_bounds__(kPcThreads) paged_copy_kernel(const __grid_constant__ PcArgs A) {
     griddep_wait();
     const int n = min(max(*A.n_copies, 0), A.most);
-    const int64_t per = (int64_t)A.pools * A.items, total = n * per;
+    const int64_t per = (int64_t)A.pools * A.parts, total = n * per;
     for (int64_t it = blockIdx.x; it < total; it += gridDim.x) {
         const int64_t copy = it / per;
-        const int rest = (int)(it - copy * per), pool = rest / A.items, part = rest - pool * A.items;
+        const int rest = (int)(it - copy * per), pool = rest / A.parts, part = rest - pool * A.parts;
         const int64_t from = A.from[copy], to = A.to[copy];
         if (from < 0 || from >= A.n_pages || to < 0 || to >= A.n_pages || from == to) continue;
-        uint8_t *const base = reinterpret_cast<uint8_t *>(A.pool[pool]);
-        const int64_t at = (int64_t)part * kPcItem + threadIdx.x * 16;
-        const uint8_t *const src = base + from * A.page_bytes + at;
-        uint8_t *const dst = base + to * A.page_bytes + at;
+        const int64_t at = (int64_t)part * A.part;
+        const int left = (int)min((int64_t)A.part, A.page_bytes - at) - (int)threadIdx.x * 16;  // bytes from this thread's first
+        uint8_t *const base = reinterpret_cast<uint8_t *>(A.pool[pool]) + at + threadIdx.x * 16;
+        const uint8_t *const src = base + from * A.page_bytes;
+        uint8_t *const dst = base + to * A.page_bytes;
         uint4 v[kPcDeep];
 #pragma unroll
         for (int j = 0; j < kPcDeep; ++j)
-            if (at + j * (kPcThreads * 16) < A.page_bytes) v[j] = *reinterpret_cast<const uint4 *>(src + j * (kPcThreads * 16));
+            if (j * (kPcThreads * 16) < left) v[j] = *reinterpret_cast<const uint4 *>(src + j * (kPcThreads * 16));
 #pragma unroll
         for (int j = 0; j < kPcDeep; ++j)
-            if (at + j * (kPcThreads * 16) < A.page_bytes) __stcs(reinterpret_cast<uint4 *>(dst + j * (kPcThreads * 16)), v[j]);
+            if (j * (kPcThreads * 16) < left) __stcs(reinterpret_cast<uint4 *>(dst + j * (kPcThreads * 16)), v[j]);
     }
 }
 
@@ -358,8 +365,9 @@ int paged_copy(void *const *pools, int n_pools, int64_t page_bytes, int64_t n_pa
         A.page_bytes = page_bytes;
         A.n_pages = n_pages;
         A.most = (int)most;
-        A.items = (int)((page_bytes + kPcItem - 1) / kPcItem);
-        const int64_t work = most * A.pools * A.items, fit = 8ll * sms;
+        A.parts = (int)((page_bytes + kPcPart - 1) / kPcPart);
+        A.part = (int)align_up((size_t)((page_bytes + A.parts - 1) / A.parts), 16);
+        const int64_t work = most * A.pools * A.parts, fit = (int64_t)kPcCtas * sms;
         SVD_CUDA_TRY(launch(paged_copy_kernel, dim3((unsigned)(work < fit ? work : fit)), dim3(kPcThreads), 0, stream, true, A));
     }
     return SVD_OK;
