@@ -1,4 +1,4 @@
-"""Verify passes of several requests over a paged 4-bit cache, with the lengths kept on the GPU.
+"""Verify passes of several requests over a paged cache in 4 or 8 bits, with the lengths kept on the GPU.
 
 A step is what "100 tokens per second ..." ("How speculative decoding gets past a per-token wall")
 describes for one sequence, for a batch of them ("Why a hiring company is writing this"): the tables
@@ -8,7 +8,10 @@ their requests' caches (svd_paged_attention).  Nothing of a step waits for the h
 counts, lengths, page ids and free pages stay in device memory, at the same addresses in every step, so a step can
 be recorded and replayed.
 
-    python -m speculative_decoding_verify_06_gb300.paged [requests] [window] [steps]
+Requests become copies of others (svd_paged_fork), for several answers to one prompt or a search, and the pages in use
+move to the start of their pool (svd_paged_compact); both carry the contents along in all layers (svd_paged_copy).
+
+    python -m speculative_decoding_verify_06_gb300.paged [requests] [window] [steps] [bits] [samples]
 
 runs a two-layer stand-in for a model on synthetic weights, accepting drafts and growing the caches.
 """
@@ -24,6 +27,8 @@ from . import svd
 class PagedBatch:
     """The caches of `requests` requests in `layers` pools of n_pages pages, one table for all layers.
 
+    bits: of a key or value in the cache, 4 (a scale for 32 dimensions of a position) or 8 (one for 16 positions).
+
     A request has up to max_window tokens in a step (lowered where windows stay shorter: the attention then
     takes smaller tiles), all requests together max_tokens.
 
@@ -34,14 +39,17 @@ class PagedBatch:
 
     def __init__(self, requests: int, layers: int, n_pages: int, page_size: int = 64, max_len: int = 32768,
                  max_window: int = 8, n_q_heads: int = 40, n_kv_heads: int = 8, rope: svd.Rope | None = None,
-                 out_dtype: int = svd.SVD_BF16, max_tokens: int | None = None, device="cuda"):
+                 out_dtype: int = svd.SVD_BF16, max_tokens: int | None = None, device="cuda", bits: int = 4):
+        if bits not in (4, 8):
+            raise ValueError(f"bits: 4 or 8, got {bits}")
         dev = torch.device(device)
+        self.bits = bits
         self.device, self.R, self.page, self.n_pages = dev, requests, page_size, n_pages
         self.Hq, self.Hkv, self.rope, self.out_dtype = n_q_heads, n_kv_heads, rope, out_dtype
         self.width = -(-max_len // page_size)
         self.max_window = self._step_window = max_window
         self.max_tokens = max_tokens or requests * max_window
-        nbytes = svd.svd_paged_cache_bytes(n_kv_heads, page_size, n_pages)
+        nbytes = (svd.svd_paged_cache_bytes if bits == 4 else svd.svd_paged8_cache_bytes)(n_kv_heads, page_size, n_pages)
         if nbytes == 0:
             raise ValueError("no such pool: see svd_paged_cache_bytes")
         self.pools = [torch.zeros(nbytes, dtype=torch.uint8, device=dev) for _ in range(layers)]
@@ -61,11 +69,15 @@ class PagedBatch:
         self.positions = torch.full((self.max_tokens,), -1, **i32)
         self.status = torch.zeros(requests, **i32)
         self.kv_len = torch.zeros(requests, **i32)
-        self.ws = torch.zeros(svd.svd_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, requests, max_window),
-                              dtype=torch.uint8, device=dev)
+        need = svd.svd_paged_attention_workspace_bytes if bits == 4 else svd.svd_paged8_attention_workspace_bytes
+        self.ws = torch.zeros(need(n_q_heads, n_kv_heads, requests, max_window), dtype=torch.uint8, device=dev)
         self.q = torch.empty((self.max_tokens, n_q_heads, 128), dtype=torch.bfloat16, device=dev)
         self.bad = torch.zeros(self.max_tokens, **i32)  # SVD_ST_* bits of the tokens appended since it was zeroed
         self.scale = 128 ** -0.5
+        self._layers = svd.Pools(self.pools, nbytes // n_pages)
+        self._copy_from, self._copy_to = (torch.full((n_pages,), -1, **i32) for _ in range(2))
+        self._n_copies = torch.zeros(1, **i32)
+        self.fork_status = torch.zeros(requests, **i32)  # of the last fork()
 
     @property
     def window(self):
@@ -76,7 +88,7 @@ class PagedBatch:
     @property
     def attention_status(self):
         """int32 [1], 0 while all is well; bit 0: a bounded wait of an attention kernel gave up, outputs since then
-        are undefined; bit 1: a finite query was above 65504 in magnitude, its row is NaN.  Stays until zeroed."""
+        are undefined; bit 1 (4 bits): a finite query was above 65504 in magnitude, its row is NaN.  Stays until zeroed."""
         return self.ws[:4].view(torch.int32)
 
     def begin(self, n_new, emitted=None, stream=None):
@@ -104,6 +116,35 @@ class PagedBatch:
             raise ValueError(f"who: [{self.R}], got {tuple(who.shape)}")
         with self._on(stream):
             torch.where(who, -self.held[self.now], self.window, out=self.window)
+
+    def fork(self, parent, emitted=None, stream=None):
+        """Request r becomes a copy of what request parent[r] keeps (int32 [R]; r itself or less than 0: it stays as it is),
+        in all layers, with pages of its own.  Comes after the last layer() of a step; emitted: the counts that the
+        next begin() gets (None: all of the last step's tokens are kept), in which a copy's count then says nothing.
+        A request that cannot become a copy (no such parent, a parent that is a copy itself or whose count is out of
+        order, no pages) stays as it is; fork_status has the reasons."""
+        self._counts("parent", parent)
+        if emitted is not None:
+            self._counts("emitted", emitted)
+        a, b = self.now, 1 - self.now
+        svd.svd_paged_fork(self.held[a], self._window[a], emitted, parent, self.R, self.page, self.table[a], self.width, self.free[a],
+                           self.n_free[a], self.n_pages, self.held[b], self._window[b], self.table[b], self.free[b], self.n_free[b],
+                           self._copy_from, self._copy_to, self._n_copies, self.fork_status, stream=stream)
+        svd.svd_paged_copy(self._layers, self.n_pages, self._copy_from, self._copy_to, self._n_copies, self.n_pages, stream=stream)
+        with self._on(stream):
+            self._state[a].copy_(self._state[b])
+        return self.fork_status
+
+    def compact(self, stream=None):
+        """The pages in use, U of them, move to ids 0 .. U - 1 of every pool (U = n_pages - n_free[now]), so that the rest
+        of the pools lies in one piece.  Comes after the last layer() of a step."""
+        a, b = self.now, 1 - self.now
+        svd.svd_paged_compact(self.held[a], self.R, self.page, self.table[a], self.width, self.n_pages, self.table[b], self.free[b],
+                              self.n_free[b], self._copy_from, self._copy_to, self._n_copies, stream=stream)
+        svd.svd_paged_copy(self._layers, self.n_pages, self._copy_from, self._copy_to, self._n_copies, self.n_pages, stream=stream)
+        pages = self.R * self.width + self.n_pages + 1  # the table, the stack and its count: the lengths stay
+        with self._on(stream):
+            self._state[a][:pages].copy_(self._state[b][:pages])
 
     def _on(self, stream):
         if stream is None:
@@ -161,28 +202,35 @@ class PagedBatch:
         pos, pos_ld = self._positions(positions, T)
         if T == 0:
             return out
-        pool = self.pools[l]
-        svd.svd_paged_append(qkv, qkv.stride(0) if T > 1 else width, T, self.Hq, self.Hkv, self.slots, pool, self.page, self.n_pages, self.q,
-                             rope=self.rope, positions=pos, positions_ld=pos_ld,
-                             dtype=svd.SVD_F32 if qkv.dtype == torch.float32 else svd.SVD_BF16, status=self.bad,
-                             stream=stream)
-        svd.svd_paged_attention(self.q, T, self.kv_len, self.q_start, self.R, self._step_window, self.table[self.now], self.width,
-                                pool, self.page, self.n_pages, self.Hq, self.Hkv, self.scale, out, self.out_dtype, self.ws,
-                                stream=stream)
+        pool, table = self.pools[l], self.table[self.now]
+        ld = qkv.stride(0) if T > 1 else width
+        kind = svd.SVD_F32 if qkv.dtype == torch.float32 else svd.SVD_BF16
+        if self.bits == 4:
+            svd.svd_paged_append(qkv, ld, T, self.Hq, self.Hkv, self.slots, pool, self.page, self.n_pages, self.q, rope=self.rope,
+                                 positions=pos, positions_ld=pos_ld, dtype=kind, status=self.bad, stream=stream)
+        else:
+            svd.svd_paged8_append(qkv, ld, T, self.Hq, self.Hkv, self.kv_len, self.q_start, self.R, table, self.width, pool, self.page,
+                                  self.n_pages, self.q, rope=self.rope, positions=pos, positions_ld=pos_ld, dtype=kind,
+                                  status=self.bad, stream=stream)
+        attend = svd.svd_paged_attention if self.bits == 4 else svd.svd_paged8_attention
+        attend(self.q, T, self.kv_len, self.q_start, self.R, self._step_window, table, self.width, pool, self.page, self.n_pages,
+               self.Hq, self.Hkv, self.scale, out, self.out_dtype, self.ws, stream=stream)
         return out
 
 
-def demo(requests: int = 8, window: int = 4, steps: int = 6, prompt: int = 200, layers: int = 2, seed: int = 0):
+def demo(requests: int = 8, window: int = 4, steps: int = 6, prompt: int = 200, layers: int = 2, seed: int = 0, bits: int = 4,
+         samples: int = 1):
     """Batched verify steps of a stand-in model: per layer q|k|v and o products of 4-bit weights
     (svd_verify_linear over all requests' window columns) around the paged attention; acceptance counts
-    are drawn instead of sampled.  Returns the PagedBatch and the kept lengths, step by step."""
+    are drawn instead of sampled.  samples > 1: the requests of each group of so many answer its first one's
+    prompt.  Returns the PagedBatch and the kept lengths, step by step."""
     from . import stack, synth
     dev = torch.device("cuda")
     C = requests * window
     hidden, kv = synth.HIDDEN, synth.N_KV_HEADS * 128
     rope = svd.Rope([10000.0 ** (-i / 64) for i in range(64)])
     b = PagedBatch(requests, layers, n_pages=requests * (prompt + (steps + 1) * window) // 64 + 2 * requests, max_len=4096,
-                   max_window=max(window, prompt), rope=rope, max_tokens=max(C, requests * prompt))
+                   max_window=max(window, prompt), rope=rope, max_tokens=max(C, requests * prompt), bits=bits)
     g = torch.Generator(device=dev)
     g.manual_seed(seed)
     # the prompts: their keys and values arrive in one step of `prompt` tokens a request
@@ -191,6 +239,8 @@ def demo(requests: int = 8, window: int = 4, steps: int = 6, prompt: int = 200, 
     o = torch.empty((b.max_tokens, b.Hq, 128), dtype=torch.bfloat16, device=dev)
     for l in range(layers):
         b.layer(l, qkv, o, n_tokens=requests * prompt)
+    if samples > 1:
+        b.fork((torch.arange(requests, device=dev) // samples * samples).to(torch.int32))
     b.max_window = window
     lin = [(stack.Linear(hidden, hidden + 2 * kv, C, seed + 10 * l, dev), stack.Linear(hidden, hidden, C, seed + 10 * l + 1, dev))
            for l in range(layers)]
@@ -213,7 +263,9 @@ def demo(requests: int = 8, window: int = 4, steps: int = 6, prompt: int = 200, 
 
 if __name__ == "__main__":
     import sys
-    batch, kept = demo(*[int(a) for a in sys.argv[1:4]])
+    args = [int(a) for a in sys.argv[1:6]]
+    batch, kept = demo(*args[:3], **dict(zip(("bits", "samples"), args[3:])))
     for n, k in enumerate(kept):
         print(f"step {n}: kept positions {k}")
+    batch.compact()
     print(f"{int(batch.n_free[batch.now])} of {batch.n_pages} pages free, status {batch.status.tolist()}")

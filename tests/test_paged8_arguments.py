@@ -1,7 +1,10 @@
 """Refusals of the 8-bit cache's and the page-moving entry points, without a GPU."""
-import pytest
+import inspect
 
-from speculative_decoding_verify_06_gb300 import build, svd
+import pytest
+import torch
+
+from speculative_decoding_verify_06_gb300 import build, paged, svd
 
 
 @pytest.fixture(scope="module")
@@ -96,3 +99,79 @@ def test_sizes(lib):
 def test_pools_keep_what_they_are_given():
     p = svd.Pools([16, 32, 48], 4112)
     assert len(p) == 3 and list(p._a) == [16, 32, 48] and p.page_bytes == 4112
+
+
+# ---- PagedBatch: what its calls are given -----------------------------------------------------------
+@pytest.fixture
+def calls(lib, monkeypatch):
+    """Every call of the entry points, recorded instead of made."""
+    made = []
+
+    def record(name):
+        f = inspect.signature(getattr(svd, name))
+
+        def call(*a, **k):
+            b = f.bind(*a, **k)
+            b.apply_defaults()
+            made.append((name, b.arguments))
+        monkeypatch.setattr(svd, name, call)
+    for name in ("svd_paged_append", "svd_paged_attention", "svd_paged8_append", "svd_paged8_attention", "svd_paged_fork", "svd_paged_copy",
+                 "svd_paged_compact"):
+        record(name)
+    return made
+
+
+def batch(**kw):
+    a = dict(requests=3, layers=2, n_pages=12, page_size=16, max_len=64, max_window=4, n_q_heads=4, n_kv_heads=2, device="cpu", bits=8)
+    return paged.PagedBatch(**{**a, **kw})
+
+
+@pytest.mark.parametrize("bits", [0, 5, 16, "8", None])
+def test_other_bits_are_refused(lib, bits):
+    with pytest.raises(ValueError, match="bits"):
+        batch(bits=bits)
+
+
+@pytest.mark.parametrize("bits,names", [(4, ["svd_paged_append", "svd_paged_attention"]), (8, ["svd_paged8_append", "svd_paged8_attention"])])
+def test_a_layer_goes_to_the_cache_of_its_bits(calls, bits, names):
+    b = batch(bits=bits)
+    assert b.pools[0].numel() == 12 * 2 * (4112 if bits == 8 else 2304)
+    b.layer(1, torch.zeros((9, 8 * 128)), torch.zeros((9, 4, 128), dtype=torch.bfloat16), n_tokens=7)
+    assert [n for n, _ in calls] == names
+    for _, a in calls:
+        assert a["n_tokens"] == 7 and a["pages"] is b.pools[1] and a["page_size"] == 16 and a["n_pages"] == 12
+    if bits == 8:
+        a = calls[0][1]
+        assert a["kv_len"] is b.kv_len and a["q_start"] is b.q_start and a["table"] is b.table[b.now] and a["max_pages"] == b.width
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_fork_and_compact_copy_whole_pages_of_all_layers(calls, bits):
+    b = batch(bits=bits)
+    assert b.fork(torch.zeros(3, dtype=torch.int32), torch.ones(3, dtype=torch.int32)) is b.fork_status
+    b.compact()
+    assert [n for n, _ in calls] == ["svd_paged_fork", "svd_paged_copy", "svd_paged_compact", "svd_paged_copy"]
+    for name, a in calls:
+        if name == "svd_paged_copy":
+            assert a["pools"].page_bytes == b.pools[0].numel() // 12 and a["pools"].pools == b.pools
+            assert a["copy_from"] is b._copy_from and a["copy_to"] is b._copy_to and a["n_copies"] is b._n_copies
+
+
+@pytest.mark.parametrize("parent", [torch.ones(3, dtype=torch.int64), torch.ones(2, dtype=torch.int32), torch.ones(3),
+                                    torch.ones(6, dtype=torch.int32)[::2], torch.ones((3, 1), dtype=torch.int32),
+                                    torch.ones(3, dtype=torch.int32, device="meta")])
+def test_parents_and_counts_of_another_form_are_refused(calls, parent):
+    good = torch.zeros(3, dtype=torch.int32)
+    for a in ((parent, None), (good, parent)):
+        with pytest.raises(ValueError, match="parent|emitted"):
+            batch().fork(*a)
+    assert not calls
+
+
+def test_compact_keeps_the_lengths(calls):
+    """The other copy's lengths are older than the state's: only the table and the stack come from there."""
+    b = batch()
+    b._state[0][-6:], b._state[1][-6:] = 5, 9
+    b._state[1][:-6] = 3
+    b.compact()
+    assert (b._state[0][-6:] == 5).all() and (b._state[0][:-6] == 3).all()
