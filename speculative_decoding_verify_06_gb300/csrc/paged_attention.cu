@@ -773,13 +773,13 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Cfg::kCols) : "memory");
 }
 template <int RP, bool F32>
-static int pa_launch(PaArgs A, cudaStream_t stream) {
+static int pa_launch(PaArgs A, int sms, cudaStream_t stream) {
     using Cfg = PaCfg<RP, F32>;
     const size_t most = Cfg::kCtas == 2 ? 110 * 1024 : 220 * 1024;  // with the static part and 1 KB reserved a CTA
     A.stages = kPaMaxStages;
     while (A.stages > 2 && Cfg::smem(A.stages, A.R) > most) --A.stages;
     const size_t smem = Cfg::smem(A.stages, A.R);
-    const int grid = Cfg::kCtas * sm_count();
+    const int grid = Cfg::kCtas * sms;
     SVD_CUDA_TRY((allow_smem<paged_attention_kernel<RP, F32>>(most)));
     // A register split above what the launch has would wait forever: refuse to launch one.
     static std::atomic<int> regs{0};
@@ -793,14 +793,7 @@ static int pa_launch(PaArgs A, cudaStream_t stream) {
     return pa_merge<RP, F32, true>(A, grid, stream);
 }
 size_t paged_attention_ws_bytes(int Hq, int Hkv, int R, int max_new) {
-    if (Hq < 1 || Hq > 4096 || Hkv < 1 || Hq % Hkv || R < 1 || R > SVD_PAGED_MAX_REQUESTS || max_new < 1 || sm_count() < 1)
-        return 0;
-    // enough for every variant up to the one that max_new takes, so that shorter windows fit too
-    const int most = pa_rows(Hq / Hkv, max_new, false);
-    size_t parts = 0;
-    for (int rp : {8, 16, 24, 32, 64, 128})
-        if (rp <= most && parts < (size_t)pa_ctas(rp) * rp) parts = (size_t)pa_ctas(rp) * rp;
-    return pa_prefix_bytes(R) + 2 * parts * (kPgDim + 2) * 4;
+    return pa_ws_bytes(Hq, Hkv, R, max_new, sm_count());
 }
 
 int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,
@@ -809,18 +802,19 @@ int paged_attention(const uint16_t *q, int T, const int32_t *kv_len, const int32
                     size_t ws_bytes, cudaStream_t stream) {
     PaArgs A;
     int rp;
+    const int sms = sm_count();
     const int rc = pa_arguments(&A, &rp, q, T, kv_len, q_start, R, max_new, table, width, pages, page, n_pages, Hq, Hkv,
-                                scale, out, out_dtype, ws, ws_bytes);
+                                scale, out, out_dtype, ws, ws_bytes, sms);
     if (rc != SVD_OK || T == 0) return rc;
     A.c *= 4.f;  // (the K operand is K / 4)
-#define SVD_PA(RP) (out_dtype == SVD_F32 ? pa_launch<RP, true>(A, stream) : pa_launch<RP, false>(A, stream))
+#define SVD_PA(RP) (out_dtype == SVD_F32 ? pa_launch<RP, true>(A, sms, stream) : pa_launch<RP, false>(A, sms, stream))
     switch (rp) {
         case 8: return SVD_PA(8);
         case 16: return SVD_PA(16);
         case 24: return SVD_PA(24);
         case 32: return SVD_PA(32);
-        case 64: return pa_launch<64, false>(A, stream);
-        default: return pa_launch<128, false>(A, stream);
+        case 64: return pa_launch<64, false>(A, sms, stream);
+        default: return pa_launch<128, false>(A, sms, stream);
     }
 #undef SVD_PA
 }

@@ -317,14 +317,24 @@ inline int pa_rows(int G, int max_new, bool f32) {
     const int64_t rows = (int64_t)G * max_new;
     return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows <= 32 || f32 ? 32 : rows <= 64 ? 64 : 128;
 }
-inline int pa_ctas(int rp) { return (rp <= 24 ? 2 : 1) * sm_count(); }  // at most
+inline int pa_ctas(int rp, int sms) { return (rp <= 24 ? 2 : 1) * sms; }  // at most
 inline size_t pa_prefix_bytes(int R) { return align_up(kPaHeader + ((size_t)R + 1) * 4, 256); }
-size_t paged_attention_ws_bytes(int Hq, int Hkv, int R, int max_new);
+// (sms is asked for once a call: the question costs a twentieth of a launch.)
+inline size_t pa_ws_bytes(int Hq, int Hkv, int R, int max_new, int sms) {
+    if (Hq < 1 || Hq > 4096 || Hkv < 1 || Hq % Hkv || R < 1 || R > SVD_PAGED_MAX_REQUESTS || max_new < 1 || sms < 1)
+        return 0;
+    // enough for every variant up to the one that max_new takes, so that shorter windows fit too
+    const int most = pa_rows(Hq / Hkv, max_new, false);
+    size_t parts = 0;
+    for (int rp : {8, 16, 24, 32, 64, 128})
+        if (rp <= most && parts < (size_t)pa_ctas(rp, sms) * rp) parts = (size_t)pa_ctas(rp, sms) * rp;
+    return pa_prefix_bytes(R) + 2 * parts * (kPgDim + 2) * 4;
+}
 
 // The arguments of an attention call, checked and laid out; *rp: the rows of its row tiles.  (Nothing is set for T = 0.)
 inline int pa_arguments(PaArgs *args, int *rp, const uint16_t *q, int T, const int32_t *kv_len, const int32_t *q_start, int R,
                         int max_new, const int32_t *table, int width, const void *pages, int page, int64_t n_pages, int Hq,
-                        int Hkv, float scale, void *out, int out_dtype, void *ws, size_t ws_bytes) {
+                        int Hkv, float scale, void *out, int out_dtype, void *ws, size_t ws_bytes, int sms) {
     if (!q || !kv_len || !q_start || !table || !pages || !out || !aligned16(q) || !aligned16(pages) ||
         !aligned16(out) || !aligned16(ws) || (out_dtype != SVD_F32 && out_dtype != SVD_BF16))
         return SVD_ERR_INVALID_ARG;
@@ -332,7 +342,7 @@ inline int pa_arguments(PaArgs *args, int *rp, const uint16_t *q, int T, const i
         !pg_pool_ok(Hkv, page, n_pages) || (int64_t)width * page > INT32_MAX - kPaTile || Hq < 1 || Hq > 4096 ||
         Hq % Hkv || (int64_t)T * Hq > INT32_MAX || !(scale > 0.f) || scale > 3.4e38f)
         return SVD_ERR_INVALID_ARG;
-    if (!ws || ws_bytes < paged_attention_ws_bytes(Hq, Hkv, R, max_new)) return SVD_ERR_WORKSPACE;
+    if (!ws || ws_bytes < pa_ws_bytes(Hq, Hkv, R, max_new, sms)) return SVD_ERR_WORKSPACE;
     if (T == 0) return SVD_OK;
     const int G = Hq / Hkv, rows_tile = pa_rows(G, max_new, out_dtype == SVD_F32);
     // the tiles of the largest call that these arguments allow are counted in 31 bits
@@ -350,7 +360,7 @@ inline int pa_arguments(PaArgs *args, int *rp, const uint16_t *q, int T, const i
     A.status = (uint32_t *)ws;
     A.prefix = (int32_t *)((uint8_t *)ws + kPaHeader);
     A.part = (float *)w;
-    A.part_ml = (float2 *)(w + (size_t)2 * pa_ctas(rows_tile) * rows_tile * kPgDim * 4);
+    A.part_ml = (float2 *)(w + (size_t)2 * pa_ctas(rows_tile, sms) * rows_tile * kPgDim * 4);
     A.n_pages = n_pages;
     A.T = T;
     A.R = R;

@@ -5,6 +5,7 @@
 #include "paged.cuh"
 
 #include <math.h>
+#include <string.h>
 
 namespace svd {
 
@@ -148,9 +149,12 @@ __device__ __forceinline__ double ap_turn_f64(const RopeArgs &A, int t, float xa
 // |inv| = m 2^e with a 53-bit m, times 1 / (2 pi) to 2^-128, in integers.
 inline uint64_t rope_phase(double inv) {
     const uint64_t c_hi = 0x28BE60DB9391054Aull, c_lo = 0x7F09D5F47D4D3770ull;
-    int e;
-    const uint64_t m = (uint64_t)ldexp(frexp(fabs(inv), &e), 53);
-    e -= 53;
+    uint64_t u;
+    memcpy(&u, &inv, sizeof u);
+    const int field = (int)(u >> 52) & 2047;
+    if (field == 0) return 0;  // (below 2^-1022: no turn within any position)
+    const uint64_t m = (u & ((1ull << 52) - 1)) | 1ull << 52;
+    const int e = field - 1075;
     const unsigned __int128 lo = (unsigned __int128)m * c_lo;
     const unsigned __int128 hi = (unsigned __int128)m * c_hi + (uint64_t)(lo >> 64);
     const uint64_t w0 = (uint64_t)lo, w1 = (uint64_t)hi, w2 = (uint64_t)(hi >> 64);  // w2:w1:w0 / 2^128

@@ -278,8 +278,11 @@ def _current_stream():
         def ask():
             return torch.cuda.current_stream().cuda_stream
     else:
+        torch.cuda.current_device()  # (initialises torch's side; after that its inner call is enough)
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
         def ask():
-            return raw(torch.cuda.current_device())
+            return raw(device())
     _current_stream = ask
     return ask()
 
