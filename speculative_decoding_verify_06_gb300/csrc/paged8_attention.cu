@@ -42,6 +42,28 @@ __device__ __forceinline__ void p8_mma_ss(uint32_t d, uint64_t a, uint64_t b, ui
         : "memory");
 }
 
+// As pa_wait(), with all but the first look out of line: the kernel's loops are short of instruction cache (a larger V loop
+// costs 200 requests of 2K a seventh).  (Not beside a register split, where the
+// compiler takes no calls, nor for fp32 outputs, which lost by it: 91 -> 106 us; bf16 262K 94.6 -> 93.0.)
+__device__ __noinline__ bool p8_wait_on(uint32_t bar, uint32_t parity, PaCtl *c) {
+    for (uint32_t left = c->limit; left; --left) {
+        if (mbar_poll(bar, parity, true)) return true;
+        if (pa_stopped(c)) return false;
+    }
+    if (!pa_stopped(c)) {
+        *reinterpret_cast<volatile uint32_t *>(&c->stop) = 1u;
+        atomicOr(c->status, 1u);
+    }
+    return false;
+}
+template <bool kInline>
+__device__ __forceinline__ bool p8_wait(uint32_t bar, uint32_t parity, PaCtl *c) {
+    if (kInline) return pa_wait(bar, parity, c);
+    bool ok = mbar_poll(bar, parity, true);
+    if (!__all_sync(~0u, ok)) ok = __all_sync(~0u, ok || p8_wait_on(bar, parity, c));
+    return ok;
+}
+
 // n (4 or 8) columns of a warp's lanes.
 template <int n>
 __device__ __forceinline__ void p8_ld(uint32_t t, float *f) {
@@ -213,6 +235,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         for (int i = 0; i < kP8Ring; ++i) mbar_init(b_seg + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    for (int i = tid; i < RP; i += kThreads) s_nref[i] = 0.f;
     if (tid < kP8Ring) {
         s_info[tid] = PaTileInfo{};
         s_seg[tid] = P8Seg{};
@@ -286,7 +309,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
     auto phase = [](uint32_t t, uint32_t n) { return (t / n) & 1u; };
 
     if (warp < kCopyWarp) {  // the first segment's queries: the V and the softmax warps, which have nothing to do yet
-        if (pa_wait(b_seg, 0u, &s_ctl)) {
+        if (p8_wait<Cfg::kSplit || F32>(b_seg, 0u, &s_ctl)) {
             const P8Seg g = s_seg[0];
             constexpr int kWarps = kCopyWarp, kEach = (RP / 2 + kWarps - 1) / kWarps;
             if (2 * warp + 2 * kWarps * (kEach - 1) < RP) p8_queries<RP, kEach>(A, g, 2 * warp, 2 * kWarps, s_q, s_qs[0], lane);
@@ -362,7 +385,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
                 const int tile = u - s0;
                 const int pg_next = u + 1 < end ? lookup(tile + 1) : -1;
                 // a wait that gave up ends the copies: no descriptor in use is overwritten
-                if (k >= A.stages && !pa_wait(b_empty + 8 * st, st_phase ^ 1u, &s_ctl)) {
+                if (k >= A.stages && !p8_wait<Cfg::kSplit || F32>(b_empty + 8 * st, st_phase ^ 1u, &s_ctl)) {
                     end = u = hi;
                     break;
                 }
@@ -405,10 +428,10 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         int st = 0;
         uint32_t st_phase = 0, n_seg = 0;
         for (uint32_t t = 0; t < count; ++t) {
-            pa_wait(b_full + 8 * st, st_phase, &s_ctl);
+            p8_wait<Cfg::kSplit || F32>(b_full + 8 * st, st_phase, &s_ctl);
             const uint32_t flags = s_info[t % kP8Ring].flags;
-            if (flags & 1u) pa_wait(n_seg ? b_q + 8 * (n_seg & 1) : b_q0, n_seg ? phase(n_seg - (~n_seg & 1u), 2) : 0u, &s_ctl);
-            if (t >= SB) pa_wait(b_sf + 8 * (t % SB), phase(t - SB, SB), &s_ctl);
+            if (flags & 1u) p8_wait<Cfg::kSplit || F32>(n_seg ? b_q + 8 * (n_seg & 1) : b_q0, n_seg ? phase(n_seg - (~n_seg & 1u), 2) : 0u, &s_ctl);
+            if (t >= SB) p8_wait<Cfg::kSplit || F32>(b_sf + 8 * (t % SB), phase(t - SB, SB), &s_ctl);
             if (lane == 0) {
                 pa_fence_after();
                 const uint64_t q = q0 + (n_seg & 1) * (Cfg::kQ / 16), ka = k0 + st * (kP8StageK / 16);
@@ -435,7 +458,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         // ---- O += V^T P^T ------------------------------------------------------------------
         const uint64_t p0 = pa_desc_p(smem_u32(s_p));
         for (uint32_t t = 0; t < count; ++t) {
-            pa_wait(b_o + 8 * (t & 1), phase(t, 2), &s_ctl);
+            p8_wait<Cfg::kSplit || F32>(b_o + 8 * (t & 1), phase(t, 2), &s_ctl);
             const uint32_t first = s_info[t % kP8Ring].flags & 1u;
             if (lane == 0) {
                 pa_fence_after();
@@ -462,11 +485,11 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         for (uint32_t n = 0; done < count; ++n) {
             const int si = n % kP8Ring;
             // a wait that gave up: the segment may not be there
-            if (!pa_wait(b_seg + 8 * si, phase(n, kP8Ring), &s_ctl)) break;
+            if (!p8_wait<Cfg::kSplit || F32>(b_seg + 8 * si, phase(n, kP8Ring), &s_ctl)) break;
             const P8Seg g = s_seg[si];
             done += g.tiles;
             if (n == 0) continue;
-            if (n >= 2) pa_wait(b_qfree + 8 * (n & 1), phase(n - 2, 2), &s_ctl);
+            if (n >= 2) p8_wait<Cfg::kSplit || F32>(b_qfree + 8 * (n & 1), phase(n - 2, 2), &s_ctl);
             uint8_t *const q = s_q + (n & 1) * Cfg::kQ;
             constexpr int kDeep = RP / 2 < 8 ? RP / 2 : 4;
             for (int i = 0; i < RP / 2; i += kDeep) p8_queries<RP, kDeep>(A, g, 2 * i, 2, q, s_qs[n & 3], lane);
@@ -481,12 +504,12 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         int st = 0;
         uint32_t st_phase = 0;
         for (uint32_t t = 0; t < count; ++t) {
-            pa_wait(b_full + 8 * st, st_phase, &s_ctl);
+            p8_wait<Cfg::kSplit || F32>(b_full + 8 * st, st_phase, &s_ctl);
             const uint32_t mask = s_info[t % kP8Ring].mask;
             const int n_pos = s_info[t % kP8Ring].n_pos;
             const bool whole = mask == 0xFFu && n_pos >= kPaTile;
             const int vb = t % VB;
-            if (t >= VB) pa_wait(b_vfree + 8 * vb, phase(t - VB, VB), &s_ctl);
+            if (t >= VB) p8_wait<Cfg::kSplit || F32>(b_vfree + 8 * vb, phase(t - VB, VB), &s_ctl);
             pa_fence_after();
             const uint32_t col = tmem + quarter + Cfg::kColV + 64 * vb;
 #pragma unroll 2
@@ -541,7 +564,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
             if (mbar_poll(b_full + 8 * st, st_phase, true)) got |= 2u;
             if (t < Cfg::PB || mbar_poll(b_pv + 8 * ((t - Cfg::PB) & 1), phase(t - Cfg::PB, 2), false)) got |= 4u;  // P is read
             got = __reduce_and_sync(~0u, got);
-            if ((got & 3u) != 3u && (!pa_wait(b_s + 8 * (t % SB), phase(t, SB), &s_ctl) || !pa_wait(b_full + 8 * st, st_phase, &s_ctl)))
+            if ((got & 3u) != 3u && (!p8_wait<Cfg::kSplit || F32>(b_s + 8 * (t % SB), phase(t, SB), &s_ctl) || !p8_wait<Cfg::kSplit || F32>(b_full + 8 * st, st_phase, &s_ctl)))
                 s_quit[sg][t & 1] = 1;
             const PaTileInfo ti = s_info[t % kP8Ring];
             const bool first = ti.flags & 1u, last = ti.flags & 2u;
@@ -605,13 +628,13 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
             // s = score + log2 of V's scale - reference, in powers of two.
 #pragma unroll
             for (int j = 0; j < RG / 2; j += 2) {
-                ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_nref + rb + 2 * j);
-                if (first) r.x = r.y = 0ull;
+                const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_nref + rb + 2 * j);  // (0 where a segment begins)
                 s[j] = pa_fma2(s[j], c2, pa_add2(r.x, lv2));
                 s[j + 1] = pa_fma2(s[j + 1], c2, pa_add2(r.y, lv2));
             }
             // What a row does not see is cut out (its first row sees the fewest positions).
             if (ti.mask != 0xFFu || (ti.tile + 1) * kPaTile > whole_to) {
+                asm volatile("");  // (a branch, and not a selection for every score of every tile)
                 const int pos = ti.tile * kPaTile + gt;
                 const bool here = ((ti.mask >> (gt >> 4)) & 1u) && pos < len;
                 // row j is token tok + (off + j) / G: it sees the position once j reaches this (a
@@ -685,7 +708,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
                         l[j] = pa_mul2(l[j], f);
                     }
                     if (!F32) {
-                        pa_wait(b_pv + 8 * ((t - 1) & 1), phase(t - 1, 2), &s_ctl);
+                        p8_wait<Cfg::kSplit || F32>(b_pv + 8 * ((t - 1) & 1), phase(t - 1, 2), &s_ctl);
                         pa_fence_after();
 #pragma unroll
                         for (int j = 0; j < RG; j += kStep) {
@@ -701,7 +724,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
                     }
                 }
             }
-            if (!(got & 4u)) pa_wait(b_pv + 8 * ((t - Cfg::PB) & 1), phase(t - Cfg::PB, 2), &s_ctl);  // P is read
+            if (!(got & 4u)) p8_wait<Cfg::kSplit || F32>(b_pv + 8 * ((t - Cfg::PB) & 1), phase(t - Cfg::PB, 2), &s_ctl);  // P is read
             if (F32 && !first) {
                 pa_fence_after();
 #pragma unroll
@@ -785,9 +808,10 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
                     s_max[0][row] = (g.token0 + tok) * A.Hq + g.head0 + rr - tok * A.G;
                     if (slot >= 0 && row < rows)
                         A.part_ml[(int64_t)slot * RP + row] = make_float2(seen ? -s_nref[row] : -INFINITY, sum);
+                    s_nref[row] = 0.f;  // for the next segment
                 }
                 group_sync();
-                pa_wait(b_pv + 8 * (t & 1), phase(t, 2), &s_ctl);
+                p8_wait<Cfg::kSplit || F32>(b_pv + 8 * (t & 1), phase(t, 2), &s_ctl);
                 pa_fence_after();
                 float o[RG];
 #pragma unroll
