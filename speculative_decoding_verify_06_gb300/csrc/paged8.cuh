@@ -36,11 +36,6 @@ __device__ __forceinline__ uint32_t p8_encode2(float a, float b) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
     return r;
 }
-__device__ __forceinline__ uint32_t p8_encode2_e5m2(float a, float b) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-    return r;
-}
 __device__ __forceinline__ uint32_t p8_decode2(uint32_t codes) {  // a pair of fp16, exact
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));

@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(256) paged8_join_kernel(const __grid_constant_
     if (tid == 0) s_first = -1;
     griddep_wait();
     griddep_launch_dependents();
-    // (at most 512 CTAs: two to an SM)
+    // (at most 512 CTAs)
     P8Split x[2] = {};
     uint32_t there[2];
 #pragma unroll
@@ -966,7 +966,8 @@ static int p8_launch(PaArgs A, P8Split *splits, int sms, cudaStream_t stream) {
     const int64_t by_request = (int64_t)A.R * (((int64_t)most_new * A.G + RP - 1) / RP), by_rows = ((int64_t)A.T * A.G + RP - 1) / RP + A.R;
     const int64_t row_tiles = A.Hkv * (by_request < by_rows ? by_request : by_rows);
     const int64_t tiles = row_tiles * (((int64_t)A.width * A.page + kPaTile - 1) / kPaTile);
-    const int grid = (int)(tiles < Cfg::kCtas * sms ? tiles : Cfg::kCtas * sms);
+    const int most_ctas = Cfg::kCtas * sms < 512 ? Cfg::kCtas * sms : 512;  // (what the join looks through)
+    const int grid = (int)(tiles < most_ctas ? tiles : most_ctas);
     SVD_CUDA_TRY((allow_smem<paged8_attention_kernel<RP, F32>>(most)));
     // A register split above what the launch has would wait forever: refuse to launch one.
     static std::atomic<int> regs{0};

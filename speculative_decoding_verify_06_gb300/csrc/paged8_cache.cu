@@ -16,7 +16,7 @@
 //
 // Codes.  A key next to the border of two codes must get the code that exact arithmetic gives, or the cache
 // would depend on how the angle was rounded.  Rotated keys are worked out in plain fp32, with an error below
-// 2.5 * 2^-24 (|x_a| + |x_b|); a code is settled where the key plus and minus that bound (the largest of a lane) round alike.  Else (in
+// 2.6 * 2^-24 (|x_a| + |x_b|) (cos and sin are off by 2^-25 and 2^-28, the product and the sum by 2^-24); a code is settled where the key plus and minus that bound (the largest of a lane) round alike.  Else (in
 // about one of a hundred heads of a token) the warp works the key out as a sum of two floats good to 2^-27 (|x_a| + |x_b|), as the 4-bit append
 // does for all, and decides by the distance from the border between the two codes; where that is within the
 // bound still, in fp64.  The scale likewise.  Values and dimensions that do not turn are exact as they come.
@@ -29,7 +29,7 @@ constexpr int kA8Warps = 8;
 constexpr int kA8Threads = 32 * kA8Warps;
 constexpr int kA8Pos = 8;                  // positions of a warp
 constexpr int kA8Low = 16 * SVD_ROPE_MAX_PAIRS;
-constexpr float kA8Err = 2.5f * 0x1p-24f;  // of a rotated key, against |x_a| + |x_b|
+constexpr float kA8Err = 3.f * 0x1p-24f;   // of a rotated key, against |x_a| + |x_b|
 
 struct A8Args {
     const void *qkv;

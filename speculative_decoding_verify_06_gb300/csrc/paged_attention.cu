@@ -772,6 +772,102 @@ paged_attention_kernel(const __grid_constant__ PaArgs A) {
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Cfg::kCols) : "memory");
 }
+// Joins the segments of a row that several CTAs hold: W warps per (token, query head), each over
+// every W-th segment, all of its loads in flight together.  What the requests' lengths alone decide
+// is worked out before the main kernel's end is waited for (the lengths were complete before it began).
+template <int RP, bool F32, int W>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) paged_merge_kernel(const __grid_constant__ PaArgs A, int ctas) {
+    constexpr int kRows = W == 1 ? 4 : 1;  // rows of a CTA
+    __shared__ float4 s_acc[W][32];
+    __shared__ float2 s_ml[W];
+    const int lane = threadIdx.x & 31, wj = W == 1 ? 0 : threadIdx.x >> 5;
+    const int64_t w = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x >> 5 : 0);
+    const int t = (int)(w / A.Hq), head = (int)(w - (int64_t)t * A.Hq);
+    int r = 0, b = A.R;
+    const bool there = t < A.T && t < A.q_start[A.R];
+    while (b - r > 1) {
+        const int mid = (r + b) >> 1;
+        if (A.q_start[mid] <= t) r = mid; else b = mid;
+    }
+    const PaReq x = pa_req(A, r);
+    const int i = t - x.q0;
+    const int h = head / A.G, rr = i * A.G + head - h * A.G, rt = rr / RP, row = rr - rt * RP;
+    int before = 0, nt = 0;
+    const bool mine = there && i >= 0 && i < x.n;
+    if (mine) {
+        for (int j = 0; j < rt; ++j) before += pa_row_tiles<RP>(A, x, j);
+        nt = pa_row_tiles<RP>(A, x, rt);
+    }
+    // A finite query that fp16 does not hold makes its row NaN and is reported (here, where it costs nothing:
+    // with the check at the main kernel's fetch of the queries, 262K took 94.7 us instead of 91.3).
+    bool far = false;
+    if (mine && wj == 0) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(A.q + w * kPgDim + 4 * lane);
+        const uint32_t m = __vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), m1 = max(m & 0xFFFFu, m >> 16);
+        far = m1 >= 0x4780u && m1 < 0x7F80u;  // 65536 .. the largest
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (far) atomicOr(A.status, 2u);
+    if (!mine) return;  // (the same for all warps of a row)
+    const int n_tiles = A.prefix[A.R], pre = A.prefix[r], per = (A.prefix[r + 1] - pre) / A.Hkv;
+    if (n_tiles == 0) return;
+    const int s0 = pre + h * per + before;
+    const int f = pa_cta_of(n_tiles, ctas, s0), e = pa_cta_of(n_tiles, ctas, s0 + nt - 1);
+    if (f == e) return;
+    // (ref, sum, acc) += (r, l, o), a part that saw nothing (r = -inf) left out.
+    float ref = -INFINITY, sum = 0.f;
+    float4 acc = {0.f, 0.f, 0.f, 0.f};
+    auto join = [&](float r1, float l1, const float4 &o1) {
+        if (r1 == -INFINITY) return;
+        const float top = ref > r1 ? ref : r1;  // (NaN: r1)
+        const float k0 = ref == -INFINITY ? 0.f : pa_ex2(ref - top), k1 = pa_ex2(r1 - top);
+        sum = sum * k0 + l1 * k1;
+        acc.x = acc.x * k0 + o1.x * k1;
+        acc.y = acc.y * k0 + o1.y * k1;
+        acc.z = acc.z * k0 + o1.z * k1;
+        acc.w = acc.w * k0 + o1.w * k1;
+        ref = top;
+    };
+    for (int c0 = f + wj; c0 <= e; c0 += 8 * W) {
+        float4 o[8];
+        float2 ml[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = c0 + j * W;
+            ml[j] = make_float2(-INFINITY, 0.f);
+            if (c <= e) {
+                const int64_t slot = (int64_t)(c == f ? 2 * f + 1 : 2 * c) * RP + row;
+                ml[j] = A.part_ml[slot];
+                o[j] = *reinterpret_cast<const float4 *>(A.part + slot * kPgDim + 4 * lane);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) join(ml[j].x, ml[j].y, o[j]);
+    }
+    if (W > 1) {
+        s_acc[wj][lane] = acc;
+        if (lane == 0) s_ml[wj] = make_float2(ref, sum);
+        __syncthreads();
+        if (wj) return;
+#pragma unroll
+        for (int j = 1; j < W; ++j) join(s_ml[j].x, s_ml[j].y, s_acc[j][lane]);
+    }
+    const float inv = ref == -INFINITY ? 0.f : 1.f / sum;
+    const int64_t at = w * kPgDim + 4 * lane;
+    if (F32) {
+        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(A.out) + at) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 q = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        uint2 v;
+        v.x = reinterpret_cast<const uint32_t &>(p);
+        v.y = reinterpret_cast<const uint32_t &>(q);
+        *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(A.out) + at) = v;
+    }
+}
+
 template <int RP, bool F32>
 static int pa_launch(PaArgs A, int sms, cudaStream_t stream) {
     using Cfg = PaCfg<RP, F32>;
@@ -790,7 +886,13 @@ static int pa_launch(PaArgs A, int sms, cudaStream_t stream) {
     }
     if (Cfg::kSplit && regs.load(std::memory_order_relaxed) < Cfg::kRegs) return SVD_ERR_UNSUPPORTED;
     SVD_CUDA_TRY(launch(paged_attention_kernel<RP, F32>, dim3(grid), dim3(Cfg::kThreads), smem, stream, true, A));
-    return pa_merge<RP, F32, true>(A, grid, stream);
+    // Few rows are split over many CTAs each, and then eight warps join one; many rows over few.
+    const int64_t rows = (int64_t)A.T * A.Hq;
+    if (rows <= 2048)
+        SVD_CUDA_TRY(launch(paged_merge_kernel<RP, F32, 8>, dim3((unsigned)rows), dim3(256), 0, stream, true, A, grid));
+    else
+        SVD_CUDA_TRY(launch(paged_merge_kernel<RP, F32, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, true, A, grid));
+    return SVD_OK;
 }
 size_t paged_attention_ws_bytes(int Hq, int Hkv, int R, int max_new) {
     return pa_ws_bytes(Hq, Hkv, R, max_new, sm_count());

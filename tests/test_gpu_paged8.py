@@ -195,6 +195,33 @@ def test_append_reports_what_is_not_finite_and_positions_without_a_page():
         assert not np.isin(got[..., :4096] % 128, 127).any()
 
 
+@pytest.mark.parametrize("dtype", [svd.SVD_F32, svd.SVD_BF16])
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_rotates_what_is_not_finite_as_the_formula_says(dtype, inter):
+    """NaN, infinities and magnitudes up to fp32's largest among rotated keys, and among values; beside them ordinary tokens."""
+    g = np.random.default_rng(31)
+    T, H = 80, 3
+    x = as_type(g.normal(0, 1, (T, 2 * H, 128)).astype(np.float32), dtype).float().numpy()
+    odd = np.array([np.nan, np.inf, -np.inf, 1e30, -3e38, 60000.0, 1e-40, 0.0, -0.0], np.float32)
+    for t in range(0, T, 3):
+        for _ in range(4):
+            x[t, g.integers(0, 2 * H), g.integers(0, 128)] = odd[g.integers(0, len(odd))]
+    x = as_type(x, dtype).float().numpy()
+    pos = g.integers(0, 1000, (1, T))
+    pos[0, ::7] = 0
+    inv = 100.0 ** (-np.arange(32) / 32)
+    lens, new = [T, 9], [T - 9, 9]
+    table, q_start, n_pages = layout(lens, new, 32, g)
+    pool = random_pool(g, n_pages, H, 32)
+    _, got, st = gpu_append(x, dtype, 0, H, lens, q_start, table, pool, 32, rope=svd.Rope(inv, interleaved=inter), positions=pos)
+    with np.errstate(invalid="ignore", over="ignore"):
+        y = paged.rotate(x.astype(np.float64), pos, inv, [0] * 32, inter)
+    want = pool.copy()
+    paged8.append(want, y[:, :H], x[:, H:], lens, q_start, table, 32)
+    assert np.array_equal(same_zeros(got), same_zeros(want))
+    assert np.array_equal(st, np.where(np.isfinite(x).all((1, 2)), 0, paged8.NONFINITE))
+
+
 @pytest.mark.parametrize("T", [40, 700])
 def test_rows_behind_the_last_request_are_left_alone(T):
     g = np.random.default_rng(T)
@@ -310,7 +337,7 @@ BOTH = pytest.mark.parametrize("out_dtype", [svd.SVD_BF16, svd.SVD_F32])
 
 
 @BOTH
-@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (8, 1), (10, 2), (13, 1), (24, 2), (32, 1), (40, 1)])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (8, 1), (10, 2), (13, 1), (24, 2), (32, 1), (40, 1), (70, 70)])
 @pytest.mark.parametrize("new", [1, 4])
 def test_attention_heads(out_dtype, Hq, Hkv, new):
     c = Case([70, 200], [new, new], Hq, Hkv, 32, seed=Hq)
@@ -354,6 +381,14 @@ def test_attention_many_requests():
     c.check(svd.SVD_BF16, c.run(svd.SVD_BF16), c.reference())
     c = Case([20] * 4096, [1] * 4096, 1, 1, 16, seed=6)
     c.check(svd.SVD_BF16, c.run(svd.SVD_BF16), c.reference())
+
+
+@BOTH
+def test_many_row_tiles_split_between_two_ctas(out_dtype):
+    g = np.random.default_rng(22)
+    lens = g.integers(300, 900, 95).tolist()
+    c = Case(lens, [1] * 95, 4, 4, 64, seed=23)
+    c.check(out_dtype, c.run(out_dtype), c.reference())
 
 
 @BOTH
