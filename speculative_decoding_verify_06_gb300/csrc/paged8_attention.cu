@@ -23,6 +23,17 @@
 //
 // Rows a mask leaves empty get zeros.  Positions past the length, or on a page outside the pool, are cut out
 // of S, and their V codes are replaced by 0, whatever their bytes.
+//
+// What bounds it (8 kv heads, 40 query heads, times in a graph, of a measured copy rate of 6686 GB/s).  For windows,
+// memory: 539 MB at 262K take 93 us (0.86; 6.4 TB/s once going), 64 ragged requests of up to 16K 220 us (0.86), 200 short ones with
+// fp32 outputs 92 us (0.74).  Some 10 us do not depend on the length: a launch, the first tile's way through copy, products and
+// softmax, and the join; one token behind 1500 positions takes 9.0 us, 32K positions 20.6.  Issue stands at 60 % there.
+// For chunks of 512 tokens (128-row tiles), 143 GFLOP in 300 us, a fourth of the product rate: about 5000 cycles a tile of
+// 128 x 128, in which S of the next tile, V's conversion, softmax and O follow one another through one P buffer, issue
+// 50 %, tensor pipe 22 %.  Copies with most of the exponentials, P's stores, V's conversion or either product
+// left out took 300 to 308 us: no one of them is the bound.  Tried and slower there: groups with barriers of their
+// own (335), scalar softmax (346), row tiles of 96 (378), 64 rows to a lane (297 to 320), the queries' parts as two products into the
+// same columns, the second in e5m2 (300; 386 with one exponent for a tile's rows and two buffers of S).
 #include "paged8.cuh"
 #include "paged_attention.cuh"
 

