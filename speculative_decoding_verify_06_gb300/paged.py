@@ -130,7 +130,7 @@ class PagedBatch:
         svd.svd_paged_fork(self.held[a], self._window[a], emitted, parent, self.R, self.page, self.table[a], self.width, self.free[a],
                            self.n_free[a], self.n_pages, self.held[b], self._window[b], self.table[b], self.free[b], self.n_free[b],
                            self._copy_from, self._copy_to, self._n_copies, self.fork_status, stream=stream)
-        svd.svd_paged_copy(self._layers, self.n_pages, self._copy_from, self._copy_to, self._n_copies, self.n_pages, stream=stream)
+        self._copy(stream)
         with self._on(stream):
             self._state[a].copy_(self._state[b])
         return self.fork_status
@@ -141,10 +141,19 @@ class PagedBatch:
         a, b = self.now, 1 - self.now
         svd.svd_paged_compact(self.held[a], self.R, self.page, self.table[a], self.width, self.n_pages, self.table[b], self.free[b],
                               self.n_free[b], self._copy_from, self._copy_to, self._n_copies, stream=stream)
-        svd.svd_paged_copy(self._layers, self.n_pages, self._copy_from, self._copy_to, self._n_copies, self.n_pages, stream=stream)
+        self._copy(stream)
         pages = self.R * self.width + self.n_pages + 1  # the table, the stack and its count: the lengths stay
         with self._on(stream):
             self._state[a][:pages].copy_(self._state[b][:pages])
+
+    def _copy(self, stream):
+        if len(self.pools) != len(self._layers) or any(a is not b for a, b in zip(self.pools, self._layers.pools)):
+            for p in self.pools:  # (another tensor in the list, a cache that was kept elsewhere)
+                self._here("pools", p, torch.uint8)
+                if not p.is_contiguous() or p.numel() != self.n_pages * self._layers.page_bytes:
+                    raise ValueError(f"pools: {self.n_pages * self._layers.page_bytes} bytes in one piece, got {tuple(p.shape)}")
+            self._layers = svd.Pools(self.pools, self._layers.page_bytes)
+        svd.svd_paged_copy(self._layers, self.n_pages, self._copy_from, self._copy_to, self._n_copies, self.n_pages, stream=stream)
 
     def _on(self, stream):
         if stream is None:

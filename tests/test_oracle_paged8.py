@@ -46,7 +46,7 @@ def test_append_and_get():
     x[0, 0, :3] = 3000.0, 0.0, 0.0
     assert paged8.append(pool, x, x, [2], [0, 1], table, 32) == []
     k, v = paged8.get(pool, [32, 33], 32)
-    assert k[0, 0, :3].tolist() == [1.0, -0.3125, 448.0] and k[1, 0, 0] == 3072.0
+    assert k[0, 0, :3].tolist() == [1.0, -0.3125, 448.0] and k[1, 0, 0] == 384.0 * 8
     x[0, 0, :3] = 50000.0, 0.0, 0.0
     paged8.append(pool, x, x, [3], [0, 1], table, 32)
     k, _ = paged8.get(pool, [32], 32)

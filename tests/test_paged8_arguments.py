@@ -157,6 +157,27 @@ def test_fork_and_compact_copy_whole_pages_of_all_layers(calls, bits):
             assert a["copy_from"] is b._copy_from and a["copy_to"] is b._copy_to and a["n_copies"] is b._n_copies
 
 
+def test_copies_go_to_the_pools_that_the_layers_use(calls):
+    """A pool that takes another's place in the list is the one that a fork and a compaction copy."""
+    b = batch()
+    b.pools[1] = torch.zeros_like(b.pools[1])
+    b.fork(torch.zeros(3, dtype=torch.int32))
+    b.compact()
+    copies = [a["pools"] for n, a in calls if n == "svd_paged_copy"]
+    assert len(copies) == 2 and all(c.pools[i] is b.pools[i] and c._a[i] == b.pools[i].data_ptr() for c in copies for i in (0, 1))
+
+
+@pytest.mark.parametrize("pool", [torch.zeros(12 * 2 * 4112 - 1, dtype=torch.uint8), torch.zeros(12 * 2 * 4112),
+                                  torch.zeros(2 * 12 * 2 * 4112, dtype=torch.uint8)[::2],
+                                  torch.zeros(12 * 2 * 4112, dtype=torch.uint8, device="meta")])
+def test_pools_of_another_form_are_not_copied(calls, pool):
+    b = batch()
+    b.pools[0] = pool
+    with pytest.raises(ValueError, match="pools"):
+        b.compact()
+    assert "svd_paged_copy" not in [n for n, _ in calls]
+
+
 @pytest.mark.parametrize("parent", [torch.ones(3, dtype=torch.int64), torch.ones(2, dtype=torch.int32), torch.ones(3),
                                     torch.ones(6, dtype=torch.int32)[::2], torch.ones((3, 1), dtype=torch.int32),
                                     torch.ones(3, dtype=torch.int32, device="meta")])
