@@ -26,12 +26,12 @@
 //
 // What bounds it (8 kv heads, 40 query heads, times in a graph, of a measured copy rate of 6686 GB/s).  For windows,
 // memory: 539 MB at 262K take 93 us (0.86; 6.4 TB/s once going), 64 ragged requests of up to 16K 220 us (0.86), 200 short ones with
-// fp32 outputs 92 us (0.74).  Some 10 us do not depend on the length: a launch, the first tile's way through copy, products and
+// fp32 outputs 90 us (0.76).  Some 10 us do not depend on the length: a launch, the first tile's way through copy, products and
 // softmax, and the join; one token behind 1500 positions takes 9.0 us, 32K positions 20.6.  Issue stands at 60 % there.
-// For chunks of 512 tokens (128-row tiles), 143 GFLOP in 300 us, a fourth of the product rate: about 5000 cycles a tile of
+// For chunks of 512 tokens (128-row tiles), 143 GFLOP in 296 us, a fourth of the product rate: about 5000 cycles a tile of
 // 128 x 128, in which S of the next tile, V's conversion, softmax and O follow one another through one P buffer, issue
 // 50 %, tensor pipe 22 %.  Copies with most of the exponentials, P's stores, V's conversion or either product
-// left out took 300 to 308 us: no one of them is the bound.  Tried and slower there: groups with barriers of their
+// left out took 300 to 308 us of 308 then: no one of them is the bound.  Tried and slower there: groups with barriers of their
 // own (335), scalar softmax (346), row tiles of 96 (378), 64 rows to a lane (297 to 320), the queries' parts as two products into the
 // same columns, the second in e5m2 (300; 386 with one exponent for a tile's rows and two buffers of S).
 #include "paged8.cuh"
@@ -252,15 +252,20 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         s_seg[tid] = P8Seg{};
         if (tid < 2 * Cfg::kGroups) s_quit[tid >> 1][tid & 1] = 0;
     }
-    // (before the wait: the kernel ahead on the stream has none, or has ended)
-    if (warp == 0) {
+    griddep_wait();
+    griddep_launch_dependents();
+    // Not before the wait: a kernel ahead that lets this one start before it has its own tensor memory would wait for this
+    // one's, and this one for its end.  By the warp that has nothing to do yet; with a register split by the first one, after the scan, where
+    // it leaves the scan fewer spills (chunks 317 -> 295 us; windows lose by that: 32K 20.7 -> 22.1).
+    constexpr int kTmemWarp = Cfg::kSplit ? 0 : kOWarp + 1;
+    auto take_tmem = [&]() {
+        if (warp != kTmemWarp) return;
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                      "r"(Cfg::kCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    griddep_wait();
-    griddep_launch_dependents();
+    };
+    if (!Cfg::kSplit) take_tmem();
 
     // Tiles before every request.
     const uint32_t lim = tid ? 0u : reinterpret_cast<volatile uint32_t *>(A.status)[1];
@@ -291,6 +296,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         if (r < A.R) s_pre[r] = n_tiles + v - mine;
         n_tiles += all;
     }
+    if (Cfg::kSplit) take_tmem();
     if (tid == 0) {
         s_pre[A.R] = n_tiles;
         s_ctl.stop = 0u;
@@ -301,7 +307,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
     const int lo = pa_lo(n_tiles, gridDim.x, blockIdx.x), hi = pa_lo(n_tiles, gridDim.x, blockIdx.x + 1);
     if (n_tiles == 0 || hi <= lo) {
         if (tid == 0) splits[blockIdx.x].rows = 0;
-        if (warp == 0)
+        if (warp == kTmemWarp)
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "r"(Cfg::kCols) : "memory");
         return;
     }
@@ -864,7 +870,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
     pa_fence_before();
     __syncthreads();
     pa_fence_after();
-    if (warp == 0)
+    if (warp == kTmemWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Cfg::kCols) : "memory");
 }
 

@@ -234,3 +234,64 @@ def test_demo(bits, samples):
     assert len(kept) == 4 and not b.status.any() and not b.bad.any() and not b.fork_status.any()
     assert all(np.all(np.diff([k[r] for k in kept]) >= 1) for r in range(8))
     assert int(b.attention_status) == 0
+
+
+def test_attention_right_behind_kernels_that_hold_tensor_memory():
+    """A product on the tensor cores, and another attention, directly ahead on the stream, launched and replayed: an attention takes its
+    tensor memory once they have ended, and all results are as they are apart."""
+    from speculative_decoding_verify_06_gb300 import stack
+    g = torch.Generator(device=DEV)
+    g.manual_seed(7)
+    lin = stack.Linear(1024, 2048, 32, 3, torch.device(DEV))
+    ws = torch.zeros(svd.svd_verify_linear_workspace_bytes(1024, 2048, 32), dtype=torch.uint8, device=DEV)
+    Hq, Hkv, page, n_pages, R = 20, 4, 64, 64, 2
+    pool = torch.randint(0, 0x70, (svd.svd_paged8_cache_bytes(Hkv, page, n_pages),), dtype=torch.uint8, generator=g, device=DEV)
+    pool.view(-1, svd.SVD_PAGED8_UNIT_BYTES)[:, 4096:4104] = torch.tensor([0, 0, 0, 0x3A] * 2, dtype=torch.uint8, device=DEV)  # 2^-11
+    table = torch.randperm(n_pages, generator=g, device=DEV).to(torch.int32).reshape(R, -1)
+    runs = []
+    for new in (4, 40, 13):  # row tiles that leave room for the product's kernel beside them, and that take a whole SM
+        T = R * new
+        q = torch.randn((T, Hq, 128), generator=g, device=DEV).to(torch.bfloat16)
+        out = torch.zeros((T, Hq, 128), dtype=torch.bfloat16, device=DEV)
+        aw = torch.zeros(svd.svd_paged8_attention_workspace_bytes(Hq, Hkv, R, new), dtype=torch.uint8, device=DEV)
+        runs.append((q, T, i32([2048, 1999]), i32([0, new, T]), new, out, aw))
+
+    def product():
+        svd.svd_verify_linear(lin.W, lin.X, 32, lin.Y, ws, flags=svd.SVD_F_PDL)
+
+    def attend(q, T, kv_len, q_start, new, out, aw):
+        svd.svd_paged8_attention(q, T, kv_len, q_start, R, new, table, table.shape[1], pool, page, n_pages, Hq, Hkv, 128 ** -0.5, out,
+                                 svd.SVD_BF16, aw)
+
+    product()
+    torch.cuda.synchronize()
+    want = [lin.Y.clone()]
+    for r in runs:
+        attend(*r)
+        torch.cuda.synchronize()
+        want.append(r[5].clone())
+
+    def all_of_them():
+        for r in runs:
+            product()
+            attend(*r)
+            attend(*r)
+
+    def same():
+        torch.cuda.synchronize()
+        assert torch.equal(lin.Y, want[0]) and all(torch.equal(r[5], w) for r, w in zip(runs, want[1:]))
+        assert not any(r[6][:4].any() for r in runs)
+
+    for _ in range(10):
+        all_of_them()
+    same()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            all_of_them()
+        for r in runs:
+            r[5].zero_()
+        for _ in range(10):
+            graph.replay()
+    same()
