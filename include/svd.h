@@ -553,7 +553,7 @@ int svd_paged_attention(const uint16_t *q, int n_tokens, const int32_t *kv_len,
  * svd_paged8_read: the values that the pool holds at slots[t] (page * page_size + offset), fp32 [T][Hkv][128] each (0
  *   for a slot outside the pool).
  * svd_paged8_attention: as svd_paged_attention, tokens, masks, outputs, workspace and errors alike.  A query row is used
- *   as a power of two times the sum of two e4m3 parts: exact for bf16 down to 2^-14 of the row's largest, and to 2^-22 of
+ *   as a power of two times the sum of two e4m3 parts (or one fp16 part, no worse): exact for bf16 down to 2^-14 of the row's largest, and to 2^-22 of
  *   it below; there is no bound on its magnitude.  A row with a query that is not finite is NaN.  The softmax's weights are
  *   used as fp16 (as two fp16 parts for fp32 outputs), and the sums are fp32.  Codes of positions before kv_len must be
  *   finite (svd_paged8_append writes no others); bytes of later ones may be anything, but for the scales of the units that hold

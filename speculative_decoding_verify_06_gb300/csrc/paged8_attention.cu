@@ -14,7 +14,8 @@
 // q = 2^e (hi + lo / 16), which stand side by side as columns of one product.  V becomes fp16 in tensor memory (a lane a
 // dimension, two positions a column; four warps), exactly, and O^T += V^T P^T runs on fp16 operands: turning 128 x 128
 // codes of V costs as much as splitting P of 24 rows into the three e4m3 parts that fp16's eleven bits fill, and less for
-// more rows.
+// more rows.  For 128 rows K goes the same way (a lane a position, two dimensions a column), against queries of one fp16
+// part under a power of two: half the columns of S to load, and room for all of it (chunks 296 -> 281 us; 64 rows lost by it, 132 -> 140).
 //
 // Softmax.  A lane holds one position of S for all rows, as in the 4-bit kernel, and the reference of a row moves
 // only when a score exceeds it by 15 (p <= 2^15 in between).  What is weighed is t = s + log2 sv(j): P = 2^(t - ref) then
@@ -26,14 +27,14 @@
 //
 // What bounds it (8 kv heads, 40 query heads, times in a graph, of a measured copy rate of 6686 GB/s).  For windows,
 // memory: 539 MB at 262K take 93 us (0.86; 6.4 TB/s once going), 64 ragged requests of up to 16K 220 us (0.86), 200 short ones with
-// fp32 outputs 90 us (0.76).  Some 10 us do not depend on the length: a launch, the first tile's way through copy, products and
+// fp32 outputs 90 to 93 us (0.75).  Some 10 us do not depend on the length: a launch, the first tile's way through copy, products and
 // softmax, and the join; one token behind 1500 positions takes 9.0 us, 32K positions 20.6.  Issue stands at 60 % there.
-// For chunks of 512 tokens (128-row tiles), 143 GFLOP in 296 us, a fourth of the product rate: about 5000 cycles a tile of
-// 128 x 128, in which S of the next tile, V's conversion, softmax and O follow one another through one P buffer, issue
-// 50 %, tensor pipe 22 %.  Copies with most of the exponentials, P's stores, V's conversion or either product
-// left out took 300 to 308 us of 308 then: no one of them is the bound.  Tried and slower there: groups with barriers of their
-// own (335), scalar softmax (346), row tiles of 96 (378), 64 rows to a lane (297 to 320), the queries' parts as two products into the
-// same columns, the second in e5m2 (300; 386 with one exponent for a tile's rows and two buffers of S).
+// For chunks of 512 tokens (128-row tiles), 143 GFLOP in 281 us, 0.26 of the product rate: some 4200 cycles a tile of
+// 128 x 128, in which four groups of softmax warps take turns with nothing but one another: issue 50 %, tensor pipe a fourth.
+// Copies with most of the exponentials, P's stores, V's conversion or either product left out took as long: no one of them is the
+// bound.  Tried and slower or no faster there: groups with barriers of their own (304 -> 335), scalar softmax (346), row tiles of 96 (378),
+// 64 rows to a lane (297 to 320), the queries' parts as two products into the same columns, the second in e5m2 (300), two buffers for
+// P beside two stages in place of three (296; prompts of 2048 391 -> 406), loads of S by fours, other register splits.
 #include "paged8.cuh"
 #include "paged_attention.cuh"
 
@@ -115,8 +116,9 @@ struct P8Seg {
     int tiles;                      // of this segment
 };
 
-// Query rows row0 + step i + (0, 1), i < n, of a segment: fetched, split and laid out by a warp, sixteen lanes to a row.
-template <int RP, int n>
+// Query rows row0 + step i + (0, 1), i < n, of a segment: fetched, split and laid out by a warp, sixteen lanes to a row; in two
+// e4m3 parts, or (kTurned) as fp16, 64 dimensions after 64: below 448, exact down to 2^-16.
+template <int RP, int n, bool kTurned>
 __device__ __forceinline__ void p8_queries(const PaArgs &A, const P8Seg &g, int row0, int step, uint8_t *q, float *qs, int lane) {
     const int ch = lane & 15;
     uint4 w[n];
@@ -142,12 +144,16 @@ __device__ __forceinline__ void p8_queries(const PaArgs &A, const P8Seg &g, int 
         const bool finite = top < 0x7F80u;
         const int e = max(p8_need(__uint_as_float(top << 16)), -118);
         const float inv = finite ? p8_pow2(-e) : 0.f;
-        uint32_t hi4[2], lo4[2];
+        uint32_t hi4[2], lo4[2], half4[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             // (0 where the row is not finite: its factor makes it NaN)
             const float a = finite ? __uint_as_float(ww[j] << 16) * inv : 0.f;
             const float b = finite ? __uint_as_float(ww[j] & 0xFFFF0000u) * inv : 0.f;
+            if (kTurned) {
+                half4[j] = pa_pack(a, b);
+                continue;
+            }
             const uint32_t c = p8_encode2(a, b);
             const float2 f = p8_floats2(c);
             const uint32_t d = p8_encode2((a - f.x) * 16.f, (b - f.y) * 16.f);  // at most 256
@@ -159,9 +165,14 @@ __device__ __forceinline__ void p8_queries(const PaArgs &A, const P8Seg &g, int 
                 lo4[j >> 1] = d;
             }
         }
-        uint8_t *const to = q + row * 128 + (((ch >> 1) ^ (row & 7)) * 16) + (ch & 1) * 8;
-        *reinterpret_cast<uint2 *>(to) = make_uint2(hi4[0], hi4[1]);
-        *reinterpret_cast<uint2 *>(to + RP * 128) = make_uint2(lo4[0], lo4[1]);
+        if (kTurned) {
+            *reinterpret_cast<uint4 *>(q + (ch >> 3) * (RP * 128) + row * 128 + (((ch & 7) ^ (row & 7)) * 16)) =
+                make_uint4(half4[0], half4[1], half4[2], half4[3]);
+        } else {
+            uint8_t *const to = q + row * 128 + (((ch >> 1) ^ (row & 7)) * 16) + (ch & 1) * 8;
+            *reinterpret_cast<uint2 *>(to) = make_uint2(hi4[0], hi4[1]);
+            *reinterpret_cast<uint2 *>(to + RP * 128) = make_uint2(lo4[0], lo4[1]);
+        }
         if (ch == 0) qs[row] = finite ? p8_pow2(e) : __int_as_float(0x7FC00000);
     }
 }
@@ -171,17 +182,18 @@ __device__ __forceinline__ void p8_queries(const PaArgs &A, const P8Seg &g, int 
 template <int RP, bool F32>
 struct P8Cfg {
     static constexpr int N = RP < 16 ? 16 : (RP + 15) / 16 * 16;
-    static constexpr int NS = 2 * RP;            // columns of S: both parts of the queries
+    static constexpr bool kTurned = RP == 128;   // K becomes fp16 in tensor memory, as V does
+    static constexpr int NS = kTurned ? RP : 2 * RP;  // columns of S: both parts of the queries, or the one
     static constexpr int NO = F32 ? 2 * RP : N;  // columns of O: for fp32 outputs P's two parts, rows j and RP + j
     static constexpr int kGroups = RP == 8 ? 1 : RP <= 32 ? 2 : 4, RG = RP / kGroups;  // softmax groups, rows of each
     static constexpr int kThreads = (4 + 4 * kGroups + 4) * 32;
     static constexpr int kCtas = RP <= (F32 ? 16 : 24) ? 2 : 1;  // per SM
     static constexpr uint32_t kCols = kCtas == 2 ? 256 : 512;
-    static constexpr int VB = 2, SB = 64 * VB + 2 * NS + NO <= (int)kCols ? 2 : 1;
-    static constexpr uint32_t kColV = 0, kColS = 64 * VB, kColO = kColS + SB * NS;
+    static constexpr int VB = 2, KB = kTurned ? 2 : 0, SB = 64 * (VB + KB) + 2 * NS + NO <= (int)kCols ? 2 : 1;
+    static constexpr uint32_t kColV = 0, kColK = 64 * VB, kColS = kColK + 64 * KB, kColO = kColS + SB * NS;
     static_assert(kColO + NO <= kCols && NS % 16 == 0 && NO % 16 == 0, "tensor memory");
     static constexpr int PB = F32 || RP == 128 ? 1 : 2;  // P buffers
-    static constexpr int kQ = NS * 128, kP = NO * 256;
+    static constexpr int kQ = 2 * RP * 128, kP = NO * 256;
     static constexpr size_t smem(int stages, int R) {
         return 1024 + (size_t)stages * (kP8StageK + kP8StageV) + 2 * kQ + PB * kP + ((size_t)R + 1) * 4;
     }
@@ -200,7 +212,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
     constexpr int NS = Cfg::NS, VB = Cfg::VB, SB = Cfg::SB, RG = Cfg::RG, kThreads = Cfg::kThreads;
     constexpr int kCopyWarp = 4 + 4 * Cfg::kGroups, kSWarp = kCopyWarp + 1, kOWarp = kCopyWarp + 2;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t s_bar[2 * kP8MaxStages + 18 + kP8Ring];
+    __shared__ __align__(8) uint64_t s_bar[2 * kP8MaxStages + 20 + kP8Ring];
     __shared__ PaTileInfo s_info[kP8Ring];
     __shared__ P8Seg s_seg[kP8Ring];
     __shared__ __align__(16) float s_nref[RP], s_del[RP], s_fac[RP], s_sum[4][RP], s_qs[4][RP];
@@ -226,11 +238,12 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
     const uint32_t b_q = b_sf + 80, b_qfree = b_sf + 96;        // queries of a segment there, read
     const uint32_t b_end = b_sf + 112, b_q0 = b_sf + 120;       // b_q0: those of the first segment
     const uint32_t b_seg = b_sf + 128;                          // segment descriptors (kP8Ring of them)
+    const uint32_t b_k = b_seg + 8 * kP8Ring, b_kfree = b_k + 16;  // K in tensor memory, read
 
     if (tid == 0) {
         for (int i = 0; i < A.stages; ++i) {
             mbar_init(b_full + 8 * i, 1);
-            mbar_init(b_empty + 8 * i, 5 + 4 * Cfg::kGroups);  // V's warps, S complete, the softmax warps (scales)
+            mbar_init(b_empty + 8 * i, (Cfg::kTurned ? 4 : 5) + 4 * Cfg::kGroups);  // K's and V's warps, S complete where it reads the stage, the softmax warps (scales)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_sf + 8 * i, 4 * Cfg::kGroups);
@@ -240,6 +253,8 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
             mbar_init(b_vfree + 8 * i, 1);
             mbar_init(b_q + 8 * i, 1);
             mbar_init(b_qfree + 8 * i, 1);
+            mbar_init(b_k + 8 * i, 4);
+            mbar_init(b_kfree + 8 * i, 1);
         }
         mbar_init(b_end, 2);
         mbar_init(b_q0, kCopyWarp);
@@ -319,7 +334,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
     const uint32_t tmem = s_tmem;
     const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
 
-    // S: NS columns of e4m3 products, both operands K-major; O: NO columns, P's rows the fast index
+    // S: NS columns of e4m3 or fp16 products, both operands K-major; O: NO columns, P's rows the fast index
     constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(NS >> 3) << 17) | (8u << 24);
     constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(Cfg::NO >> 3) << 17) | (8u << 24);
     // Tile t's phase of a barrier that counts the tiles of one of two buffers, or of n.
@@ -329,8 +344,8 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         if (p8_wait<Cfg::kSplit || F32>(b_seg, 0u, &s_ctl)) {
             const P8Seg g = s_seg[0];
             constexpr int kWarps = kCopyWarp, kEach = (RP / 2 + kWarps - 1) / kWarps;
-            if (2 * warp + 2 * kWarps * (kEach - 1) < RP) p8_queries<RP, kEach>(A, g, 2 * warp, 2 * kWarps, s_q, s_qs[0], lane);
-            else if (kEach > 1) p8_queries<RP, kEach - (kEach > 1)>(A, g, 2 * warp, 2 * kWarps, s_q, s_qs[0], lane);
+            if (2 * warp + 2 * kWarps * (kEach - 1) < RP) p8_queries<RP, kEach, Cfg::kTurned>(A, g, 2 * warp, 2 * kWarps, s_q, s_qs[0], lane);
+            else if (kEach > 1) p8_queries<RP, kEach - (kEach > 1), Cfg::kTurned>(A, g, 2 * warp, 2 * kWarps, s_q, s_qs[0], lane);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -445,7 +460,8 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         int st = 0;
         uint32_t st_phase = 0, n_seg = 0;
         for (uint32_t t = 0; t < count; ++t) {
-            p8_wait<Cfg::kSplit || F32>(b_full + 8 * st, st_phase, &s_ctl);
+            if (Cfg::kTurned) p8_wait<Cfg::kSplit || F32>(b_k + 8 * (t & 1), phase(t, 2), &s_ctl);
+            else p8_wait<Cfg::kSplit || F32>(b_full + 8 * st, st_phase, &s_ctl);
             const uint32_t flags = s_info[t % kP8Ring].flags;
             if (flags & 1u) p8_wait<Cfg::kSplit || F32>(n_seg ? b_q + 8 * (n_seg & 1) : b_q0, n_seg ? phase(n_seg - (~n_seg & 1u), 2) : 0u, &s_ctl);
             if (t >= SB) p8_wait<Cfg::kSplit || F32>(b_sf + 8 * (t % SB), phase(t - SB, SB), &s_ctl);
@@ -453,9 +469,16 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
                 pa_fence_after();
                 const uint64_t q = q0 + (n_seg & 1) * (Cfg::kQ / 16), ka = k0 + st * (kP8StageK / 16);
                 const uint32_t d = tmem + Cfg::kColS + NS * (t % SB);
+                if (Cfg::kTurned) {
+                    const uint32_t kt = tmem + Cfg::kColK + 64 * (t & 1);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) p8_mma_ss(d, ka + 2 * s, q + 2 * s, kIdescS, s ? 1u : 0u);
-                pa_commit(b_empty + 8 * st);
+                    for (int s = 0; s < 8; ++s) pa_mma(d, kt + 8 * s, q + (s >> 2) * (RP * 128 / 16) + 2 * (s & 3), kIdescS, s ? 1u : 0u);
+                    pa_commit(b_kfree + 8 * (t & 1));
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) p8_mma_ss(d, ka + 2 * s, q + 2 * s, kIdescS, s ? 1u : 0u);
+                    pa_commit(b_empty + 8 * st);
+                }
                 pa_commit(b_s + 8 * (t % SB));
                 if (flags & 2u) pa_commit(b_qfree + 8 * (n_seg & 1));
             }
@@ -509,7 +532,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
             if (n >= 2) p8_wait<Cfg::kSplit || F32>(b_qfree + 8 * (n & 1), phase(n - 2, 2), &s_ctl);
             uint8_t *const q = s_q + (n & 1) * Cfg::kQ;
             constexpr int kDeep = RP / 2 < 8 ? RP / 2 : 4;
-            for (int i = 0; i < RP / 2; i += kDeep) p8_queries<RP, kDeep>(A, g, 2 * i, 2, q, s_qs[n & 3], lane);
+            for (int i = 0; i < RP / 2; i += kDeep) p8_queries<RP, kDeep, Cfg::kTurned>(A, g, 2 * i, 2, q, s_qs[n & 3], lane);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) pa_arrive(b_q + 8 * (n & 1));
@@ -525,6 +548,27 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
             const uint32_t mask = s_info[t % kP8Ring].mask;
             const int n_pos = s_info[t % kP8Ring].n_pos;
             const bool whole = mask == 0xFFu && n_pos >= kPaTile;
+            if (Cfg::kTurned) {  // K: lane = position, columns of two dimensions (what is no position is cut out of S)
+                if (t >= 2) p8_wait<Cfg::kSplit || F32>(b_kfree + 8 * (t & 1), phase(t - 2, 2), &s_ctl);
+                pa_fence_after();
+                const uint8_t *const krow = s_k + st * kP8StageK + tid * kPgDim;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(krow + ((c ^ (tid & 7)) << 4));
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[2 * i] = p8_decode2(ww[i] & 0xFFFFu);
+                        o[2 * i + 1] = p8_decode2(ww[i] >> 16);
+                    }
+                    pa_st8(tmem + quarter + Cfg::kColK + 64 * (t & 1) + 8 * c, o);
+                }
+                pa_wait_st();
+                pa_fence_before();
+                __syncwarp();
+                if (lane == 0) pa_arrive(b_k + 8 * (t & 1));
+            }
             const int vb = t % VB;
             if (t >= VB) p8_wait<Cfg::kSplit || F32>(b_vfree + 8 * vb, phase(t - VB, VB), &s_ctl);
             pa_fence_after();
@@ -604,7 +648,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
                 float h[2][kStep], f[2][kStep];
                 const uint32_t col = tmem + quarter + Cfg::kColS + NS * (t % SB) + rb;
                 p8_ld<kStep>(col, h[0]);
-                p8_ld<kStep>(col + RP, f[0]);
+                if (!Cfg::kTurned) p8_ld<kStep>(col + RP, f[0]);
 #pragma unroll
                 for (int j = 0; j < RG; j += kStep) {
                     constexpr int kHalf = kStep / 2;
@@ -612,11 +656,16 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
                     pa_wait_ld();
                     if (j + kStep < RG) {
                         p8_ld<kStep>(col + j + kStep, h[now ^ 1]);
-                        p8_ld<kStep>(col + RP + j + kStep, f[now ^ 1]);
+                        if (!Cfg::kTurned) p8_ld<kStep>(col + RP + j + kStep, f[now ^ 1]);
                     }
 #pragma unroll
                     for (int i = 0; i < kHalf; i += 2) {
                         const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(s_qs[n_seg & 3] + rb + j + 2 * i);
+                        if (Cfg::kTurned) {
+                            s[j / 2 + i] = pa_mul2(pa_f2(h[now][2 * i], h[now][2 * i + 1]), q.x);
+                            s[j / 2 + i + 1] = pa_mul2(pa_f2(h[now][2 * i + 2], h[now][2 * i + 3]), q.y);
+                            continue;
+                        }
                         s[j / 2 + i] = pa_mul2(pa_fma2(pa_f2(f[now][2 * i], f[now][2 * i + 1]), q_step, pa_f2(h[now][2 * i], h[now][2 * i + 1])), q.x);
                         s[j / 2 + i + 1] =
                             pa_mul2(pa_fma2(pa_f2(f[now][2 * i + 2], f[now][2 * i + 3]), q_step, pa_f2(h[now][2 * i + 2], h[now][2 * i + 3])), q.y);

@@ -482,6 +482,33 @@ def test_a_query_that_is_not_a_number_stays_in_its_row():
         c.check(out_dtype, got, ref)
 
 
+@pytest.mark.parametrize("new", [12, 40, 129])
+@pytest.mark.parametrize("content", ["magnitudes", "small", "not finite", "rising", "scales", "spread", "missing pages"])
+def test_contents_in_long_row_tiles(content, new):
+    """What the tests above bring to windows, in row tiles of 64 and of 128 rows, the last ones part full."""
+    k_exp, v_exp = {"magnitudes": ((-64, -63), (-4, -1)), "small": ((-40, -30), (-4, -1)), "scales": ((-2, 2), (-64, 8)),
+                    "spread": ((2, 3), (-4, -1))}.get(content, ((-4, -1), (-4, -1)))
+    c = Case([300, 150, 700], [new, 3, min(new, 60)], 5, 1, 32, seed=30 + new, k_exp=k_exp, v_exp=v_exp)
+    if content == "magnitudes":  # k_exp keeps the scores of the largest rows finite
+        for t in range(c.T):
+            c.q[t, t % 5] = c.q[t, t % 5] * 2.0 ** (60, -60, -130, 7)[t % 4]
+        c.q[4, 1, 7] *= 2.0 ** 7
+        c.q[5, 3] = 0
+    if content == "rising":
+        for p in range(0, 700, 16):
+            c.pool[c.table[2, p // 32], 0, p % 32 // 16, 4096:4100] = np.array([2.0 ** (-10 + p // 64)], np.float32).view(np.uint8)
+    if content == "missing pages":
+        c.table[0, 0], c.table[0, 7], c.table[2, 3:12], c.table[1] = -1, c.n_pages, 2 ** 31 - 1, -9
+    ref = c.reference()
+    if content == "not finite":
+        c.q[2, 3, 7], c.q[new + 1, 0, :] = float("nan"), float("inf")
+    got = c.run(svd.SVD_BF16)
+    if content == "not finite":
+        assert np.isnan(got[2, 3]).all() and np.isnan(got[new + 1, 0]).all()
+        got[2, 3], got[new + 1, 0] = ref[0][2, 3], ref[0][new + 1, 0]
+    c.check(svd.SVD_BF16, got, ref)
+
+
 def test_offsets_past_32_bits():
     """A pool of 5 GB with the request's pages at its end."""
     c = Case([100], [2], 8, 8, 256, seed=13)
