@@ -8,11 +8,11 @@
 //   V apart), and no smaller than the scale that earlier positions of the unit have;  code = e4m3(y / 2^e)
 //
 // Units.  A scale belongs to 16 positions, so a unit is written by one CTA: the tokens of a request that lie in one unit
-// are a run, and the CTA of the run's first token handles all of it: two kv heads, two warps for the keys of one and
-// two for its values, eight positions to a warp.  A lane keeps four dimensions of them in shared memory, where the
+// are a run, and the CTA of the run's first token handles all of it, for two kv heads, with four warps to a head that take turns at its
+// tokens, keys and values alike.  A lane keeps four dimensions of them in shared memory, where the
 // copies bring them while the angles are worked out (in registers, eight positions took 128 of them; cut down to 64, that
-// spilled).  The largest magnitude takes one exchange.  Where earlier positions keep a smaller scale, their codes
-// are rounded again in place.
+// spilled).  The largest magnitudes take one exchange.  Codes of values go through shared memory to whole rows of the
+// page.  Where earlier positions keep a smaller scale, their codes are rounded again; what the unit held is fetched ahead of the angles.
 //
 // Codes.  A key next to the border of two codes must get the code that exact arithmetic gives, or the cache
 // would depend on how the angle was rounded.  Rotated keys are worked out in plain fp32, with an error below
@@ -21,14 +21,15 @@
 // does for all, and decides by the distance from the border between the two codes; where that is within the
 // bound still, in fp64.  The scale likewise.  Values and dimensions that do not turn are exact as they come.
 //
-// What bounds it (times in a graph).  4 tokens take 4.7 us, a launch and the chain of one unit: copies and angles,
-// rotation, the exchange, the codes.  256 tokens of as many requests take 9.1 us: each opens a unit of its own, and a unit that
-// grows reads its codes back.  4099 tokens of 32 + 16 heads take 28.7 us for 92 MB, 0.48 of the copy rate: issue at
-// 48 %, 20 of 64 warps there on average (three CTAs to an SM, by registers), in waits for copies, shared memory and each other.  On the way there, in us: a CTA
+// What bounds it (times in a graph).  4 tokens take 4.6 us, a launch and the chain of one unit: loads that follow from one
+// another, angles, rotation, the exchange, the codes.  64 windows of 4 tokens take 8.5 us: every CTA has such a chain, some two, and all are there
+// at once.  4099 tokens of 32 + 16 heads take 27.2 us for 92 MB, 0.51 of the copy rate: issue at
+// half, three CTAs to an SM (by registers), whose warps wait for copies, shared memory and each other.  On the way there, in us: a CTA
 // to a unit with all of it in registers 112, halves of a unit 109, one maximum's border cases kept apart from
 // the certain ones 60 (a maximum of 448 * 2^e itself, frequent in bf16, had gone the slow way), query heads one at a time 47,
 // inputs in shared memory 40, a bound for a lane and not an element 35, angle tables in shared memory 30,
-// fp64 for one element at a time 28.7.
+// fp64 for one element at a time 28.7; two warps for the keys of eight positions each and two for their values, of which the latter were done
+// in a third of the time, until here.
 #include "paged8.cuh"
 #include "paged_rope.cuh"
 
@@ -36,7 +37,7 @@ namespace svd {
 
 constexpr int kA8Warps = 8;
 constexpr int kA8Threads = 32 * kA8Warps;
-constexpr int kA8Pos = 8;                  // positions of a warp
+constexpr int kA8Pos = 4;                  // positions of a warp, of keys and of values
 constexpr int kA8Low = 16 * SVD_ROPE_MAX_PAIRS;
 constexpr float kA8Err = 3.f * 0x1p-24f;   // of a rotated key, against |x_a| + |x_b|
 
@@ -50,6 +51,7 @@ struct A8Args {
     int64_t n_pages;
     int T, R, width, Hq, Hkv, page;
     int block, kv_parts;  // tokens of a CTA; CTAs of the kv heads (which come first)
+    int q_step;           // query heads of all CTAs that share a block of tokens: a warp takes every q_step-th
     int row_bits;         // the power of two that holds all pairs
     RopeArgs rope;
 };
@@ -202,19 +204,13 @@ __device__ __forceinline__ int a8_clamp(int e) { return min(max(e, kP8ExpLo), kP
 // The largest magnitude of a warp's values (0 where there is none; NaN counts for nothing).
 __device__ __forceinline__ float a8_most(float top) { return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top))); }
 
-// What the two warps of a unit's keys, or of its values, tell each other: a value each, the larger one wins.
-__device__ __forceinline__ uint32_t a8_both(uint32_t mine, uint32_t *s_both, int warp, int lane) {
-    if (lane == 0) s_both[warp] = mine;
-    asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
-    const uint32_t theirs = s_both[warp ^ 1];
-    asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
-    return max(mine, theirs);
-}
-
-// A run's part in a warp: positions a .. b - 1 of the warp's eight, the first of them token t.
-struct A8Part {
-    int t, a, b;
+// What the four warps of a head tell each other.
+struct A8Head {
+    uint4 top[4];        // the largest key, with and less what it may be off, and the largest value
+    int need[4];         // exponents that keys ask for, where those leave it open
 };
+__device__ __forceinline__ void a8_sync(int warp) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + (warp >> 2)) : "memory"); }
+
 // Sixteen or eight bytes into the front of a slot of shared memory.
 __device__ __forceinline__ void a8_fetch(float4 *to, const float *from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
@@ -241,9 +237,9 @@ __device__ __forceinline__ bool a8_odd(const float x[4]) {  // one is not finite
 // The exponent (less the lowest) that a warp's part of a run asks for, from its keys in fp64; what is not finite is
 // reported.
 template <typename T>
-__device__ __forceinline__ int a8_need_f64(const A8Args &A, const T *row, int t, int n, int lane) {
+__device__ __forceinline__ int a8_need_f64(const A8Args &A, const T *row, int t, int n, int lane) {  // n tokens, four apart
     double top = 0.0;
-    for (; n > 0; --n, ++t) {
+    for (; n > 0; --n, t += 4) {
         float x[4], xb[4];
         ap_floats(ap_raw(row + (int64_t)t * A.ld + 4 * lane), x);
         a8_mates(a8_lane(A.rope, lane), x, xb);
@@ -261,17 +257,32 @@ __device__ __forceinline__ int a8_need_f64(const A8Args &A, const T *row, int t,
     return e - kP8ExpLo;
 }
 
-// The keys of a run.  row: the head's key of token 0; i0: the run's first position in the unit; half: the warp's
-// eight positions; s_cs: cos and sin of the run's tokens, the first of which is token t0; slot: the lane's, 32 apart.
+// What a unit holds that a run in it may change or has to keep: its scales, a dimension's values, and the words of earlier
+// positions' keys that the warp would round again.
+struct A8Old {
+    uint4 v;
+    float2 scales;
+    uint32_t k[4];
+};
+__device__ __forceinline__ void a8_old(A8Old *o, const uint8_t *unit, int i0, int n, int turn, int lane) {
+    if (n < 16) o->v = *reinterpret_cast<const uint4 *>(unit + kP8VCodes + 16 * (32 * turn + lane));
+    if (i0 > 0) o->scales = *reinterpret_cast<const float2 *>(unit + kP8Scales);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (turn + 4 * k < i0) o->k[k] = reinterpret_cast<const uint32_t *>(unit)[32 * (turn + 4 * k) + lane];
+}
+
+// A run in a unit: four warps take turns at its tokens, keys and values alike.  row: the head's key of token 0; i0, n: the run's first position and its
+// length; t0: its first token, with the others' cos and sin in s_cs; slot, v_slot: the lane's, 32 apart.
 template <typename T>
-__device__ __forceinline__ void a8_keys(const A8Args &A, const T *row, const A8Part P, int i0, int half, int t0, uint8_t *unit,
-                                        const float2 *s_cs, uint32_t *s_both, float4 *slot, int warp,
-                                        int lane) {
+__device__ __forceinline__ void a8_unit(const A8Args &A, const T *row, int i0, int n, int t0, uint8_t *unit, const A8Old &old,
+                                        const float2 *s_cs, A8Head *s, float4 *slot, float4 *v_slot, int warp, int lane) {
+    const int turn = warp & 3, dim = 32 * turn + lane, mine = (n - turn + 3) >> 2;  // tokens turn, turn + 4 ... of the run
+    const int e0 = i0 > 0 ? p8_exponent(old.scales.x) : kP8ExpLo, v0 = i0 > 0 ? p8_exponent(old.scales.y) : kP8ExpLo;
     const A8Lane l = a8_lane(A.rope, lane);
-    const int e0 = i0 > 0 ? p8_exponent(*reinterpret_cast<const float *>(unit + kP8Scales)) : kP8ExpLo;
     float top = 0.f, none = 0.f, turned = 0.f;  // none: NaN where a value is not finite; turned: not 0 where an angle is no quarter turn
 #pragma unroll 2
-    for (int p = P.a; p < P.b; ++p) {
+    for (int p = 0; p < mine; ++p) {
         float x[4];
         a8_slot<T>(slot + 32 * p, x);
         if (A.rope.pairs) {
@@ -279,7 +290,7 @@ __device__ __forceinline__ void a8_keys(const A8Args &A, const T *row, const A8P
             a8_mates(l, x, xb);
             if (l.on) {
                 float c[4], s[4];
-                a8_turn(l, s_cs + (P.t - t0 + p - P.a) * SVD_ROPE_MAX_PAIRS, c, s);
+                a8_turn(l, s_cs + (turn + 4 * p) * SVD_ROPE_MAX_PAIRS, c, s);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     turned = fmaxf(turned, fminf(fabsf(c[j]), fabsf(s[j])));
@@ -305,19 +316,85 @@ __device__ __forceinline__ void a8_keys(const A8Args &A, const T *row, const A8P
     // are ordered as they are).  All ones: something is not finite, or too large, and all of the run's keys are open.
     const float big = a8_most(top), sure = a8_most(none_open ? top : 0.f), near = a8_most(none_open ? 0.f : top), far = a8_most(off);
     const bool wild = __any_sync(~0u, none != 0.f) || big > kP8MaxAbs;
-    const uint32_t hi = a8_both(wild ? ~0u : __float_as_uint(fmaxf(sure, near > 0.f ? near + far : 0.f)), s_both, warp, lane);
-    const uint32_t lo = a8_both(wild ? 0u : __float_as_uint(fmaxf(sure, near - far)), s_both, warp, lane);
+    // The largest value.
+    float v_top = 0.f, v_none = 0.f;
+#pragma unroll
+    for (int p = 0; p < kA8Pos; ++p) {
+        if (p >= mine) break;
+        float x[4];
+        a8_slot<T>(v_slot + 32 * p, x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v_top = fmaxf(v_top, fabsf(x[j]));
+            v_none = fmaf(x[j], 0.f, v_none);
+        }
+    }
+    if (__any_sync(~0u, v_none != 0.f || v_top > kP8MaxAbs)) {  // what is no number counts as 0, and magnitudes end
+        v_top = 0.f;
+        for (int p = 0; p < mine; ++p) {
+            float x[4];
+            a8_slot<T>(v_slot + 32 * p, x);
+            if (__any_sync(~0u, a8_odd(x)) && A.status && lane == 0) atomicOr(A.status + t0 + turn + 4 * p, SVD_ST_NONFINITE);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] = x[j] == x[j] ? fminf(fmaxf(x[j], -kP8MaxAbs), kP8MaxAbs) : 0.f;
+                v_top = fmaxf(v_top, fabsf(x[j]));
+            }
+            a8_put<T>(v_slot + 32 * p, x);
+        }
+    }
+    v_top = a8_most(v_top);
+    if (lane == 0)
+        s->top[turn] = make_uint4(wild ? ~0u : __float_as_uint(fmaxf(sure, near > 0.f ? near + far : 0.f)),
+                                     wild ? 0u : __float_as_uint(fmaxf(sure, near - far)), __float_as_uint(v_top), 0u);
+    a8_sync(warp);
+    uint32_t hi = 0, lo = 0, vb = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const uint4 m = s->top[w];
+        hi = max(hi, m.x);
+        lo = max(lo, m.y);
+        vb = max(vb, m.z);
+    }
+
+    // Codes of values (slots of no token hold anything: their bytes are not used), and into the warp's slots with them: those of
+    // dimension 4l + j at word 40 j + l, so that no two lanes meet in a bank, here or where rows are read.
+    uint32_t *const v_codes = reinterpret_cast<uint32_t *>(v_slot - lane);
+    const int ve = max(a8_clamp(p8_need(__uint_as_float(vb))), v0);
+    {
+        const float inv = p8_pow2(-ve);
+        uint32_t w[4];
+#pragma unroll
+        for (int p = 0; p < kA8Pos; p += 2) {
+            float a4[4], b4[4];
+            a8_slot<T>(v_slot + 32 * p, a4);
+            a8_slot<T>(v_slot + 32 * p + 32, b4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t two = p8_encode2(a4[j] * inv, b4[j] * inv);
+                if (p) w[j] |= two << 16;
+                else w[j] = two;
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v_codes[40 * j + lane] = w[j];
+    }
+
+    // Codes of keys.
     int e = a8_clamp(p8_need(__uint_as_float(hi)));
     uint32_t again = 0;  // positions whose codes are open
     if (hi == ~0u || a8_clamp(p8_need(__uint_as_float(lo))) != e) {
-        e = (int)a8_both((uint32_t)a8_need_f64(A, row, P.t, P.b - P.a, lane), s_both, warp, lane) + kP8ExpLo;
-        e = max(e, e0);
-        again = (1u << P.b) - (1u << P.a);
+        const int need = a8_need_f64(A, row, t0 + turn, mine, lane);
+        if (lane == 0) s->need[turn] = need;
+        a8_sync(warp);
+        e = max(max(max(s->need[0], s->need[1]), max(s->need[2], s->need[3])) + kP8ExpLo, e0);
+        again = (1u << max(mine, 0)) - 1u;
     } else {
         e = max(e, e0);
         const float inv = p8_pow2(-e), d = off * inv;
 #pragma unroll 2
-        for (int p = P.a; p < P.b; ++p) {
+        for (int p = 0; p < mine; ++p) {
             const float4 y = slot[32 * p];
             const float y4[4] = {y.x, y.y, y.z, y.w};
             float a[4], b[4];
@@ -329,111 +406,75 @@ __device__ __forceinline__ void a8_keys(const A8Args &A, const T *row, const A8P
             const uint32_t codes = p8_encode2(a[0], a[1]) | (p8_encode2(a[2], a[3]) << 16);
             const uint32_t other = p8_encode2(b[0], b[1]) | (p8_encode2(b[2], b[3]) << 16);
             if (__any_sync(~0u, codes != other)) again |= 1u << p;
-            const int i = kA8Pos * half + p;
+            const int i = i0 + turn + 4 * p;
             *reinterpret_cast<uint32_t *>(unit + i * kPgDim + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4) = codes;
         }
     }
     for (; again; again &= again - 1u) {
-        const int p = __ffs(again) - 1, t = P.t + p - P.a, i = kA8Pos * half + p;
-        const uint32_t codes = a8_codes(A, t, row + (int64_t)t * A.ld, lane, e, s_cs + (t - t0) * SVD_ROPE_MAX_PAIRS);
+        const int k = turn + 4 * (__ffs(again) - 1), t = t0 + k, i = i0 + k;
+        const uint32_t codes = a8_codes(A, t, row + (int64_t)t * A.ld, lane, e, s_cs + k * SVD_ROPE_MAX_PAIRS);
         *reinterpret_cast<uint32_t *>(unit + i * kPgDim + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4) = codes;
     }
     if (e > e0 && i0 > 0) {
-        uint32_t *const words = reinterpret_cast<uint32_t *>(unit) + 32 * half + lane;  // of earlier positions, 64 apart
         const float down = p8_pow2(e0 - e);
-        uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (half + 2 * k < i0) w[k] = words[64 * k];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (half + 2 * k < i0) words[64 * k] = a8_again(w[k], down);
+        for (int k = 0; k < 4; ++k)
+            if (turn + 4 * k < i0) reinterpret_cast<uint32_t *>(unit)[32 * (turn + 4 * k) + lane] = a8_again(old.k[k], down);
     }
-    if (half == 0 && lane == 0) *reinterpret_cast<float *>(unit + kP8Scales) = p8_pow2(e);
-}
 
-// The values of a run; n: its length.
-template <typename T>
-__device__ __forceinline__ void a8_values(const A8Args &A, const A8Part P, int i0, int n, int half, uint8_t *unit, uint32_t *s_both,
-                                          float4 *slot, int warp, int lane) {
-    uint2 *const rows = reinterpret_cast<uint2 *>(unit + kP8VCodes) + 8 * lane + half;  // of the lane's dimensions, 16 bytes apart
-    uint2 old[4];
+    // Rows of values, a dimension to a lane: new bytes i0 .. i0 + n - 1, earlier ones under the scale as it is now, later
+    // ones as they were.
+    a8_sync(warp);  // (also: every warp has read the scales)
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = v_codes[(k - turn) * (2 * kA8Pos * 32 * 4) + 40 * (lane & 3) + (dim >> 2)];
+    // in the order of tokens: byte k of the warps' four words is word k
+    const uint32_t a01 = __byte_perm(v[0], v[1], 0x5140), a23 = __byte_perm(v[2], v[3], 0x5140);
+    const uint32_t b01 = __byte_perm(v[0], v[1], 0x7362), b23 = __byte_perm(v[2], v[3], 0x7362);
+    uint32_t w[4] = {__byte_perm(a01, a23, 0x5410), __byte_perm(a01, a23, 0x7632), __byte_perm(b01, b23, 0x5410),
+                     __byte_perm(b01, b23, 0x7632)};
+    if (i0 > 0) {  // token 0 goes to byte i0
+        const int by = 8 * (i0 & 3);
+        w[3] = __funnelshift_l(w[2], w[3], by);
+        w[2] = __funnelshift_l(w[1], w[2], by);
+        w[1] = __funnelshift_l(w[0], w[1], by);
+        w[0] <<= by;
+        if (i0 & 4) {
+            w[3] = w[2];
+            w[2] = w[1];
+            w[1] = w[0];
+        }
+        if (i0 & 8) {
+            w[3] = w[1];
+            w[2] = w[0];
+        }
+    }
+    uint32_t was[4] = {old.v.x, old.v.y, old.v.z, old.v.w};
     if (n < 16) {
+        const float down = p8_pow2(v0 - ve);
+        const bool grown = i0 > 0 && ve > v0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) old[j] = rows[2 * j];
-    }
-    const int e0 = i0 > 0 ? p8_exponent(*reinterpret_cast<const float *>(unit + kP8Scales + 4)) : kP8ExpLo;
-    float top = 0.f, none = 0.f;
-#pragma unroll 2
-    for (int p = P.a; p < P.b; ++p) {
-        float x[4];
-        a8_slot<T>(slot + 32 * p, x);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            top = fmaxf(top, fabsf(x[j]));
-            none = fmaf(x[j], 0.f, none);
-        }
-    }
-    if (__any_sync(~0u, none != 0.f || top > kP8MaxAbs)) {  // what is no number counts as 0, and magnitudes end
-        top = 0.f;
-        for (int p = P.a; p < P.b; ++p) {
-            float x[4];
-            a8_slot<T>(slot + 32 * p, x);
-            if (__any_sync(~0u, a8_odd(x)) && A.status && lane == 0) atomicOr(A.status + P.t + p - P.a, SVD_ST_NONFINITE);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] = x[j] == x[j] ? fminf(fmaxf(x[j], -kP8MaxAbs), kP8MaxAbs) : 0.f;
-                top = fmaxf(top, fabsf(x[j]));
-            }
-            a8_put<T>(slot + 32 * p, x);
-        }
-    }
-    const float big = __uint_as_float(a8_both(__float_as_uint(a8_most(top)), s_both, warp, lane));
-    const int e = max(a8_clamp(p8_need(big)), e0);
-    const float inv = p8_pow2(-e), down = p8_pow2(e0 - e);
-    const bool grown = i0 > 0 && e > e0;
-    uint32_t w[4][2];  // [dimension][four positions]
-#pragma unroll
-    for (int p = 0; p < kA8Pos; p += 2) {  // (slots of no position hold anything: their bytes are not used)
-        float a4[4], b4[4];
-        a8_slot<T>(slot + 32 * p, a4);
-        a8_slot<T>(slot + 32 * p + 32, b4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t two = p8_encode2(a4[j] * inv, b4[j] * inv);
-            if (p & 2) w[j][p >> 2] |= two << 16;
-            else w[j][p >> 2] = two;
-        }
-    }
-    // New bytes i0 .. i0 + n - 1, earlier ones under the scale as it is now, later ones as they were.
-    if (n < 16) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const int first = kA8Pos * half + 4 * g;
-            const int a = min(max(i0 - first, 0), 4), b = min(max(i0 + n - first, 0), 4);  // new bytes of the word
+        for (int q = 0; q < 4; ++q) {
+            const int a = min(max(i0 - 4 * q, 0), 4), b = min(max(i0 + n - 4 * q, 0), 4);  // new bytes of the word
             const uint32_t ma = a < 4 ? ~0u << (8 * a) : 0u, mb = b < 4 ? ~0u << (8 * b) : 0u, fresh = ma & ~mb;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t keep = g ? old[j].y : old[j].x;
-                if (grown && a > 0) keep = (a8_again(keep, down) & ~ma) | (keep & ma);
-                w[j][g] = (w[j][g] & fresh) | (keep & ~fresh);
-            }
+            if (grown && a > 0) was[q] = (a8_again(was[q], down) & ~ma) | (was[q] & ma);
+            w[q] = (w[q] & fresh) | (was[q] & ~fresh);
         }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) rows[2 * j] = make_uint2(w[j][0], w[j][1]);
-    if (half == 0 && lane == 0) *reinterpret_cast<float *>(unit + kP8Scales + 4) = p8_pow2(e);
+    reinterpret_cast<uint4 *>(unit + kP8VCodes)[dim] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (dim == 0) *reinterpret_cast<float2 *>(unit + kP8Scales) = make_float2(p8_pow2(e), p8_pow2(ve));
 }
 
-constexpr size_t kA8Smem = kA8Warps * kA8Pos * 32 * sizeof(float4) + 2 * kA8Low * sizeof(float2);
+constexpr size_t kA8Smem = kA8Warps * 2 * kA8Pos * 32 * sizeof(float4) + 2 * kA8Low * sizeof(float2);
 
 template <typename T>
 __global__ void __launch_bounds__(kA8Threads, 3) paged8_append_kernel(const __grid_constant__ A8Args A) {
-    extern __shared__ float4 s_x[];  // [warp][position][lane], then the angles
+    extern __shared__ float4 s_x[];  // [warp][keys, values][position][lane], then the angles
     __shared__ __align__(16) A8Tables s_tab;
-    __shared__ uint32_t s_both[kA8Warps];
+    __shared__ __align__(16) A8Head s_head[2];
     __shared__ int s_r;
-    float2 *const s_cs = reinterpret_cast<float2 *>(s_x + kA8Warps * kA8Pos * 32);
+    __shared__ int4 s_run;  // of the block's first token: where its request's tokens begin and end, and the request's length
+    float2 *const s_cs = reinterpret_cast<float2 *>(s_x + kA8Warps * 2 * kA8Pos * 32);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const T *const qkv = reinterpret_cast<const T *>(A.qkv) + 4 * lane;
     const int t0 = blockIdx.x * A.block, t1 = min(t0 + A.block, A.T);
@@ -444,92 +485,105 @@ __global__ void __launch_bounds__(kA8Threads, 3) paged8_append_kernel(const __gr
 
     if ((int)blockIdx.y >= A.kv_parts) {
         // ---- queries: a warp takes a head of the block's tokens -----------------------------------
-        const int head = ((int)blockIdx.y - A.kv_parts) * kA8Warps + warp, end = A.q_start[A.R];
-        const bool there = head < A.Hq;
-        const T *row = qkv + t0 * A.ld + (int64_t)head * kPgDim;
+        const int first = ((int)blockIdx.y - A.kv_parts) * kA8Warps + warp, end = A.q_start[A.R];
         constexpr int kAhead = sizeof(T) == 2 ? 8 : 4;
         decltype(ap_raw(qkv)) ahead[kAhead];
+        auto fetch = [&](int head) {
+            const T *const row = qkv + t0 * A.ld + (int64_t)head * kPgDim;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (there && t0 + k < t1) ahead[k] = ap_raw(row + k * A.ld);
+            for (int k = 0; k < kAhead; ++k)
+                if (head < A.Hq && t0 + k < t1) ahead[k] = ap_raw(row + k * A.ld);
+        };
+        fetch(first);
         a8_angles(A, t0, t1 - t0, s_cs, s_tab);
         __syncthreads();
-        if (!there) return;
         const A8Lane l = a8_lane(A.rope, lane);
-        __nv_bfloat16 *q = A.q + ((int64_t)t0 * A.Hq + head) * kPgDim + 4 * lane;
         const int n = min(t1, end) - t0;
-        for (int g = 0; g < n; g += kAhead) {
+#pragma unroll 1
+        for (int head = first; head < A.Hq; head += A.q_step) {
+            const T *const row = qkv + t0 * A.ld + (int64_t)head * kPgDim;
+            __nv_bfloat16 *q = A.q + ((int64_t)t0 * A.Hq + head) * kPgDim + 4 * lane;
+            for (int g = 0; g < n; g += kAhead) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int t = g + k;
-                if (t >= n) break;
-                float x[4], xb[4];
-                ap_floats(ahead[k], x);
-                if (t0 + t + kAhead < t1) ahead[k] = ap_raw(row + (int64_t)(t + kAhead) * A.ld);
-                if (A.rope.pairs) {
-                    a8_mates(l, x, xb);
-                    if (l.on) {
-                        float c[4], s[4];
-                        a8_turn(l, s_cs + t * SVD_ROPE_MAX_PAIRS, c, s);
+                for (int k = 0; k < kAhead; ++k) {
+                    const int t = g + k;
+                    if (t >= n) break;
+                    float x[4], xb[4];
+                    ap_floats(ahead[k], x);
+                    if (t0 + t + kAhead < t1) ahead[k] = ap_raw(row + (int64_t)(t + kAhead) * A.ld);
+                    if (A.rope.pairs) {
+                        a8_mates(l, x, xb);
+                        if (l.on) {
+                            float c[4], s[4];
+                            a8_turn(l, s_cs + t * SVD_ROPE_MAX_PAIRS, c, s);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], c[j], xb[j] * s[j]);
+                            for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], c[j], xb[j] * s[j]);
+                        }
                     }
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+                    uint2 o;
+                    o.x = reinterpret_cast<const uint32_t &>(a);
+                    o.y = reinterpret_cast<const uint32_t &>(b);
+                    *reinterpret_cast<uint2 *>(q) = o;
+                    q += A.Hq * kPgDim;
                 }
-                const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-                uint2 o;
-                o.x = reinterpret_cast<const uint32_t &>(a);
-                o.y = reinterpret_cast<const uint32_t &>(b);
-                *reinterpret_cast<uint2 *>(q) = o;
-                q += A.Hq * kPgDim;
             }
+            fetch(head + A.q_step);
         }
         return;
     }
 
     // ---- keys and values: the runs that begin in this block of tokens, two kv heads ------------------
-    const int h = 2 * (int)blockIdx.y + (warp >> 2), is_v = (warp >> 1) & 1, half = warp & 1;
+    const int h = 2 * (int)blockIdx.y + (warp >> 2), turn = warp & 3;
     for (int r = tid; r < A.R; r += kA8Threads) {
-        if (A.q_start[r] <= t0 && t0 < A.q_start[r + 1]) atomicMax(&s_r, r);
+        const int a = A.q_start[r], b = A.q_start[r + 1];
+        if (a <= t0 && t0 < b) {
+            atomicMax(&s_r, r);
+            s_run = make_int4(a, b, A.kv_len[r], 0);
+        }
     }
     __syncthreads();
     int r = s_r;
     if (r < 0) return;  // behind the last request
+    int q0 = s_run.x, q2 = s_run.y, len = s_run.z;
     for (int t = t0; t < t1;) {
-        while (r + 1 < A.R && A.q_start[r + 1] <= t) ++r;
-        const int q0 = A.q_start[r], q2 = A.q_start[r + 1], q1 = min(q2, A.T);
-        const int64_t at = (int64_t)A.kv_len[r] - ((int64_t)q2 - q0) + ((int64_t)t - q0);  // position of token t
-        const int i0 = (int)(at & 15), end = min(t + 16 - i0, q1);
+        if (q2 <= t) {
+            while (r + 1 < A.R && A.q_start[r + 1] <= t) ++r;
+            q0 = A.q_start[r];
+            q2 = A.q_start[r + 1];
+            len = A.kv_len[r];
+        }
+        const int64_t at = (int64_t)len - ((int64_t)q2 - q0) + ((int64_t)t - q0);  // position of token t
+        const int i0 = (int)(at & 15), end = min(t + 16 - i0, min(q2, A.T));
         if (end <= t || t < q0) return;  // (behind the last request, or a q_start that does not ascend)
         if (t != q0 && i0 != 0) {  // the run began in another block
             t = end;
             continue;
         }
         const int n = end - t;  // positions i0 .. i0 + n - 1 of the unit
-        const T *const row = qkv + (int64_t)(A.Hq + h + is_v * A.Hkv) * kPgDim;
-        A8Part P;
-        P.a = min(max(i0 - kA8Pos * half, 0), kA8Pos);
-        P.b = min(max(i0 + n - kA8Pos * half, 0), kA8Pos);
-        P.t = t + (half ? max(kA8Pos - i0, 0) : 0);
-        float4 *const slot = s_x + warp * (kA8Pos * 32) + lane;
-        if (h < A.Hkv)
-            for (int p = P.a; p < P.b; ++p) a8_fetch(slot + 32 * p, row + (int64_t)(P.t + p - P.a) * A.ld);
         int64_t pg = -1;
         if (at >= 0 && at < (int64_t)A.width * A.page) pg = A.table[(int64_t)r * A.width + (uint32_t)at / (uint32_t)A.page];
-        if (pg < 0 || pg >= A.n_pages) {
-            if (A.status && h == 0 && warp == 0 && lane < n) atomicOr(A.status + t + lane, SVD_ST_BAD_SLOT);
-            a8_fetched();
-            t = end;
-            continue;
-        }
+        const T *const row = qkv + (int64_t)(A.Hq + h) * kPgDim;
+        float4 *const slot = s_x + warp * (2 * kA8Pos * 32) + lane, *const v_slot = slot + kA8Pos * 32;
+        if (h < A.Hkv)
+            for (int k = turn, p = 0; k < n; k += 4, ++p) {
+                const T *const from = row + (int64_t)(t + k) * A.ld;
+                a8_fetch(slot + 32 * p, from);
+                a8_fetch(v_slot + 32 * p, from + A.Hkv * kPgDim);
+            }
         __syncthreads();  // (the angles of the run before are read)
+        const bool stored = pg >= 0 && pg < A.n_pages;
+        const int place = (int)((uint32_t)at % (uint32_t)A.page) >> 4;
+        uint8_t *const unit = A.pages + ((pg * A.Hkv + h) * (A.page >> 4) + place) * (int64_t)kP8UnitBytes;
+        A8Old old = {};
+        if (stored && h < A.Hkv) a8_old(&old, unit, i0, n, turn, lane);  // (on its way while the angles are worked out)
         a8_angles(A, t, n, s_cs, s_tab);
         a8_fetched();
         __syncthreads();
-        if (h < A.Hkv) {
-            const int place = (int)((uint32_t)at % (uint32_t)A.page) >> 4;
-            uint8_t *const unit = A.pages + ((pg * A.Hkv + h) * (A.page >> 4) + place) * (int64_t)kP8UnitBytes;
-            if (is_v) a8_values<T>(A, P, i0, n, half, unit, s_both, slot, warp, lane);
-            else a8_keys(A, row - 4 * lane, P, i0, half, t, unit, s_cs, s_both, slot, warp, lane);
+        if (!stored) {
+            if (A.status && h == 0 && warp == 0 && lane < n) atomicOr(A.status + t + lane, SVD_ST_BAD_SLOT);
+        } else if (h < A.Hkv) {
+            a8_unit(A, row - 4 * lane, i0, n, t, unit, old, s_cs, &s_head[warp >> 2], slot, v_slot, warp, lane);
         }
         t = end;
     }
@@ -571,10 +625,16 @@ int paged8_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv
     // As many tokens to a CTA, up to sixteen, as let nearly all CTAs be there at once.
     A.kv_parts = (Hkv + 1) / 2;
     while (1 << A.row_bits < A.rope.pairs) ++A.row_bits;
-    const int parts = A.kv_parts + (Hq + kA8Warps - 1) / kA8Warps;
+    int q_parts = (Hq + kA8Warps - 1) / kA8Warps;
+    const int parts = A.kv_parts + q_parts;
     A.block = 1;
     while (A.block < 16 && (int64_t)T * parts > 4ll * sms * A.block) A.block *= 2;
-    const dim3 grid((unsigned)((T + A.block - 1) / A.block), (unsigned)parts);
+    // Two query heads to a warp where that lets all CTAs be there at once, three to an SM (64 windows of 4 tokens, 40 + 16 heads: 9.5 -> 8.45 us;
+    // chunks of 4099 tokens, far from that, gain nothing by it: 28.4 -> 28.5).
+    const int blocks = (T + A.block - 1) / A.block, half = (q_parts + 1) / 2;
+    if ((int64_t)blocks * (A.kv_parts + q_parts) > 3ll * sms && (int64_t)blocks * (A.kv_parts + half) <= 3ll * sms) q_parts = half;
+    A.q_step = q_parts * kA8Warps;
+    const dim3 grid((unsigned)blocks, (unsigned)(A.kv_parts + q_parts));
     if (dtype == SVD_F32) {
         SVD_CUDA_TRY((allow_smem<paged8_append_kernel<float>>(kA8Smem)));
         SVD_CUDA_TRY(launch(paged8_append_kernel<float>, grid, dim3(kA8Threads), kA8Smem, stream, true, A));

@@ -114,6 +114,31 @@ def test_append(dtype, lens, new, Hq, Hkv, page, axes, pairs, inter, pad):
         assert np.array_equal(q, as_type(x[:, :Hq], svd.SVD_BF16).double().numpy())
 
 
+@pytest.mark.parametrize("dtype", [svd.SVD_F32, svd.SVD_BF16])
+@pytest.mark.parametrize("Hq,new", [(37, 4), (40, None)])
+def test_append_of_many_windows(dtype, Hq, new):
+    """256 tokens of 64 requests, begun at every place of a unit, behind positions whose scales they raise or not: query heads that are
+    no multiple of a CTA's, two of them to a warp; rows behind the last token stay as they are."""
+    g = np.random.default_rng(Hq)
+    n_new = np.full(64, 4) if new else np.bincount(np.repeat(np.arange(64), 4)[g.integers(0, 256, 253)], minlength=64)
+    lens = n_new + np.arange(64) + g.integers(0, 3, 64) * 16
+    table, q_start, n_pages = layout(lens.tolist(), n_new.tolist(), 32, g)
+    pool = random_pool(g, n_pages, 8, 32, e_lo=-9, e_hi=-5)
+    T, pad = int(q_start[-1]), 256 - int(q_start[-1])
+    x = as_type(g.normal(0, 1, (T, Hq + 16, 128)).astype(np.float32) * 2.0 ** g.integers(-3, 4, (T, 1, 1)), dtype).float().numpy()
+    pos = np.zeros((1, 256), np.int64)
+    pos[0, :T] = np.concatenate([np.arange(n - k, n) for n, k in zip(lens, n_new)])
+    inv = 1e4 ** (-np.arange(64) / 64)
+    args = (lens.tolist(), q_start, table)
+    q, got, st = gpu_append(x, dtype, Hq, 8, *args, pool, 32, rope=svd.Rope(inv), positions=pos, T=T + pad)
+    y = paged.rotate(x.astype(np.float64), pos[:, :T], inv, [0] * 64, False)
+    want = pool.copy()
+    assert not paged8.append(want, y[:, Hq:Hq + 8], x[:, Hq + 8:], *args, 32)
+    assert np.array_equal(same_zeros(got), same_zeros(want)) and not st.any()
+    check_q(q[:T], y[:, :Hq])
+    assert np.all(q[T:] == -7.0)
+
+
 def test_append_next_to_the_borders_of_codes_and_scales():
     """Values on and one ulp off every border between two codes, and blocks whose largest is 448 scales or one ulp off."""
     v = paged8.VALUE[:127]
