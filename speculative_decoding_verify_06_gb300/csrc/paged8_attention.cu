@@ -114,6 +114,7 @@ struct P8Seg {
     int base, len, slot;            // position of token 0; workspace slot, or -1: write the output
     int tok, off;                   // token of row 0, and row 0 among its heads
     int tiles;                      // of this segment
+    int req, head, tile0;           // request, kv head, first tile along the cache
 };
 
 // Query rows row0 + step i + (0, 1), i < n, of a segment: fetched, split and laid out by a warp, sixteen lanes to a row; in two
@@ -127,8 +128,9 @@ __device__ __forceinline__ void p8_queries(const PaArgs &A, const P8Seg &g, int 
         const int row = row0 + step * i + (lane >> 4);
         w[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row < g.rows) {
-            const int rr = g.row0 + row, tok = rr / A.G;
-            w[i] = *reinterpret_cast<const uint4 *>(A.q + ((int64_t)(g.token0 + tok) * A.Hq + g.head0 + rr - tok * A.G) * kPgDim + ch * 8);
+            // row's token behind token g.tok: (g.off + row) / G, exact (below 2^13, by G <= 4096)
+            const int rr = g.off + row, tok = A.G == 1 ? rr : (int)__umulhi((uint32_t)rr, A.g_magic);
+            w[i] = *reinterpret_cast<const uint4 *>(A.q + ((int64_t)(g.token0 + g.tok + tok) * A.Hq + g.head0 + rr - tok * A.G) * kPgDim + ch * 8);
         }
     }
 #pragma unroll
@@ -354,63 +356,24 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
     if (warp >= kCopyWarp && Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsRest));
     if (warp == kCopyWarp) {
         // ---- copies: lane j < 8 brings unit j of each tile ---------------------------------
-        // Descriptors of tile t (and its segment) go into ring entry t mod 16.  A stage is refilled after V of its
+        // Descriptors of tile t go into ring entry t mod 16.  A stage is refilled after V of its
         // tile is turned, and that runs at most two tiles ahead of O: the slowest reader, a softmax warp that ends a
         // segment, is at tile t - 8 at the earliest.
-        int r = 0;
-        {
-            int a = 0, b = A.R;
-            while (b - a > 1) {
-                const int mid = (a + b) >> 1;
-                if (s_pre[mid] <= lo) a = mid; else b = mid;
-            }
-            r = a;
-        }
         const bool copies = s_ctl.limit != 0u;  // (a limit of no polls, the test hook: as if the copy engine had stopped)
         int u = lo, k = 0, n_seg = 0, st = 0;
         uint32_t st_phase = 0;
-        PaReq x = pa_req(A, r);
-        int head_tiles = pa_head_tiles<RP>(A, x);
-        P8Split split = {};
         while (u < hi) {
-            while (s_pre[r + 1] <= u) {
-                ++r;
-                if (s_pre[r + 1] > u) {
-                    x = pa_req(A, r);
-                    head_tiles = pa_head_tiles<RP>(A, x);
-                }
-            }
-            const int h = (u - s_pre[r]) / head_tiles;
-            int s0 = s_pre[r] + h * head_tiles, rt = 0, nt = pa_row_tiles<RP>(A, x, 0);
-            while (s0 + nt <= u) {
-                s0 += nt;
-                nt = pa_row_tiles<RP>(A, x, ++rt);
-            }
-            int end = min(hi, s0 + nt);
             const int si = n_seg % kP8Ring;
-            if (lane == 0) {
-                P8Seg g;
-                g.token0 = x.q0;
-                g.head0 = h * A.G;
-                g.row0 = rt * RP;
-                g.rows = min(RP, x.rows - rt * RP);
-                g.base = x.base;
-                g.len = x.len;
-                g.slot = u == s0 && end == s0 + nt ? -1 : 2 * (int)blockIdx.x + (u == s0 ? 1 : 0);
-                g.tok = g.row0 / A.G;
-                g.off = g.row0 - g.tok * A.G;
-                g.tiles = end - u;
-                s_seg[si] = g;
-                pa_arrive(b_seg + 8 * si);
-                if (u == s0 && end < s0 + nt) split = {g.token0, g.head0, g.row0, g.rows, pa_cta_of(n_tiles, gridDim.x, s0 + nt - 1), {}};
-            }
+            if (!p8_wait<Cfg::kSplit || F32>(b_seg + 8 * si, phase(n_seg, kP8Ring), &s_ctl)) break;
+            const int h = s_seg[si].head, len = s_seg[si].len, s0 = u - s_seg[si].tile0, r = s_seg[si].req;
+            int end = u + s_seg[si].tiles;
             const int upp = A.page / kPgUnitPos;
             // j / upp for j < 2^28 (upp <= 16)
             auto page_of = [&](int j) { return upp == 1 ? j : (int)__umulhi((uint32_t)j, A.upp_magic); };
             const int32_t *const row = A.table + (int64_t)r * A.width;
             auto lookup = [&](int tile) -> int {
                 const int j = tile * kPaTileUnits + lane;
-                return lane < kPaTileUnits && j * kPgUnitPos < x.len ? row[page_of(j)] : -1;
+                return lane < kPaTileUnits && j * kPgUnitPos < len ? row[page_of(j)] : -1;
             };
             int pg = lookup(u - s0);
             for (; u < end; ++u, ++k) {
@@ -426,7 +389,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
                 if (lane == 0) {
                     PaTileInfo t;
                     t.mask = mask;
-                    t.n_pos = x.len - tile * kPaTile;
+                    t.n_pos = len - tile * kPaTile;
                     t.tile = tile;
                     const bool first = tile == 0 || u == lo;
                     t.flags = (first ? 1u : 0u) | (u + 1 == end ? 2u : 0u) | ((uint32_t)si << 2);
@@ -448,7 +411,6 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
             }
             ++n_seg;
         }
-        if (lane == 0) splits[blockIdx.x] = split;
         // Whatever the other warps do (one may still give up a wait once this one has no more to copy), the
         // copies in flight land before the CTA ends.
         for (int j = max(0, k - A.stages); copies && j < k; ++j)
@@ -518,25 +480,75 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         }
         __syncwarp();
     } else if (warp == kOWarp + 1) {
-        // ---- queries, of all segments but the first ----------------------------------------
-        // Segment n + 2 takes n's buffer once the last S of n is complete.  The rows' factors have four: that S
-        // waited for softmax warps to have read S, and the factors with it, two tiles before.
-        uint32_t done = 0;
-        for (uint32_t n = 0; done < count; ++n) {
-            const int si = n % kP8Ring;
-            // a wait that gave up: the segment may not be there
-            if (!p8_wait<Cfg::kSplit || F32>(b_seg + 8 * si, phase(n, kP8Ring), &s_ctl)) break;
-            const P8Seg g = s_seg[si];
-            done += g.tiles;
+        // ---- segments, and the queries of all but the first --------------------------------
+        // Segment n + 1 is announced before the queries of n are fetched, so that copies and queries run ahead of one
+        // another.  Segment n + 2 takes n's buffer once the last S of n is complete.  The rows' factors have four: that S
+        // waited for softmax warps to have read S, and the factors with it, two tiles before.  (Descriptors have sixteen, and the slowest
+        // reader is a few segments behind.)
+        int r = 0;
+        {
+            int a = 0, b = A.R;
+            while (b - a > 1) {
+                const int mid = (a + b) >> 1;
+                if (s_pre[mid] <= lo) a = mid; else b = mid;
+            }
+            r = a;
+        }
+        PaReq x = pa_req(A, r);
+        int head_tiles = pa_head_tiles<RP>(A, x), u = lo, there = 0;
+        P8Split split = {};
+        for (int n = 0; n < there || u < hi; ++n) {
+            // (twice for the first)
+            while (u < hi && there < n + 2) {
+                while (s_pre[r + 1] <= u) {
+                    ++r;
+                    if (s_pre[r + 1] > u) {
+                        x = pa_req(A, r);
+                        head_tiles = pa_head_tiles<RP>(A, x);
+                    }
+                }
+                const int h = (u - s_pre[r]) / head_tiles;
+                int s0 = s_pre[r] + h * head_tiles, rt = 0, nt = pa_row_tiles<RP>(A, x, 0);
+                while (s0 + nt <= u) {
+                    s0 += nt;
+                    nt = pa_row_tiles<RP>(A, x, ++rt);
+                }
+                const int end = min(hi, s0 + nt), si = there % kP8Ring;
+                if (lane == 0) {
+                    P8Seg g;
+                    g.token0 = x.q0;
+                    g.head0 = h * A.G;
+                    g.row0 = rt * RP;
+                    g.rows = min(RP, x.rows - rt * RP);
+                    g.base = x.base;
+                    g.len = x.len;
+                    g.slot = u == s0 && end == s0 + nt ? -1 : 2 * (int)blockIdx.x + (u == s0 ? 1 : 0);
+                    g.tok = g.row0 / A.G;
+                    g.off = g.row0 - g.tok * A.G;
+                    g.tiles = end - u;
+                    g.req = r;
+                    g.head = h;
+                    g.tile0 = u - s0;
+                    s_seg[si] = g;
+                    pa_arrive(b_seg + 8 * si);
+                    if (u == s0 && end < s0 + nt) split = {g.token0, g.head0, g.row0, g.rows, pa_cta_of(n_tiles, gridDim.x, s0 + nt - 1), {}};
+                }
+                __syncwarp();
+                u = end;
+                ++there;
+            }
             if (n == 0) continue;
-            if (n >= 2) p8_wait<Cfg::kSplit || F32>(b_qfree + 8 * (n & 1), phase(n - 2, 2), &s_ctl);
+            // a wait that gave up: what is in the buffer may still be read
+            if (n >= 2 && !p8_wait<Cfg::kSplit || F32>(b_qfree + 8 * (n & 1), phase(n - 2, 2), &s_ctl)) break;
+            const P8Seg g = s_seg[n % kP8Ring];
             uint8_t *const q = s_q + (n & 1) * Cfg::kQ;
-            constexpr int kDeep = RP / 2 < 8 ? RP / 2 : 4;
+            constexpr int kDeep = RP == 24 ? 6 : RP == 128 ? 4 : RP / 2 < 8 ? RP / 2 : 8;  // pairs of rows in flight, by registers
             for (int i = 0; i < RP / 2; i += kDeep) p8_queries<RP, kDeep, Cfg::kTurned>(A, g, 2 * i, 2, q, s_qs[n & 3], lane);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) pa_arrive(b_q + 8 * (n & 1));
         }
+        if (lane == 0) splits[blockIdx.x] = split;
     } else if (warp < 4) {
         if (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsV));
         // ---- V: lane = dimension, columns of two positions ---------------------------------

@@ -24,6 +24,7 @@ struct PaArgs {
     int64_t n_pages;
     int T, R, max_new, width, page, Hq, Hkv, G, stages;
     uint32_t upp_magic;  // ceil(2^32 / units of a page)
+    uint32_t g_magic;    // x / G = x g_magic / 2^32 for x < 2^13, G > 1
     float c;          // scale * log2(e), over what K is scaled by
 };
 
@@ -263,6 +264,7 @@ inline int pa_arguments(PaArgs *args, int *rp, const uint16_t *q, int T, const i
     A.Hq = Hq;
     A.Hkv = Hkv;
     A.G = G;
+    A.g_magic = (uint32_t)(((1ull << 32) + G - 1) / G);
     A.c = scale * 1.4426950408889634f;
     *args = A;
     *rp = rows_tile;
