@@ -26,15 +26,17 @@
 // of S, and their V codes are replaced by 0, whatever their bytes.
 //
 // What bounds it (8 kv heads, 40 query heads, times in a graph, of a measured copy rate of 6686 GB/s).  For windows,
-// memory: 539 MB at 262K take 93 us (0.86; 6.4 TB/s once going), 64 ragged requests of up to 16K 220 us (0.86), 200 short ones with
-// fp32 outputs 90 to 93 us (0.75).  Some 10 us do not depend on the length: a launch, the first tile's way through copy, products and
-// softmax, and the join; one token behind 1500 positions takes 9.0 us, 32K positions 20.6.  Issue stands at 60 % there.
-// For chunks of 512 tokens (128-row tiles), 143 GFLOP in 281 us, 0.26 of the product rate: some 4200 cycles a tile of
-// 128 x 128, in which four groups of softmax warps take turns with nothing but one another: issue 50 %, tensor pipe a fourth.
-// Copies with most of the exponentials, P's stores, V's conversion or either product left out took as long: no one of them is the
-// bound.  Tried and slower or no faster there: groups with barriers of their own (304 -> 335), scalar softmax (346), row tiles of 96 (378),
-// 64 rows to a lane (297 to 320), the queries' parts as two products into the same columns, the second in e5m2 (300), two buffers for
-// P beside two stages in place of three (296; prompts of 2048 391 -> 406), loads of S by fours, other register splits.
+// memory: 539 MB at 262K take 93.5 us (0.86; 6.4 TB/s once going), 64 ragged requests of up to 16K 215 us (0.89), 200 short ones with
+// fp32 outputs 85 us (0.80).  Some 10 us do not depend on the length: a launch, the first tile's way through copy, products and
+// softmax, and the join; one token behind 1500 positions takes 9.0 us, 32K positions 21.  Issue stands at 60 % there.  Where a
+// request has few tiles, the borders between segments: 64 requests of 512 positions take 29 us for 43 MB.
+// For chunks of 512 tokens (128-row tiles), 143 GFLOP in 232 us, 0.32 of the product rate: some 3400 cycles a tile of
+// 128 x 128, in which four groups of softmax warps take turns with nothing but one another.
+// Tried and slower or no faster there: groups with barriers of their
+// own (304 -> 335), scalar softmax (304 -> 346), row tiles of 96 (378), 64 rows to a lane (297 to 320), the queries' parts as two products
+// into the same columns, the second in e5m2 (300), two buffers for P beside two stages in place of three (296 of 296; prompts of 2048
+// 391 -> 406), loads of S by fours, other register splits.  One warp that heard of a segment when its copies began took long
+// enough over its queries to hold all others up (281 -> 232): the segments are announced ahead.
 #include "paged8.cuh"
 #include "paged_attention.cuh"
 
@@ -195,6 +197,10 @@ struct P8Cfg {
     static constexpr uint32_t kColV = 0, kColK = 64 * VB, kColS = kColK + 64 * KB, kColO = kColS + SB * NS;
     static_assert(kColO + NO <= kCols && NS % 16 == 0 && NO % 16 == 0, "tensor memory");
     static constexpr int PB = F32 || RP == 128 ? 1 : 2;  // P buffers
+    // Queries of all segments but the first: for windows by the V warps, where a segment begins (one warp took 7 to 17 thousand
+    // cycles for 24 rows, as long as four tiles: 64 requests of 512 positions 37 -> 29 us); long row tiles have more tiles to a
+    // segment, and V warps of few registers; fp32 outputs lose by the larger V loop (200 short requests 84 -> 94).
+    static constexpr bool kVQueries = RP <= 32 && !F32;
     static constexpr int kQ = 2 * RP * 128, kP = NO * 256;
     static constexpr size_t smem(int stages, int R) {
         return 1024 + (size_t)stages * (kP8StageK + kP8StageV) + 2 * kQ + PB * kP + ((size_t)R + 1) * 4;
@@ -253,7 +259,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
             mbar_init(b_s + 8 * i, 1);
             mbar_init(b_pv + 8 * i, 1);
             mbar_init(b_vfree + 8 * i, 1);
-            mbar_init(b_q + 8 * i, 1);
+            mbar_init(b_q + 8 * i, Cfg::kVQueries ? 5 : 1);
             mbar_init(b_qfree + 8 * i, 1);
             mbar_init(b_k + 8 * i, 4);
             mbar_init(b_kfree + 8 * i, 1);
@@ -540,12 +546,16 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
             if (n == 0) continue;
             // a wait that gave up: what is in the buffer may still be read
             if (n >= 2 && !p8_wait<Cfg::kSplit || F32>(b_qfree + 8 * (n & 1), phase(n - 2, 2), &s_ctl)) break;
-            const P8Seg g = s_seg[n % kP8Ring];
-            uint8_t *const q = s_q + (n & 1) * Cfg::kQ;
-            constexpr int kDeep = RP == 24 ? 6 : RP == 128 ? 4 : RP / 2 < 8 ? RP / 2 : 8;  // pairs of rows in flight, by registers
-            for (int i = 0; i < RP / 2; i += kDeep) p8_queries<RP, kDeep, Cfg::kTurned>(A, g, 2 * i, 2, q, s_qs[n & 3], lane);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
+            if (!Cfg::kVQueries) {
+                const P8Seg g = s_seg[n % kP8Ring];
+                uint8_t *const q = s_q + (n & 1) * Cfg::kQ;
+                constexpr int kDeep = RP == 24 ? 6 : RP == 128 ? 4 : RP / 2 < 8 ? RP / 2 : 8;  // pairs of rows in flight, by registers
+                for (int i = 0; i < RP / 2; i += kDeep) p8_queries<RP, kDeep, Cfg::kTurned>(A, g, 2 * i, 2, q, s_qs[n & 3], lane);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            }
+            // (also where the V warps fetch them: no S of segment n before this warp has seen that of n - 2 complete, or the
+            // wait above could miss it)
             if (lane == 0) pa_arrive(b_q + 8 * (n & 1));
         }
         if (lane == 0) splits[blockIdx.x] = split;
@@ -554,10 +564,10 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
         // ---- V: lane = dimension, columns of two positions ---------------------------------
         const uint8_t *const vrow = s_v + tid * 16;
         int st = 0;
-        uint32_t st_phase = 0;
+        uint32_t st_phase = 0, n_next = 1;
         for (uint32_t t = 0; t < count; ++t) {
             p8_wait<Cfg::kSplit || F32>(b_full + 8 * st, st_phase, &s_ctl);
-            const uint32_t mask = s_info[t % kP8Ring].mask;
+            const uint32_t mask = s_info[t % kP8Ring].mask, flags = s_info[t % kP8Ring].flags;
             const int n_pos = s_info[t % kP8Ring].n_pos;
             const bool whole = mask == 0xFFu && n_pos >= kPaTile;
             if (Cfg::kTurned) {  // K: lane = position, columns of two dimensions (what is no position is cut out of S)
@@ -608,6 +618,20 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
             if (lane == 0) {
                 pa_arrive(b_empty + 8 * st);
                 pa_arrive(b_o + 8 * (t & 1));
+            }
+            if (Cfg::kVQueries && (flags & 1u)) {  // segment n_next - 1 begins: the queries of the next one
+                if (t + s_seg[flags >> 2].tiles < count) {
+                    const uint32_t b = n_next & 1;
+                    if (p8_wait<Cfg::kSplit || F32>(b_seg + 8 * (n_next % kP8Ring), phase(n_next, kP8Ring), &s_ctl) &&
+                        (n_next < 2 || p8_wait<Cfg::kSplit || F32>(b_qfree + 8 * b, phase(n_next - 2, 2), &s_ctl))) {
+                        const P8Seg g = s_seg[n_next % kP8Ring];
+                        p8_queries<RP, RP / 8, Cfg::kTurned>(A, g, 2 * warp, 8, s_q + b * Cfg::kQ, s_qs[n_next & 3], lane);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) pa_arrive(b_q + 8 * b);
+                }
+                ++n_next;
             }
             if (++st == A.stages) {
                 st = 0;
@@ -1057,9 +1081,10 @@ static int p8_launch(PaArgs A, P8Split *splits, int sms, cudaStream_t stream) {
     if (Cfg::kSplit && regs.load(std::memory_order_relaxed) < Cfg::kRegs) return SVD_ERR_UNSUPPORTED;
     SVD_CUDA_TRY(launch(paged8_attention_kernel<RP, F32>, dim3(grid), dim3(Cfg::kThreads), smem, stream, true, A, splits));
     // No more row tiles are split than there are, nor more than there are borders between CTAs.  Few row tiles are split over
-    // many CTAs each, and then eight warps join a row.
+    // at least eight CTAs each, and then eight warps join a row (five parts to a tile, 8 requests of 4096 positions: 26 us with
+    // eight warps, 20 with one; twelve, one token behind 1500: 9.1 and 9.7).
     const int n = (int)(row_tiles < grid ? row_tiles : grid);
-    if (row_tiles * 4 <= grid)
+    if (row_tiles * 8 <= grid)
         SVD_CUDA_TRY(launch(paged8_join_kernel<RP, F32, 8>, dim3(n, RP), dim3(256), 0, stream, true, A, (const P8Split *)splits, grid));
     else
         SVD_CUDA_TRY(launch(paged8_join_kernel<RP, F32, 1>, dim3(n, (RP + 7) / 8), dim3(256), 0, stream, true, A, (const P8Split *)splits, grid));

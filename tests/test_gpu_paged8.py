@@ -507,6 +507,18 @@ def test_a_query_that_is_not_a_number_stays_in_its_row():
         c.check(out_dtype, got, ref)
 
 
+@BOTH
+@pytest.mark.parametrize("Hq,most", [(8, 1), (32, 4), (24, 7), (72, 7)])
+def test_many_short_segments(out_dtype, Hq, most):
+    """700 requests of one or two tiles and eight heads: some twenty segments to a CTA, more than there are descriptors of
+    them in flight, in row tiles of 8, 16, 24 and 64 (fp32: 32) rows; some requests without positions or tokens."""
+    g = np.random.default_rng(Hq)
+    new = g.integers(0, most + 1, 700)
+    lens = np.where(g.random(700) < 0.05, new, new + g.integers(0, 200, 700))
+    c = Case(lens.tolist(), new.tolist(), Hq, 8, 256, seed=Hq)
+    c.check(out_dtype, c.run(out_dtype), c.reference())
+
+
 @pytest.mark.parametrize("new", [12, 40, 129])
 @pytest.mark.parametrize("content", ["magnitudes", "small", "not finite", "rising", "scales", "spread", "missing pages"])
 def test_contents_in_long_row_tiles(content, new):
