@@ -15,7 +15,7 @@
 // dimension, two positions a column; four warps), exactly, and O^T += V^T P^T runs on fp16 operands: turning 128 x 128
 // codes of V costs as much as splitting P of 24 rows into the three e4m3 parts that fp16's eleven bits fill, and less for
 // more rows.  For 128 rows K goes the same way (a lane a position, two dimensions a column), against queries of one fp16
-// part under a power of two: half the columns of S to load, and room for all of it (chunks 296 -> 281 us; 64 rows lost by it, 132 -> 140).
+// part under a power of two: half the columns of S to load, and room for all of it (chunks 255 -> 233 us; 64 rows lose by it, 102 -> 119).
 //
 // Softmax.  A lane holds one position of S for all rows, as in the 4-bit kernel, and the reference of a row moves
 // only when a score exceeds it by 15 (p <= 2^15 in between).  What is weighed is t = s + log2 sv(j): P = 2^(t - ref) then
@@ -30,13 +30,14 @@
 // fp32 outputs 85 us (0.80).  Some 10 us do not depend on the length: a launch, the first tile's way through copy, products and
 // softmax, and the join; one token behind 1500 positions takes 9.0 us, 32K positions 21.  Issue stands at 60 % there.  Where a
 // request has few tiles, the borders between segments: 64 requests of 512 positions take 29 us for 43 MB.
-// For chunks of 512 tokens (128-row tiles), 143 GFLOP in 232 us, 0.32 of the product rate: some 3400 cycles a tile of
+// For chunks of 512 tokens (128-row tiles), 143 GFLOP in 235 us, 0.32 of the product rate: some 3400 cycles a tile of
 // 128 x 128, in which four groups of softmax warps take turns with nothing but one another.
 // Tried and slower or no faster there: groups with barriers of their
 // own (304 -> 335), scalar softmax (304 -> 346), row tiles of 96 (378), 64 rows to a lane (297 to 320), the queries' parts as two products
 // into the same columns, the second in e5m2 (300), two buffers for P beside two stages in place of three (296 of 296; prompts of 2048
-// 391 -> 406), loads of S by fours, other register splits.  One warp that heard of a segment when its copies began took long
-// enough over its queries to hold all others up (281 -> 232): the segments are announced ahead.
+// 391 -> 406), loads of S by fours.  Registers: 32 for V warps leave 64 to the one that walks the segments (40 and 56: 233 of 235, but
+// a prompt of 2048 tokens 344 of 331).  One warp that heard of a segment when its copies began took long
+// enough over its queries to hold all others up (281 -> 233): the segments are announced ahead.
 #include "paged8.cuh"
 #include "paged_attention.cuh"
 
@@ -208,7 +209,7 @@ struct P8Cfg {
     // Registers of a thread where softmax warps get some of the others' (24 warps of 80; see kSplit below).
     static constexpr int kRegs = RP == 128 ? 80 : 0;
     static constexpr bool kSplit = RP == 128;
-    static constexpr int kRegsV = 40, kRegsRest = 56, kRegsS = 96;
+    static constexpr int kRegsV = 32, kRegsRest = 64, kRegsS = 96;
     static_assert(!kSplit || 4 * kRegsV + 4 * kRegsRest + 4 * kGroups * kRegsS <= (8 + 4 * kGroups) * kRegs,
                   "a split may not ask for more than the launch has");
 };
@@ -574,7 +575,7 @@ paged8_attention_kernel(const __grid_constant__ PaArgs A, P8Split *__restrict__ 
                 if (t >= 2) p8_wait<Cfg::kSplit || F32>(b_kfree + 8 * (t & 1), phase(t - 2, 2), &s_ctl);
                 pa_fence_after();
                 const uint8_t *const krow = s_k + st * kP8StageK + tid * kPgDim;
-#pragma unroll 1
+#pragma unroll 2
                 for (int c = 0; c < 8; ++c) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(krow + ((c ^ (tid & 7)) << 4));
                     const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
