@@ -182,8 +182,9 @@ __device__ __forceinline__ void p8_queries(const PaArgs &A, const P8Seg &g, int 
     }
 }
 
-// Warps: four for V, four for each softmax group (two groups for up to 32 rows, four for more), one that copies, two that issue the MMAs of S
-// and of O, one that fetches and splits queries.  Two CTAs to an SM where registers and tensor memory allow.
+// Warps: four for V (and K, where it is turned, and the next segment's queries for windows), four for each softmax group (two groups for
+// up to 32 rows, four for more), one that copies, two that issue the MMAs of S and of O, one that walks the segments ahead of the copies
+// and splits their queries where the V warps do not.  Two CTAs to an SM where registers and tensor memory allow.
 template <int RP, bool F32>
 struct P8Cfg {
     static constexpr int N = RP < 16 ? 16 : (RP + 15) / 16 * 16;
