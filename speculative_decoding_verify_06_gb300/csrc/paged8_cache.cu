@@ -565,13 +565,13 @@ __global__ void __launch_bounds__(kA8Threads, 3) paged8_append_kernel(const __gr
         if (at >= 0 && at < (int64_t)A.width * A.page) pg = A.table[(int64_t)r * A.width + (uint32_t)at / (uint32_t)A.page];
         const T *const row = qkv + (int64_t)(A.Hq + h) * kPgDim;
         float4 *const slot = s_x + warp * (2 * kA8Pos * 32) + lane, *const v_slot = slot + kA8Pos * 32;
+        __syncthreads();  // (of the run before, the angles are read, and the codes of values in all four warps' slots)
         if (h < A.Hkv)
             for (int k = turn, p = 0; k < n; k += 4, ++p) {
                 const T *const from = row + (int64_t)(t + k) * A.ld;
                 a8_fetch(slot + 32 * p, from);
                 a8_fetch(v_slot + 32 * p, from + A.Hkv * kPgDim);
             }
-        __syncthreads();  // (the angles of the run before are read)
         const bool stored = pg >= 0 && pg < A.n_pages;
         const int place = (int)((uint32_t)at % (uint32_t)A.page) >> 4;
         uint8_t *const unit = A.pages + ((pg * A.Hkv + h) * (A.page >> 4) + place) * (int64_t)kP8UnitBytes;

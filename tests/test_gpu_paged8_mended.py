@@ -1,0 +1,51 @@
+"""The paged 8-bit calls and the moves of pages on the GPU in cases that once went wrong or that nothing ordered, against the
+fp64 reference: appends whose CTAs handle many runs one after the other."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged, paged8
+from speculative_decoding_verify_06_gb300 import svd
+from tests.gpu_helpers import DEV, lib, to_dev
+from tests.test_gpu_paged8 import as_type, layout, random_pool, same_zeros
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    lib()
+
+
+@pytest.mark.parametrize("dtype", [svd.SVD_F32, svd.SVD_BF16])
+@pytest.mark.parametrize("most,Hkv,rotate", [(1, 4, False), (4, 3, True), (9, 2, True)])
+def test_appends_of_many_runs_to_a_cta(dtype, most, Hkv, rotate):
+    """Some 5000 tokens in windows of 1 to `most`, begun at every place of a unit: up to sixteen runs follow one another in a CTA, and
+    each fills shared memory that all warps of a head read at the end of the run before.  Every byte, thirty times over."""
+    g = np.random.default_rng(most + Hkv)
+    R = min(4096, 10000 // (most + 1))
+    new = g.integers(1, most + 1, R)
+    lens = (new + g.integers(0, 40, R)).tolist()
+    table, q_start, n_pages = layout(lens, new.tolist(), 32, g)
+    pool = random_pool(g, n_pages, Hkv, 32, e_lo=-9, e_hi=-5)
+    T = int(q_start[-1])
+    x = g.normal(0, 1, (T, 2 * Hkv, 128)).astype(np.float32) * 2.0 ** g.integers(-3, 4, (T, 1, 1))
+    x = as_type(x, dtype).float().numpy()
+    pos = np.concatenate([np.arange(n - k, n) for n, k in zip(lens, new)])[None]
+    inv = 1e4 ** (-np.arange(64) / 64)
+    y = paged.rotate(x.astype(np.float64), pos, inv, [0] * 64, False) if rotate else x.astype(np.float64)
+    want = pool.copy()
+    assert not paged8.append(want, y[:, :Hkv], x[:, Hkv:], lens, q_start, table, 32)
+    rows, start = as_type(x.reshape(T, -1), dtype).to(DEV), to_dev(pool.reshape(-1))
+    lens_d, q_d, tab, pos_d = to_dev(np.array(lens, np.int32)), to_dev(q_start), to_dev(table), to_dev(pos.astype(np.int32))
+    status = torch.zeros(T, dtype=torch.int32, device=DEV)
+    first = None
+    for _ in range(30):
+        p = start.clone()
+        svd.svd_paged8_append(rows, 2 * Hkv * 128, T, 0, Hkv, lens_d, q_d, R, tab, tab.shape[1], p, 32, n_pages, None,
+                              rope=svd.Rope(inv) if rotate else None, positions=pos_d, positions_ld=T, dtype=dtype, status=status)
+        if first is None:
+            first = p
+            assert np.array_equal(same_zeros(p.cpu().numpy().reshape(pool.shape)), same_zeros(want))
+        assert torch.equal(p, first)
+    assert not status.any()
