@@ -543,10 +543,11 @@ int svd_paged_attention(const uint16_t *q, int n_tokens, const int32_t *kv_len,
  *
  * svd_paged8_append: request r has the tokens q_start[r] .. q_start[r + 1] - 1, the last of them at position
  *   kv_len[r] - 1 of the request, which lies in page table[r][position / page_size].  Rows of qkv, rotation and q as for
- *   svd_paged_append, but a token from q_start[n_requests] on is left alone, its row of q too.  Per unit, kv head, and K and V
- *   apart: e = the smallest exponent (-64..7) with 448 * 2^e >= every magnitude that the call brings to the unit; where
- *   the unit has positions before the call's first one in it, at least the exponent it has, and if it grows, their codes are
- *   rounded again to code * scale / 2^e.  New codes are value / 2^e to nearest (ties to even); scale and codes are decided as in
+ *   svd_paged_append, but a token from q_start[n_requests] on is left alone, its row of q too (and one before q_start[0], where
+ *   that is not 0, as for one of several groups of requests, is stored for none).  Per unit, kv head, and K and V apart: e = the
+ *   smallest exponent (-64..7) with 448 * 2^e >= every magnitude that the call brings to the unit; where the unit has
+ *   positions before the call's first one in it, at least the exponent it has, and if it grows, their codes are rounded
+ *   again to code * scale / 2^e.  New codes are value / 2^e to nearest (ties to even); scale and codes are decided as in
  *   exact arithmetic.  NaN counts as 0 and magnitudes end at 57344; status (NULL, or int32 [n_tokens] that the call ORs
  *   into) has SVD_ST_NONFINITE, and SVD_ST_BAD_SLOT for a token whose position has no page in the pool: it is not
  *   stored.  Bytes of other positions stay.  A page belongs to one request.

@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kA8Threads, 3) paged8_append_kernel(const __gr
     __shared__ __align__(16) A8Tables s_tab;
     __shared__ __align__(16) A8Head s_head[2];
     __shared__ int s_r;
-    __shared__ int4 s_run;  // of the block's first token: where its request's tokens begin and end, and the request's length
+    __shared__ int4 s_run;  // of the block's first token that a request has: where the request's tokens begin and end, and its length
     float2 *const s_cs = reinterpret_cast<float2 *>(s_x + kA8Warps * 2 * kA8Pos * 32);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const T *const qkv = reinterpret_cast<const T *>(A.qkv) + 4 * lane;
@@ -535,9 +535,10 @@ __global__ void __launch_bounds__(kA8Threads, 3) paged8_append_kernel(const __gr
 
     // ---- keys and values: the runs that begin in this block of tokens, two kv heads ------------------
     const int h = 2 * (int)blockIdx.y + (warp >> 2), turn = warp & 3;
+    const int begin = max(t0, A.q_start[0]);  // (tokens before the first request's belong to none)
     for (int r = tid; r < A.R; r += kA8Threads) {
         const int a = A.q_start[r], b = A.q_start[r + 1];
-        if (a <= t0 && t0 < b) {
+        if (a <= begin && begin < b) {
             atomicMax(&s_r, r);
             s_run = make_int4(a, b, A.kv_len[r], 0);
         }
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(kA8Threads, 3) paged8_append_kernel(const __gr
     int r = s_r;
     if (r < 0) return;  // behind the last request
     int q0 = s_run.x, q2 = s_run.y, len = s_run.z;
-    for (int t = t0; t < t1;) {
+    for (int t = begin; t < t1;) {
         if (q2 <= t) {
             while (r + 1 < A.R && A.q_start[r + 1] <= t) ++r;
             q0 = A.q_start[r];

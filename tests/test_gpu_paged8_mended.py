@@ -1,5 +1,5 @@
 """The paged 8-bit calls and the moves of pages on the GPU in cases that once went wrong or that nothing ordered, against the
-fp64 reference: appends whose CTAs handle many runs one after the other."""
+fp64 reference: appends whose CTAs handle many runs one after the other; requests whose tokens do not begin at row 0."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +7,7 @@ import torch
 from oracle import paged, paged8
 from speculative_decoding_verify_06_gb300 import svd
 from tests.gpu_helpers import DEV, lib, to_dev
-from tests.test_gpu_paged8 import as_type, layout, random_pool, same_zeros
+from tests.test_gpu_paged8 import BOTH, Case, as_type, check_q, gpu_append, layout, random_pool, same_zeros
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,37 @@ def test_appends_of_many_runs_to_a_cta(dtype, most, Hkv, rotate):
             assert np.array_equal(same_zeros(p.cpu().numpy().reshape(pool.shape)), same_zeros(want))
         assert torch.equal(p, first)
     assert not status.any()
+
+
+@pytest.mark.parametrize("dtype", [svd.SVD_F32, svd.SVD_BF16])
+@pytest.mark.parametrize("first", [1, 5, 15, 16, 37, 2000])
+def test_append_for_the_second_of_two_groups(dtype, first):
+    """q_start[0] = first: the rows before are another group's.  Whatever block of tokens the first request begins in, all of it is stored."""
+    g = np.random.default_rng(first)
+    new = [0, 3, 0, 40, 1, 16, 500]
+    lens = [9, 3, 0, 77, 17, 16, 501]
+    table, q_start, n_pages = layout(lens, new, 32, g)
+    pool = random_pool(g, n_pages, 3, 32)
+    q_start = (q_start + first).astype(np.int32)
+    T = int(q_start[-1])
+    x = as_type(g.normal(0, 1, (T, 8, 128)).astype(np.float32), dtype).float().numpy()
+    pos = g.integers(0, 3000, (1, T))
+    inv = 1e4 ** (-np.arange(64) / 64)
+    q, got, st = gpu_append(x, dtype, 2, 3, lens, q_start, table, pool, 32, rope=svd.Rope(inv), positions=pos)
+    y = paged.rotate(x.astype(np.float64), pos, inv, [0] * 64, False)
+    want = pool.copy()
+    assert not paged8.append(want, y[first:, 2:5], x[first:, 5:], lens, q_start - first, table, 32)
+    assert np.array_equal(same_zeros(got), same_zeros(want)) and not st.any()
+    check_q(q[first:], y[first:, :2])
+
+
+@BOTH
+@pytest.mark.parametrize("first", [3, 130])
+def test_attention_for_the_second_of_two_groups(out_dtype, first):
+    c = Case([70, 200, 15], [4, 1, 9], 6, 2, 32, seed=first)
+    o, a, e, _ = c.reference()
+    rows = np.full((first, 6, 128), np.nan)
+    c.q = torch.cat([torch.ones(first, 6, 128, dtype=torch.bfloat16), c.q])
+    c.q_start = (c.q_start + first).astype(np.int32)
+    c.T += first
+    c.check(out_dtype, c.run(out_dtype), (np.concatenate([rows, o]), np.concatenate([rows, a]), np.concatenate([rows[..., 0], e])))
