@@ -34,6 +34,9 @@ __host__ __device__ __forceinline__ int pg_v_byte(int i) {
     return (i & 12) | ((i & 1) << 1) | ((i >> 1) & 1);
 }
 
+// Dynamic shared memory that needs no asking: of the 48 KB, a kernel's static part counts too.
+constexpr size_t kPlainSmem = 40 * 1024;
+
 // Lets a kernel have `bytes` of dynamic shared memory: asked once for each kernel and device (the
 // call costs as much as a tenth of a launch).
 template <auto *kernel>

@@ -169,7 +169,7 @@ int paged_fork(const int32_t *held, const int32_t *window, const int32_t *emitte
     const FkArgs A = {held, window, emitted, parent, table, free_ids, n_free, held_out, window_out, table_out, free_out,
                       n_free_out, copy_from, copy_to, n_copies, status, R, page, width, (int)n_pages};
     const size_t smem = (size_t)R * 25 + 8;
-    if (smem > 48 * 1024) SVD_CUDA_TRY(allow_smem<paged_fork_kernel>((size_t)SVD_PAGED_MAX_REQUESTS * 25 + 8));
+    if (smem > kPlainSmem) SVD_CUDA_TRY(allow_smem<paged_fork_kernel>((size_t)SVD_PAGED_MAX_REQUESTS * 25 + 8));
     const int64_t work = (int64_t)R * mv_items(width) + 2 * mv_items(n_pages);
     const int grid = (int)(work < 2 * sms ? work : 2 * sms);
     SVD_CUDA_TRY(launch(paged_fork_kernel, dim3(grid), dim3(kTbThreads), smem, stream, true, A));
@@ -296,7 +296,7 @@ int paged_compact(const int32_t *held, int R, int page, const int32_t *table, in
     const CpArgs A = {held, table, table_out, free_out, n_free_out, copy_from, copy_to, n_copies, R, page, width,
                       (int)n_pages};
     const size_t smem = ((size_t)n_pages + 31) / 32 * 4;
-    if (smem > 40 * 1024) SVD_CUDA_TRY(allow_smem<paged_compact_kernel>((size_t)SVD_PAGED_COMPACT_MAX_PAGES / 8));
+    if (smem > kPlainSmem) SVD_CUDA_TRY(allow_smem<paged_compact_kernel>((size_t)SVD_PAGED_COMPACT_MAX_PAGES / 8));
     const int64_t work = (int64_t)R * mv_items(width) + 2 * mv_items(n_pages);
     const int grid = (int)(work < sms ? work : sms);
     SVD_CUDA_TRY(launch(paged_compact_kernel, dim3(grid), dim3(kTbThreads), smem, stream, true, A));

@@ -1,5 +1,10 @@
 """The paged 8-bit calls and the moves of pages on the GPU in cases that once went wrong or that nothing ordered, against the
-fp64 reference: appends whose CTAs handle many runs one after the other; requests whose tokens do not begin at row 0."""
+fp64 reference: appends whose CTAs handle many runs one after the other; requests whose tokens do not begin at row 0;
+numbers of requests whose sums just fill the shared memory that a launch gets unasked."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +13,7 @@ from oracle import paged, paged8
 from speculative_decoding_verify_06_gb300 import svd
 from tests.gpu_helpers import DEV, lib, to_dev
 from tests.test_gpu_paged8 import BOTH, Case, as_type, check_q, gpu_append, layout, random_pool, same_zeros
+from tests.test_gpu_paged_moves import gpu_fork, same, state
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +89,19 @@ def test_attention_for_the_second_of_two_groups(out_dtype, first):
     c.q_start = (c.q_start + first).astype(np.int32)
     c.T += first
     c.check(out_dtype, c.run(out_dtype), (np.concatenate([rows, o]), np.concatenate([rows, a]), np.concatenate([rows[..., 0], e])))
+
+
+def fork_once(R):
+    g = np.random.default_rng(R)
+    held, table, free = state(g, R, 16, 3, 500)
+    window = np.minimum(held, g.integers(0, 9, R))
+    parent = np.where(g.random(R) < 0.3, g.integers(0, R, R), -1)
+    args = (held, window, g.integers(0, window + 1), parent, 16, table, free, 500)
+    same(gpu_fork(*args), paged8.fork(*args))
+
+
+@pytest.mark.parametrize("R", [1638, 1639, 1960, 1961, 1963, 1965, 1966])
+def test_a_first_fork_of_any_number_of_requests(R):
+    """In a process of its own: a call that asked for more shared memory before would let this one have it."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", f"import tests.test_gpu_paged8_mended as t; t.lib(); t.fork_once({R})"], cwd=root, check=True, timeout=300)
