@@ -199,7 +199,7 @@ static int tb_launch(TbArgs A, int64_t n_pages, int64_t tokens, cudaStream_t str
     A.n_pages = (int)n_pages;
     A.tokens = (int)tokens;
     const size_t smem = (size_t)A.R * 25 + 8;
-    if (smem > 48 * 1024)
+    if (smem > kPlainSmem)
         SVD_CUDA_TRY(allow_smem<paged_tables_kernel>((size_t)SVD_PAGED_MAX_REQUESTS * 25 + 8));
     auto items = [](int64_t n) { return (n + kTbChunk - 1) / kTbChunk; };
     const int64_t work = (int64_t)A.R * items(A.width) + items(n_pages) + items(tokens);

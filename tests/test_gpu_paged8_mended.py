@@ -12,6 +12,7 @@ import torch
 from oracle import paged, paged8
 from speculative_decoding_verify_06_gb300 import svd
 from tests.gpu_helpers import DEV, lib, to_dev
+from tests.test_gpu_paged import gpu_tables, same_tables
 from tests.test_gpu_paged8 import BOTH, Case, as_type, check_q, gpu_append, layout, random_pool, same_zeros
 from tests.test_gpu_paged_moves import gpu_fork, same, state
 
@@ -105,3 +106,18 @@ def test_a_first_fork_of_any_number_of_requests(R):
     """In a process of its own: a call that asked for more shared memory before would let this one have it."""
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run([sys.executable, "-c", f"import tests.test_gpu_paged8_mended as t; t.lib(); t.fork_once({R})"], cwd=root, check=True, timeout=300)
+
+
+def tables_once(R):
+    g = np.random.default_rng(R)
+    held, table, free = state(g, R, 16, 3, 500)
+    window = np.minimum(held, g.integers(0, 9, R))
+    emitted, new = g.integers(0, window + 1), g.integers(0, 5, R)
+    args = (held, window, emitted, new, 16, table, free, 500, 3 * R)
+    same_tables(gpu_tables(*args), paged.tables(*args))
+
+
+@pytest.mark.parametrize("R", [1638, 1639, 1960, 1961, 1963, 1965, 1966])
+def test_first_tables_of_any_number_of_requests(R):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", f"import tests.test_gpu_paged8_mended as t; t.lib(); t.tables_once({R})"], cwd=root, check=True, timeout=300)
