@@ -555,8 +555,8 @@ int svd_paged_attention(const uint16_t *q, int n_tokens, const int32_t *kv_len,
  *   for a slot outside the pool).
  * svd_paged8_attention: as svd_paged_attention, tokens, masks, outputs, workspace and errors alike.  A query row is used
  *   as a power of two times the sum of two e4m3 parts (or one fp16 part, no worse): exact for bf16 down to 2^-14 of the row's largest, and to 2^-22 of
- *   it below; there is no bound on its magnitude.  A row with a query that is not finite is NaN.  The softmax's weights are
- *   used as fp16 (as two fp16 parts for fp32 outputs), and the sums are fp32.  Codes of positions before kv_len must be
+ *   it below; there is no bound on its magnitude but that of its scores, which are fp32: where |scale * log2(e) * <q, k_j>| reaches 2^128,
+ *   the row is undefined.  A row with a query that is not finite is NaN.  The softmax's weights are used as fp16 (as two fp16 parts for fp32 outputs), and the sums are fp32.  Codes of positions before kv_len must be
  *   finite (svd_paged8_append writes no others); bytes of later ones may be anything, but for the scales of the units that hold
  *   positions.  The workspace's first word gets bit 0 only.
  *

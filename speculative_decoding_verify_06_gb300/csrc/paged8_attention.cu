@@ -147,7 +147,7 @@ __device__ __forceinline__ void p8_queries(const PaArgs &A, const P8Seg &g, int 
 #pragma unroll
         for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
         const bool finite = top < 0x7F80u;
-        const int e = max(p8_need(__uint_as_float(top << 16)), -118);
+        const int e = max(p8_need(__uint_as_float(top << 16)), A.q_down - 126);
         const float inv = finite ? p8_pow2(-e) : 0.f;
         uint32_t hi4[2], lo4[2], half4[4];
 #pragma unroll
@@ -178,7 +178,7 @@ __device__ __forceinline__ void p8_queries(const PaArgs &A, const P8Seg &g, int 
             *reinterpret_cast<uint2 *>(to) = make_uint2(hi4[0], hi4[1]);
             *reinterpret_cast<uint2 *>(to + RP * 128) = make_uint2(lo4[0], lo4[1]);
         }
-        if (ch == 0) qs[row] = finite ? p8_pow2(e) : __int_as_float(0x7FC00000);
+        if (ch == 0) qs[row] = finite ? p8_pow2(e - A.q_down) : __int_as_float(0x7FC00000);
     }
 }
 
@@ -1115,6 +1115,11 @@ int paged8_attention(const uint16_t *q, int T, const int32_t *kv_len, const int3
     const size_t at = p8_splits_at(Hq, Hkv, R, max_new, sms);
     if (ws_bytes < at + (size_t)2 * sms * sizeof(P8Split)) return SVD_ERR_WORKSPACE;
     if (T == 0) return SVD_OK;
+    // A sum of codes reaches 448^2 * 128 < 2^25 and a row's power of two 2^120: over 2^20, their product stays in fp32's range
+    // whatever the scales of keys, so that a row is lost only where its scores leave that range.  (Scales from 2^64 on would take c
+    // out of it in turn; there, a score leaves the range before that product does.)
+    A.q_down = scale < 0x1p64f ? 20 : 0;
+    A.c *= A.q_down ? 0x1p20f : 1.f;
     P8Split *const splits = (P8Split *)((uint8_t *)ws + at);
 #define SVD_P8(RP) (out_dtype == SVD_F32 ? p8_launch<RP, true>(A, splits, sms, stream) : p8_launch<RP, false>(A, splits, sms, stream))
     switch (rp) {

@@ -26,6 +26,7 @@ struct PaArgs {
     uint32_t upp_magic;  // ceil(2^32 / units of a page)
     uint32_t g_magic;    // x / G = x g_magic / 2^32 for x < 2^13, G > 1
     float c;          // scale * log2(e), over what K is scaled by
+    int q_down;       // 8 bits: rows of queries are held over 2^q_down, which c makes up for
 };
 
 // ---- geometry shared by the two kernels -----------------------------------------------------

@@ -1,6 +1,6 @@
 """The paged 8-bit calls and the moves of pages on the GPU in cases that once went wrong or that nothing ordered, against the
 fp64 reference: appends whose CTAs handle many runs one after the other; requests whose tokens do not begin at row 0;
-numbers of requests whose sums just fill the shared memory that a launch gets unasked."""
+numbers of requests whose sums just fill the shared memory that a launch gets unasked; queries near the largest that bf16 holds, and scales of scores far from 1."""
 import os
 import subprocess
 import sys
@@ -121,3 +121,18 @@ def tables_once(R):
 def test_first_tables_of_any_number_of_requests(R):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run([sys.executable, "-c", f"import tests.test_gpu_paged8_mended as t; t.lib(); t.tables_once({R})"], cwd=root, check=True, timeout=300)
+
+
+@pytest.mark.parametrize("new,out_dtype", [(1, svd.SVD_BF16), (1, svd.SVD_F32), (4, svd.SVD_BF16), (4, svd.SVD_F32), (12, svd.SVD_BF16),
+                                           (60, svd.SVD_BF16)])
+@pytest.mark.parametrize("q_exp,k_exp,scale_exp", [(120, -64, -64), (125, -64, -64), (126, -64, 0), (116, -30, -90), (100, 7, -110), (116, 7, -122),
+                                                   (-40, -20, 63), (-44, -20, 64), (-100, -3, 100), (-60, -64, 124)])
+def test_queries_and_scales_of_any_size(new, out_dtype, q_exp, k_exp, scale_exp):
+    """Rows as large as bf16 holds against keys as small as the cache holds, and the other way round: scores that are no larger than
+    usual, or finite at least, give what the formula says."""
+    c = Case([300, 150], [new, min(new, 3)], 5, 1, 64, seed=new, k_exp=(k_exp, k_exp + 1))
+    c.q = (c.q.double().clamp(-2.5, 2.5) * 2.0 ** q_exp).to(torch.bfloat16)
+    c.q[0, 0] = torch.finfo(torch.bfloat16).max if q_exp > 110 else c.q[0, 0]
+    assert torch.isfinite(c.q).all()
+    c.scale = 128 ** -0.5 * 2.0 ** scale_exp
+    c.check(out_dtype, c.run(out_dtype), c.reference())
