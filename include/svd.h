@@ -551,6 +551,9 @@ int svd_paged_attention(const uint16_t *q, int n_tokens, const int32_t *kv_len,
  *   exact arithmetic.  NaN counts as 0 and magnitudes end at 57344; status (NULL, or int32 [n_tokens] that the call ORs
  *   into) has SVD_ST_NONFINITE, and SVD_ST_BAD_SLOT for a token whose position has no page in the pool: it is not
  *   stored.  Bytes of other positions stay.  A page belongs to one request.
+ *   A unit's scale does not shrink while positions before the call's first one stay in it, also where the tokens that asked for
+ *   it were drafts and are gone: what the cache holds then depends on the windows in which it was written.  A larger
+ *   scale s costs a value at most 2^-10 s (codes are rounded again among e4m3's subnormals only).
  * svd_paged8_read: the values that the pool holds at slots[t] (page * page_size + offset), fp32 [T][Hkv][128] each (0
  *   for a slot outside the pool).
  * svd_paged8_attention: as svd_paged_attention, tokens, masks, outputs, workspace and errors alike.  A query row is used

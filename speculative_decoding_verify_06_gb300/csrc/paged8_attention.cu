@@ -29,12 +29,15 @@
 // memory: 539 MB at 262K take 93.5 us (0.86; 6.4 TB/s once going), 64 ragged requests of up to 16K 215 us (0.89), 200 short ones with
 // fp32 outputs 85 us (0.80).  Some 10 us do not depend on the length: a launch, the first tile's way through copy, products and
 // softmax, and the join; one token behind 1500 positions takes 9.0 us, 32K positions 21.  Issue stands at 60 % there.  Where a
-// request has few tiles, the borders between segments: 64 requests of 512 positions take 29 us for 43 MB.
+// request has few tiles, the borders between segments: 64 requests of up to 512 positions take 29 us for 43 MB.
 // For chunks of 512 tokens (128-row tiles), 143 GFLOP in 235 us, 0.32 of the product rate: some 3400 cycles a tile of
-// 128 x 128, in which four groups of softmax warps take turns with nothing but one another.
+// 128 x 128, in which four groups of softmax warps take turns with nothing but one another.  A first prompt, with nothing
+// behind it, is furthest from what its products need: 2048 tokens take 334 us for 43 GFLOP (0.07 of the rate), eight of 300
+// tokens 127 us for 54 MB.  A segment has 8.5 tiles there, some 60 us of them in all, and one warp brings and splits the 128 query rows of
+// every segment but a CTA's first.  fp32 outputs, in tiles of 32 rows, take 548 us for the 2048 tokens.
 // Tried and slower or no faster there: groups with barriers of their
 // own (304 -> 335), scalar softmax (304 -> 346), row tiles of 96 (378), 64 rows to a lane (297 to 320), the queries' parts as two products
-// into the same columns, the second in e5m2 (300), two buffers for P beside two stages in place of three (296 of 296; prompts of 2048
+// into the same columns, the second in e5m2 (300), two buffers for P beside two stages in place of three (296 of 296; a prompt of 2048
 // 391 -> 406), loads of S by fours.  Registers: 32 for V warps leave 64 to the one that walks the segments (40 and 56: 233 of 235, but
 // a prompt of 2048 tokens 344 of 331).  One warp that heard of a segment when its copies began took long
 // enough over its queries to hold all others up (281 -> 233): the segments are announced ahead.
@@ -200,8 +203,10 @@ struct P8Cfg {
     static_assert(kColO + NO <= kCols && NS % 16 == 0 && NO % 16 == 0, "tensor memory");
     static constexpr int PB = F32 || RP == 128 ? 1 : 2;  // P buffers
     // Queries of all segments but the first: for windows by the V warps, where a segment begins (one warp took 7 to 17 thousand
-    // cycles for 24 rows, as long as four tiles: 64 requests of 512 positions 37 -> 29 us); long row tiles have more tiles to a
-    // segment, and V warps of few registers; fp32 outputs lose by the larger V loop (200 short requests 84 -> 94).
+    // cycles for 24 rows, as long as four tiles: 64 requests of up to 512 positions 37 -> 29 us); long row tiles have more tiles to a
+    // segment, and V warps of few registers; fp32 outputs in 8-row tiles lose by the larger V loop (200 short requests of one token 84 ->
+    // 94).  Not measured: fp32 outputs in tiles of 16 to 32 rows, where the one warp is as slow (64 requests of up to 512 positions, windows of 4: 41 us,
+    // and 29 for bf16), and 64 rows.
     static constexpr bool kVQueries = RP <= 32 && !F32;
     static constexpr int kQ = 2 * RP * 128, kP = NO * 256;
     static constexpr size_t smem(int stages, int R) {

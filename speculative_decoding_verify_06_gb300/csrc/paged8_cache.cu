@@ -22,9 +22,10 @@
 // bound still, in fp64.  The scale likewise.  Values and dimensions that do not turn are exact as they come.
 //
 // What bounds it (times in a graph).  4 tokens take 4.6 us, a launch and the chain of one unit: loads that follow from one
-// another, angles, rotation, the exchange, the codes.  64 windows of 4 tokens take 8.5 us: every CTA has such a chain, some two, and all are there
-// at once.  4099 tokens of 32 + 16 heads take 27.2 us for 92 MB, 0.51 of the copy rate: issue at
-// half, three CTAs to an SM (by registers), whose warps wait for copies, shared memory and each other.  On the way there, in us: a CTA
+// another, angles, rotation, the exchange, the codes.  64 windows of 4 tokens take 8.4 us: every CTA has such a chain, some two, and all are there
+// at once.  4099 tokens of 32 + 16 heads in bf16 take 27.5 us for 92 MB, 0.50 of the copy rate: issue at
+// half, three CTAs to an SM (by registers), whose warps wait for copies, shared memory and each other (in fp32 43 us
+// for 143 MB, 0.50 too).  On the way there, in us: a CTA
 // to a unit with all of it in registers 112, halves of a unit 109, one maximum's border cases kept apart from
 // the certain ones 60 (a maximum of 448 * 2^e itself, frequent in bf16, had gone the slow way), query heads one at a time 47,
 // inputs in shared memory 40, a bound for a lane and not an element 35, angle tables in shared memory 30,
@@ -647,8 +648,10 @@ int paged8_append(const void *qkv, int dtype, int64_t ld, int T, int Hq, int Hkv
 }
 
 // ---- read-back -----------------------------------------------------------------------------
-// One warp per slot and kv head; a lane's four dimensions of K and of V.  1.8 us for 4 tokens, 11.2 for 4099 (34 MB of fp32
-// written, which bound it: consecutive tokens of one head to a CTA, whose V lines L1 would then hold, take as long).
+// One warp per slot and kv head; a lane's four dimensions of K and of V.  1.8 us for 4 tokens, 11.2 for 4099 (42 MB, 34 of them fp32
+// written, which stay in L2).  Bounded by the latency of its loads, of which the slot comes first and then codes, scales and single
+// bytes of 128 rows of values (long scoreboard 23 an instruction issued, in the profiler; issue 39 %).  More of them in flight did not
+// help: two or four slots to a warp with consecutive tokens of one head to a CTA, whose lines of V L1 would then hold, took 12.1 and 12.2, one 11.2.
 __global__ void __launch_bounds__(256) paged8_read_kernel(const int64_t *__restrict__ slots, int T, int Hkv,
                                                           const uint8_t *__restrict__ pages, int page, int64_t n_slots,
                                                           float *__restrict__ k, float *__restrict__ v) {

@@ -27,7 +27,8 @@ from . import svd
 class PagedBatch:
     """The caches of `requests` requests in `layers` pools of n_pages pages, one table for all layers.
 
-    bits: of a key or value in the cache, 4 (a scale for 32 dimensions of a position) or 8 (one for 16 positions).
+    bits: of a key or value in the cache, 4 (a scale for 32 dimensions of a position) or 8 (one for 16 positions, which a rejected
+    draft among them may have raised: see svd_paged8_append).
 
     A request has up to max_window tokens in a step (lowered where windows stay shorter: the attention then
     takes smaller tiles), all requests together max_tokens.
